@@ -268,6 +268,97 @@ ZHA_API int zha_dense_decode_noalloc(const zha_config* cfg, const void* K, const
                              const void* Q, float* O, int32_t B, void* stream);
 
 /*
+ * zha_prefix_scratch_bytes / zha_prefix_decode: dense softmax attention of B
+ * sequences that share a long prefix, each with a cache of its own behind it,
+ * for m query tokens per sequence (m = 1: one decode step; m > 1: e.g. drafted
+ * tokens).  The shared tokens are read once for all B * m queries instead of
+ * once per sequence.
+ *   K, V     - [Hkv][ld][d] element type: the shared prefix, tokens [0, n).  n may
+ *              be 0 (K and V may then be NULL).
+ *   K_own, V_own - [B][Hkv][ld_own][d] element type: every sequence's own
+ *              tokens, the m query tokens' own rows last.  ld_own may be 0
+ *              (no own caches; K_own, V_own and own_len may then be NULL).
+ *   own_len  - [B] int32, device: own tokens of each sequence, read on the
+ *              device (a value outside [0, ld_own] is taken as the nearer end).
+ *              Rows past a sequence's length are never used, whatever they hold.
+ *   Q        - [B][m][Hq][d] element type;  O - [B][m][Hq][d] fp32.
+ *   lse      - optional [B][m][Hq] fp32: natural logarithm of the softmax
+ *              denominator (to join the result with attention over other keys).
+ * Query token i of sequence b sees the whole prefix and its own tokens
+ * [0, own_len[b] - m + i + 1).  A query that sees no key at all gets O = 0 and
+ * lse = -inf.  K and V must be finite where a query token of the call may see them.
+ *   scratch  - scratch_bytes bytes, 256-byte aligned, at least
+ *              zha_prefix_scratch_bytes(cfg, B, m, n, ld_own) (0 for an invalid
+ *              request), which covers every call with no more sequences, query tokens,
+ *              prefix tokens and own tokens; ZHA_ERR_CAPACITY when it is too small.
+ *              Its first 256 bytes hold a status word and must be zero before the first call (see
+ *              zha_scratch_status); the rest needs no initialisation.  Calls that
+ *              share a scratch must be issued in order on one stream; graphs
+ *              captured with one scratch must not replay at the same time.
+ * B * m * Hq < 2^24; B is not bound by cfg->max_batch.
+ * Asynchronous on `stream`; can be captured into a CUDA graph.
+ */
+ZHA_API size_t zha_prefix_scratch_bytes(const zha_config* cfg, int32_t B, int32_t m, int64_t n, int64_t ld_own);
+ZHA_API int zha_prefix_decode(const zha_config* cfg, const void* K, const void* V, int64_t ld, int64_t n,
+                      const void* K_own, const void* V_own, int64_t ld_own, const int32_t* own_len, const void* Q,
+                      float* O, float* lse, int32_t B, int32_t m, void* scratch, size_t scratch_bytes, void* stream);
+
+/*
+ * zha_weights_scratch_bytes / zha_dense_weights: dense softmax attention of m
+ * query tokens of one context over tokens [0, n) that also adds up how much
+ * attention every token receives, the sums zha_cache_evict goes by.
+ *   K, V     - [Hkv][ld][d] element type.  V and O NULL: the sums alone.
+ *   Q        - [m][Hq][d] element type;  O - [m][Hq][d] fp32.
+ *   causal   - 0: every query sees all n tokens; 1: the queries are those of the
+ *              context's last m tokens (m <= n), query i sees [0, n - m + i + 1).
+ *   acc_in   - [Hkv][ld_acc_in] fp32, the sums so far (NULL: zeros);
+ *   acc_out  - [Hkv][ld_acc_out] fp32: acc_out[h][j] = acc_in[h][j] + the softmax
+ *              weight of token j summed over the m queries and the query heads
+ *              of KV head h, j in [0, n); entries past n are left as they are.
+ *              acc_out may be acc_in (with ld_acc_out == ld_acc_in); otherwise
+ *              they must not overlap.
+ * Every sum is taken in a fixed order: equal calls give equal bits.
+ * Scratch, stream and graphs as for zha_prefix_decode (n >= 1; m * Hq < 2^24).
+ */
+ZHA_API size_t zha_weights_scratch_bytes(const zha_config* cfg, int32_t m, int64_t n);
+ZHA_API int zha_dense_weights(const zha_config* cfg, const void* K, const void* V, int64_t ld, int64_t n, const void* Q,
+                      float* O, int32_t m, int32_t causal, const float* acc_in, int64_t ld_acc_in, float* acc_out,
+                      int64_t ld_acc_out, void* scratch, size_t scratch_bytes, void* stream);
+
+/*
+ * zha_cache_evict: shorten a cache of n tokens to `keep` tokens per KV head:
+ * the first `first`, the last `last`, and between them those with the largest
+ * sums in acc (ties to the lower token; NaN counts as lower than everything).
+ * The kept tokens' rows of K and V and their sums move to the front in token
+ * order.
+ *   K, V     - [Hkv][ld][d] element type;  acc - [Hkv][ld_acc] fp32.
+ *   K_out, V_out - [Hkv][ld_out][d], acc_out - [Hkv][ld_acc_out], rows [0, keep)
+ *              of each head are written, the others left as they are.  An output may be
+ *              its own input (same pointer and row stride); then the rows move in place.
+ *              Otherwise it must not overlap any input.  Where acc is shortened in place,
+ *              its entries [keep, n) are set to zero: the places of tokens to come.
+ *   idx      - [Hkv][keep] int32: the kept tokens of each head, ascending.
+ * 0 <= first, 0 <= last, 1 <= keep, first + last <= keep <= n.
+ * Needs no scratch.  Asynchronous on `stream`; can be captured into a graph.
+ */
+ZHA_API int zha_cache_evict(const zha_config* cfg, const void* K, const void* V, int64_t ld, int64_t n, const float* acc,
+                    int64_t ld_acc, int64_t keep, int64_t first, int64_t last, void* K_out, void* V_out, int64_t ld_out,
+                    float* acc_out, int64_t ld_acc_out, int32_t* idx, void* stream);
+
+/*
+ * zha_tree_evict: zha_cache_evict in place on a tree's own cache, then the tree
+ * over the kept tokens (as zha_tree_build(keep)).  acc - [Hkv][ld_acc], shortened
+ * in place.  `keep` is at most zha_tree_size.
+ */
+ZHA_API int zha_tree_evict(zha_tree* tree, float* acc, int64_t ld_acc, int64_t keep, int64_t first, int64_t last,
+                   int32_t* idx, void* stream);
+
+/* Synchronise `stream` and return the status word at the start of a scratch of
+ * zha_prefix_decode or zha_dense_weights (ZHA_OK, or ZHA_ERR_TIMEOUT when a bounded wait
+ * on a copy or a matrix product ran out in a call since the last look); clears it. */
+ZHA_API int zha_scratch_status(void* scratch, void* stream);
+
+/*
  * zha_tree_set_step_p: top-p thresholds per routing step, for routing whose
  * threshold changes with the depth in the tree and with the context length
  * ("Zyphra Hierarchical Attention", closing section on matching the degree of

@@ -30,7 +30,7 @@ size_t dense_static_floats();
 cudaError_t dense_static_scratch(float** out);
 }  // namespace zha
 
-#include "zha_args.cuh"
+#include "zha_rows.cuh"
 
 using namespace zha;
 
@@ -549,6 +549,278 @@ int zha_dense_decode_noalloc(const zha_config* cfg, const void* K, const void* V
   e = launch_dense(a, cfg->dtype, cfg->d, B, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail_cuda(e, "zha_dense_decode_noalloc");
   return ZHA_OK;
+}
+
+// ------------------------------------------------------------------ shared prefix, weights, eviction
+
+static bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+// Whether [a, a + na) and [b, b + nb) share a byte.
+static bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+static constexpr uint64_t kScratchHead = 256;  // status word
+
+// Largest token counts: positions and byte offsets fit int64 with room to spare.
+static constexpr int64_t kMaxTokens = int64_t(1) << 31;
+
+static int check_tokens(int64_t ld, int64_t n, const char* msg) {
+  return n < 0 || ld < n || ld >= kMaxTokens ? fail(ZHA_ERR_INVALID, msg) : ZHA_OK;
+}
+
+static int prefix_plan(const zha_config* cfg, int32_t B, int32_t m, int64_t n, int64_t ld_own, RowsPlan* p) {
+  int rc = validate(cfg);
+  if (rc) return rc;
+  if (B < 1 || m < 1) return fail(ZHA_ERR_INVALID, "B and m must be >= 1");
+  if (int64_t(B) * m >= (int64_t(1) << 24) || int64_t(B) * m * cfg->n_q_heads >= (int64_t(1) << 24))
+    return fail(ZHA_ERR_UNSUPPORTED, "B * m * n_q_heads must be < 2^24");
+  if (n < 0 || n >= kMaxTokens || ld_own < 0 || ld_own >= kMaxTokens)
+    return fail(ZHA_ERR_INVALID, "n and ld_own must be in [0, 2^31)");
+  rows_plan(cfg->dtype, cfg->d, cfg->n_kv_heads, cfg->n_q_heads / cfg->n_kv_heads, B, m, n, ld_own, p);
+  return ZHA_OK;
+}
+
+static uint64_t rows_part_bytes(const zha_config* cfg, const RowsPlan& p) {
+  return align256(p.part_rows * uint64_t(cfg->d + 2) * 4);
+}
+
+static uint64_t rows_bound_bytes(const zha_config* cfg, int64_t B, int64_t m, int64_t n, int64_t ld_own) {
+  return align256(rows_part_bound(cfg->dtype, cfg->d, cfg->n_kv_heads, cfg->n_q_heads / cfg->n_kv_heads, B, m, n,
+                                  ld_own) * uint64_t(cfg->d + 2) * 4);
+}
+
+static void fill_rows(const zha_config* cfg, const RowsPlan& p, void* scratch, RowsArgs* a) {
+  std::memset(a, 0, sizeof(*a));
+  a->hq = cfg->n_q_heads;
+  a->hkv = cfg->n_kv_heads;
+  a->group = cfg->n_q_heads / cfg->n_kv_heads;
+  a->rb = p.rb;
+  a->kt = p.kt;
+  a->pp = p.pp;
+  a->po = p.po;
+  a->rp = p.rp;
+  a->ro = p.ro;
+  a->nc = p.nc;
+  a->part_own = int64_t(p.part_own);
+  a->scale = 1.0f / std::sqrt(float(cfg->d));
+  a->status = static_cast<int*>(scratch);
+  a->part = reinterpret_cast<float*>(static_cast<char*>(scratch) + kScratchHead);
+}
+
+size_t zha_prefix_scratch_bytes(const zha_config* cfg, int32_t B, int32_t m, int64_t n, int64_t ld_own) {
+  RowsPlan p;
+  if (prefix_plan(cfg, B, m, n, ld_own, &p)) return 0;
+  return size_t(kScratchHead + rows_bound_bytes(cfg, B, m, n, ld_own));
+}
+
+int zha_prefix_decode(const zha_config* cfg, const void* K, const void* V, int64_t ld, int64_t n, const void* K_own,
+                      const void* V_own, int64_t ld_own, const int32_t* own_len, const void* Q, float* O, float* lse,
+                      int32_t B, int32_t m, void* scratch, size_t scratch_bytes, void* stream) {
+  RowsPlan p;
+  int rc = prefix_plan(cfg, B, m, n, ld_own, &p);
+  if (rc) return rc;
+  if ((rc = check_tokens(ld, n, "need 0 <= n <= ld < 2^31"))) return rc;
+  if (!Q || !O || !scratch) return fail(ZHA_ERR_INVALID, "Q, O or scratch is NULL");
+  if (n > 0 && (!K || !V)) return fail(ZHA_ERR_INVALID, "K and V go with n > 0");
+  if (ld_own > 0 && (!K_own || !V_own || !own_len))
+    return fail(ZHA_ERR_INVALID, "K_own, V_own and own_len go with ld_own > 0");
+  if (!aligned(K, 16) || !aligned(V, 16) || !aligned(K_own, 16) || !aligned(V_own, 16) || !aligned(Q, 16) ||
+      !aligned(O, 16) || !aligned(lse, 4) || !aligned(own_len, 4))
+    return fail(ZHA_ERR_INVALID, "K, V, K_own, V_own, Q and O must be 16-byte aligned, lse and own_len 4-byte");
+  if (!aligned(scratch, 256)) return fail(ZHA_ERR_INVALID, "scratch must be 256-byte aligned");
+  if (scratch_bytes < kScratchHead + rows_part_bytes(cfg, p))
+    return fail(ZHA_ERR_CAPACITY, "scratch is smaller than zha_prefix_scratch_bytes");
+  RowsArgs a;
+  fill_rows(cfg, p, scratch, &a);
+  a.K = K;
+  a.V = V;
+  a.Ko = K_own;
+  a.Vo = V_own;
+  a.own_len = own_len;
+  a.Q = Q;
+  a.O = O;
+  a.lse = lse;
+  a.ld = ld;
+  a.n = n;
+  a.ld_own = ld_own;
+  a.B = B;
+  a.m = m;
+  a.rows = int64_t(B) * m * a.group;
+  a.has_own = ld_own > 0 ? 1 : 0;
+  cudaError_t e = launch_rows(a, cfg->dtype, cfg->d, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail_cuda(e, "zha_prefix_decode");
+  return ZHA_OK;
+}
+
+// Scratch of zha_dense_weights: status, partials, the rows' log-sum-exp, the row splits' column sums.
+static int weights_layout(const zha_config* cfg, int32_t m, int64_t n, RowsPlan* rp, WeightsPlan* wp, uint64_t* lse_off,
+                          uint64_t* sums_off, uint64_t* bytes) {
+  int rc = prefix_plan(cfg, 1, m, n, 0, rp);
+  if (rc) return rc;
+  if (n < 1) return fail(ZHA_ERR_INVALID, "n must be >= 1");
+  const int64_t rows = int64_t(m) * (cfg->n_q_heads / cfg->n_kv_heads);
+  weights_plan(cfg->dtype, cfg->d, cfg->n_kv_heads, rows, n, wp);
+  *lse_off = kScratchHead + rows_part_bytes(cfg, *rp);
+  *sums_off = align256(*lse_off + uint64_t(m) * cfg->n_q_heads * 4);
+  *bytes = align256(*sums_off + (wp->rsplit > 1 ? uint64_t(wp->rsplit) * cfg->n_kv_heads * uint64_t(n) * 4 : 0));
+  return ZHA_OK;
+}
+
+size_t zha_weights_scratch_bytes(const zha_config* cfg, int32_t m, int64_t n) {
+  RowsPlan rp;
+  WeightsPlan wp;
+  uint64_t lse_off, sums_off, bytes;
+  if (weights_layout(cfg, m, n, &rp, &wp, &lse_off, &sums_off, &bytes)) return 0;
+  return size_t(kScratchHead + rows_bound_bytes(cfg, 1, m, n, 0) + align256(uint64_t(m) * cfg->n_q_heads * 4) +
+                align256(weights_sums_bound(cfg->n_kv_heads, n) * 4));
+}
+
+int zha_dense_weights(const zha_config* cfg, const void* K, const void* V, int64_t ld, int64_t n, const void* Q,
+                      float* O, int32_t m, int32_t causal, const float* acc_in, int64_t ld_acc_in, float* acc_out,
+                      int64_t ld_acc_out, void* scratch, size_t scratch_bytes, void* stream) {
+  RowsPlan rp;
+  WeightsPlan wp;
+  uint64_t lse_off, sums_off, bytes;
+  int rc = weights_layout(cfg, m, n, &rp, &wp, &lse_off, &sums_off, &bytes);
+  if (rc) return rc;
+  if ((rc = check_tokens(ld, n, "need 1 <= n <= ld < 2^31"))) return rc;
+  if (!K || !Q || !acc_out || !scratch) return fail(ZHA_ERR_INVALID, "K, Q, acc_out or scratch is NULL");
+  if ((V == nullptr) != (O == nullptr)) return fail(ZHA_ERR_INVALID, "V and O go together");
+  if (causal != 0 && causal != 1) return fail(ZHA_ERR_INVALID, "causal must be 0 or 1");
+  if (causal && m > n) return fail(ZHA_ERR_INVALID, "causal needs m <= n");
+  if (ld_acc_out < n || (acc_in && ld_acc_in < n)) return fail(ZHA_ERR_INVALID, "the sums' row strides must be >= n");
+  if (!aligned(K, 16) || !aligned(V, 16) || !aligned(Q, 16) || !aligned(O, 16) || !aligned(acc_in, 4) ||
+      !aligned(acc_out, 4))
+    return fail(ZHA_ERR_INVALID, "K, V, Q and O must be 16-byte aligned, the sums 4-byte");
+  const uint64_t in_bytes = (uint64_t(cfg->n_kv_heads - 1) * ld_acc_in + n) * 4;
+  const uint64_t out_bytes = (uint64_t(cfg->n_kv_heads - 1) * ld_acc_out + n) * 4;
+  if (acc_in && !(acc_in == acc_out && ld_acc_in == ld_acc_out) && overlap(acc_in, in_bytes, acc_out, out_bytes))
+    return fail(ZHA_ERR_INVALID, "acc_in and acc_out overlap");
+  if (!aligned(scratch, 256)) return fail(ZHA_ERR_INVALID, "scratch must be 256-byte aligned");
+  if (scratch_bytes < bytes) return fail(ZHA_ERR_CAPACITY, "scratch is smaller than zha_weights_scratch_bytes");
+  RowsArgs a;
+  fill_rows(cfg, rp, scratch, &a);
+  a.K = K;
+  a.V = V;
+  a.Q = Q;
+  a.O = O;
+  a.lse = reinterpret_cast<float*>(static_cast<char*>(scratch) + lse_off);
+  a.ld = ld;
+  a.n = n;
+  a.B = 1;
+  a.m = m;
+  a.rows = int64_t(m) * a.group;
+  a.causal = causal;
+  WeightsArgs w;
+  std::memset(&w, 0, sizeof(w));
+  w.K = K;
+  w.Q = Q;
+  w.lse = a.lse;
+  w.acc_in = acc_in;
+  w.acc_out = acc_out;
+  w.sums = reinterpret_cast<float*>(static_cast<char*>(scratch) + sums_off);
+  w.status = a.status;
+  w.ld = ld;
+  w.n = n;
+  w.ld_acc_in = ld_acc_in;
+  w.ld_acc_out = ld_acc_out;
+  w.rows = a.rows;
+  w.m = m;
+  w.hq = a.hq;
+  w.hkv = a.hkv;
+  w.group = a.group;
+  w.causal = causal;
+  w.rsplit = wp.rsplit;
+  w.rows_per_split = wp.rows_per_split;
+  w.scale = a.scale;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_rows(a, cfg->dtype, cfg->d, st);
+  if (e != cudaSuccess) return fail_cuda(e, "zha_dense_weights: attention");
+  e = launch_weights(w, cfg->dtype, cfg->d, st);
+  if (e != cudaSuccess) return fail_cuda(e, "zha_dense_weights: sums");
+  return ZHA_OK;
+}
+
+int zha_cache_evict(const zha_config* cfg, const void* K, const void* V, int64_t ld, int64_t n, const float* acc,
+                    int64_t ld_acc, int64_t keep, int64_t first, int64_t last, void* K_out, void* V_out, int64_t ld_out,
+                    float* acc_out, int64_t ld_acc_out, int32_t* idx, void* stream) {
+  int rc = validate(cfg);
+  if (rc) return rc;
+  if (!K || !V || !acc || !K_out || !V_out || !acc_out || !idx) return fail(ZHA_ERR_INVALID, "a pointer is NULL");
+  if ((rc = check_tokens(ld, n, "need 1 <= n <= ld < 2^31"))) return rc;
+  if (keep < 1 || keep > n) return fail(ZHA_ERR_INVALID, "need 1 <= keep <= n");
+  if (first < 0 || last < 0 || first > keep || last > keep - first)
+    return fail(ZHA_ERR_INVALID, "need first, last >= 0 and first + last <= keep");
+  if (ld_acc < n || ld_out < keep || ld_acc_out < keep || ld_out >= kMaxTokens || ld_acc >= kMaxTokens ||
+      ld_acc_out >= kMaxTokens)
+    return fail(ZHA_ERR_INVALID, "need ld_acc >= n, ld_out >= keep and ld_acc_out >= keep, all < 2^31");
+  if (!aligned(K, 16) || !aligned(V, 16) || !aligned(K_out, 16) || !aligned(V_out, 16) || !aligned(acc, 4) ||
+      !aligned(acc_out, 4) || !aligned(idx, 4))
+    return fail(ZHA_ERR_INVALID, "K, V and their outputs must be 16-byte aligned, acc, acc_out and idx 4-byte");
+  EvictArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.row_bytes = cfg->d * elem_size(cfg->dtype);
+  const uint64_t hk = uint64_t(cfg->n_kv_heads) - 1, rb = uint64_t(a.row_bytes);
+  // inputs and outputs with the bytes they span; an output may be its own input (rows of a head then move
+  // towards its front, in order), and shares nothing with any other buffer
+  const struct { const void* p; uint64_t n; } in[3] = {{K, (hk * ld + n) * rb}, {V, (hk * ld + n) * rb},
+                                                       {acc, (hk * ld_acc + n) * 4}};
+  const struct { const void* p; uint64_t n; bool same; } out[4] = {
+      {K_out, (hk * ld_out + keep) * rb, K_out == K && ld_out == ld},
+      {V_out, (hk * ld_out + keep) * rb, V_out == V && ld_out == ld},
+      {acc_out, (hk * ld_acc_out + keep) * 4, acc_out == acc && ld_acc_out == ld_acc},
+      {idx, (hk + 1) * keep * 4, false}};
+  for (int o = 0; o < 4; ++o) {
+    for (int i = 0; i < 3; ++i)
+      if (!(out[o].same && i == o) && overlap(out[o].p, out[o].n, in[i].p, in[i].n))
+        return fail(ZHA_ERR_INVALID, "an output overlaps an input (only an output that is its own input may)");
+    for (int q = 0; q < o; ++q)
+      if (overlap(out[o].p, out[o].n, out[q].p, out[q].n)) return fail(ZHA_ERR_INVALID, "two outputs overlap");
+    if (out[o].same) a.in_place = 1;
+  }
+  a.K = K;
+  a.V = V;
+  a.acc = acc;
+  a.K_out = K_out;
+  a.V_out = V_out;
+  a.acc_out = acc_out;
+  a.idx = idx;
+  a.ld = ld;
+  a.ld_acc = ld_acc;
+  a.ld_out = ld_out;
+  a.ld_acc_out = ld_acc_out;
+  a.n = n;
+  a.keep = keep;
+  a.first = first;
+  a.last = last;
+  a.hkv = cfg->n_kv_heads;
+  cudaError_t e = launch_evict(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail_cuda(e, "zha_cache_evict");
+  return ZHA_OK;
+}
+
+int zha_tree_evict(zha_tree* t, float* acc, int64_t ld_acc, int64_t keep, int64_t first, int64_t last, int32_t* idx,
+                   void* stream) {
+  if (!t) return fail(ZHA_ERR_INVALID, "tree is NULL");
+  int rc = zha_cache_evict(&t->cfg, t->dev.K, t->dev.V, t->cfg.capacity, t->n, acc, ld_acc, keep, first, last, t->dev.K,
+                           t->dev.V, t->cfg.capacity, acc, ld_acc, idx, stream);
+  if (rc) return rc;
+  return zha_tree_build(t, keep, stream);
+}
+
+int zha_scratch_status(void* scratch, void* stream) {
+  if (!scratch) return fail(ZHA_ERR_INVALID, "scratch is NULL");
+  cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail_cuda(e, "zha_scratch_status: synchronize");
+  int status = 0;
+  e = cudaMemcpy(&status, scratch, sizeof(int), cudaMemcpyDeviceToHost);
+  if (e != cudaSuccess) return fail_cuda(e, "zha_scratch_status: read");
+  if (status == 0) return ZHA_OK;
+  const int zero = 0;
+  cudaMemcpy(scratch, &zero, sizeof(int), cudaMemcpyHostToDevice);
+  return fail(status, "a kernel raised an error status (a bounded wait on a copy or a matrix product ran out)");
 }
 
 int zha_tree_set_step_p(zha_tree* t, const float* p, int32_t n) {

@@ -1,0 +1,541 @@
+// Many query rows over one KV cache on the CUDA cores (fp32 configurations),
+// the join of the partials, and the column sums of the softmax weights.
+// The work split is described in zha_rows.cuh.
+#include "zha_rows.cuh"
+
+namespace zha {
+
+constexpr int kRowsThreads = 128;
+constexpr int kRowsKeys = 64;  // keys per tile
+constexpr int kWeightsCtas = 148 * 4;  // CTAs that the weights pass splits its rows up to
+
+// ------------------------------------------------------------------ attention, CUDA cores
+// One CTA: RB = 8 * RT rows against tiles of 64 keys.  A half-warp owns RT
+// rows: for S = Q K^T each lane holds RT rows x 4 keys (key = lane + 16 j), so a
+// row's maximum and sum are shuffles within the half-warp; for O += P V each lane
+// holds the same RT rows x d/16 columns, P passed through shared memory within
+// the warp.  Rows of shared memory are padded by 16 bytes, so 16-byte reads of 8
+// consecutive rows meet no bank conflict.  Per 4 dimensions a lane does 16 RT
+// FMAs on RT + 4 16-byte reads: the FMA pipe bounds it for RT >= 4, HBM for RT = 1
+// (few rows).
+template <typename T, int D, int RT>
+__global__ void __launch_bounds__(kRowsThreads) rows_scalar_kernel(RowsArgs a) {
+  constexpr int RB = 8 * RT, LD = D + 4, PLD = kRowsKeys + 4, CT = D / 16;
+  constexpr int EPC = 16 / sizeof(T), CPR = D / EPC;  // elements per 16-byte chunk, chunks per row
+  extern __shared__ __align__(16) float sm[];
+  float* sq = sm;
+  float* sk = sq + RB * LD;
+  float* sv = sk + kRowsKeys * LD;
+  float* sp = sv + kRowsKeys * LD;
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int half = wid * 2 + (lane >> 4), l16 = lane & 15;
+  const float c2 = a.scale * 1.4426950408889634f;  // weights as powers of two
+  const RowsTotals tot = rows_totals(a);
+  int64_t x = cta_first_tile(tot.all, a.nc, blockIdx.x);
+  const int64_t x_end = cta_first_tile(tot.all, a.nc, blockIdx.x + 1);
+  bool first_of_cta = true;
+  while (x < x_end) {
+    const RowsSeg s = rows_find(a, tot, x);
+    const int64_t seg_rows = s.own ? int64_t(a.m) * a.group : a.rows;
+    const int64_t r0 = int64_t(s.p) * RB;
+    const int nrows = int(min64(RB, seg_rows - r0));
+    const int64_t row_off = s.own ? int64_t(s.b) * a.m * a.group : 0;  // the sequence's first row of the head
+    const int64_t len = s.own ? own_tokens(a, s.b) : a.n;
+    const T* Kh = s.own ? static_cast<const T*>(a.Ko) + (int64_t(s.b) * a.hkv + s.h) * a.ld_own * D
+                        : static_cast<const T*>(a.K) + int64_t(s.h) * a.ld * D;
+    const T* Vh = s.own ? static_cast<const T*>(a.Vo) + (int64_t(s.b) * a.hkv + s.h) * a.ld_own * D
+                        : (a.V ? static_cast<const T*>(a.V) + int64_t(s.h) * a.ld * D : nullptr);
+    __syncthreads();
+    for (int i = tid; i < RB * CPR; i += kRowsThreads) {
+      const int r = i / CPR, c = i % CPR;
+      float v[EPC];
+#pragma unroll
+      for (int e = 0; e < EPC; ++e) v[e] = 0.f;
+      if (r < nrows)
+        unpack16<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(a.Q) +
+                                                    row_index(a, s.h, row_off + r0 + r) * D + c * EPC), v);
+#pragma unroll
+      for (int e = 0; e < EPC; e += 4)
+        *reinterpret_cast<float4*>(sq + r * LD + c * EPC + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+    }
+    int64_t lim[RT];
+    float m_run[RT], l_run[RT], o[RT][CT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const int64_t r = r0 + half * RT + i;
+      lim[i] = r >= seg_rows ? 0 : (s.own ? own_limit(a, len, r) : prefix_limit(a, r));
+      m_run[i] = -INFINITY;
+      l_run[i] = 0.f;
+#pragma unroll
+      for (int j = 0; j < CT; ++j) o[i][j] = 0.f;
+    }
+    const int64_t t_end = min64(s.first + s.tiles, x_end) - s.first;
+    for (int64_t t = x - s.first; t < t_end; ++t) {
+      const int64_t k0 = t * kRowsKeys;
+      __syncthreads();
+      for (int i = tid; i < kRowsKeys * CPR; i += kRowsThreads) {
+        const int r = i / CPR, c = i % CPR;
+        float k[EPC], v[EPC];
+#pragma unroll
+        for (int e = 0; e < EPC; ++e) k[e] = v[e] = 0.f;  // keys past the range: zeros, never what lies there
+        if (k0 + r < len) {
+          unpack16<T>(ldg_stream(Kh + (k0 + r) * D + c * EPC), k);
+          if (Vh) unpack16<T>(ldg_stream(Vh + (k0 + r) * D + c * EPC), v);
+        }
+#pragma unroll
+        for (int e = 0; e < EPC; e += 4) {
+          *reinterpret_cast<float4*>(sk + r * LD + c * EPC + e) = make_float4(k[e], k[e + 1], k[e + 2], k[e + 3]);
+          if (Vh) *reinterpret_cast<float4*>(sv + r * LD + c * EPC + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        }
+      }
+      __syncthreads();
+      float acc[RT][4];
+#pragma unroll
+      for (int i = 0; i < RT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+#pragma unroll 4
+      for (int e = 0; e < D; e += 4) {
+        float4 kv[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(sk + (l16 + 16 * j) * LD + e);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          const float4 qv = *reinterpret_cast<const float4*>(sq + (half * RT + i) * LD + e);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            acc[i][j] = fmaf(qv.x, kv[j].x, acc[i][j]);
+            acc[i][j] = fmaf(qv.y, kv[j].y, acc[i][j]);
+            acc[i][j] = fmaf(qv.z, kv[j].z, acc[i][j]);
+            acc[i][j] = fmaf(qv.w, kv[j].w, acc[i][j]);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        float mx = m_run[i];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          acc[i][j] = k0 + l16 + 16 * j < lim[i] ? acc[i][j] * c2 : -INFINITY;
+          mx = fmaxf(mx, acc[i][j]);
+        }
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+        const float base = mx == -INFINITY ? 0.f : mx;  // a row that sees nothing yet: every weight 2^-inf = 0
+        const float sc = exp2f(m_run[i] - base);
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float p = exp2f(acc[i][j] - base);
+          sum += p;
+          if (Vh) sp[(half * RT + i) * PLD + l16 + 16 * j] = p;
+        }
+        l_run[i] = fmaf(l_run[i], sc, sum);
+        m_run[i] = mx;
+#pragma unroll
+        for (int j = 0; j < CT; ++j) o[i][j] *= sc;
+      }
+      if (Vh) {
+        __syncwarp();
+#pragma unroll 2
+        for (int k = 0; k < kRowsKeys; k += 4) {
+          float4 pv[RT];
+#pragma unroll
+          for (int i = 0; i < RT; ++i) pv[i] = *reinterpret_cast<const float4*>(sp + (half * RT + i) * PLD + k);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            float vv[CT];
+#pragma unroll
+            for (int j = 0; j < CT; j += 4) {  // columns l16*4 + 64*(j/4): 16 lanes read 256 contiguous bytes
+              const float4 v4 = *reinterpret_cast<const float4*>(sv + (k + kk) * LD + l16 * 4 + 16 * j);
+              vv[j] = v4.x;
+              vv[j + 1] = v4.y;
+              vv[j + 2] = v4.z;
+              vv[j + 3] = v4.w;
+            }
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+              const float p = kk == 0 ? pv[i].x : (kk == 1 ? pv[i].y : (kk == 2 ? pv[i].z : pv[i].w));
+#pragma unroll
+              for (int j = 0; j < CT; ++j) o[i][j] = fmaf(p, vv[j], o[i][j]);
+            }
+          }
+        }
+        __syncwarp();
+      }
+    }
+    // the segment's share of this CTA: a partial, or the row's result where the CTA holds the whole segment
+    const bool whole = !a.has_own && x == s.first && t_end == s.tiles;
+    const int64_t slot = part_row(a, blockIdx.x, s.own, s.id, first_of_cta);
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const int rl = half * RT + i;
+      float l = l_run[i];
+#pragma unroll
+      for (int off = 8; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+      if (rl < nrows) {
+        const int64_t ri = row_index(a, s.h, row_off + r0 + rl);
+        float* P = whole ? nullptr : a.part + (slot + rl) * (D + 2);
+        if (l16 == 0) {
+          if (!whole) {
+            P[0] = m_run[i];
+            P[1] = l;
+          } else if (a.lse) {
+            a.lse[ri] = l > 0.f ? (m_run[i] + log2f(l)) * 0.6931471805599453f : (l == 0.f ? -INFINITY : l);
+          }
+        }
+        if (a.V || s.own) {
+          const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+#pragma unroll
+          for (int j = 0; j < CT; ++j) {
+            const int col = l16 * 4 + 16 * (j & ~3) + (j & 3);
+            if (whole) a.O[ri * D + col] = o[i][j] * inv;
+            else P[2 + col] = o[i][j];
+          }
+        }
+      }
+    }
+    first_of_cta = false;
+    x = s.first + t_end;
+  }
+}
+
+// ------------------------------------------------------------------ join of the partials
+// o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s over the CTAs that touched the
+// row's segments, in CTA order (prefix first); W warps per row take strided
+// partials and are joined in warp order, so the result does not depend on timing.
+template <int D, int W>
+__global__ void __launch_bounds__(256) rows_combine_kernel(RowsArgs a) {
+  constexpr int EL = D / 32;
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int64_t item = int64_t(blockIdx.x) * (8 / W) + wid / W;  // row of all heads
+  const int w = wid % W;
+  const int64_t total_rows = a.rows * a.hkv;
+  const bool live = item < total_rows;
+  const int h = live ? int(item / a.rows) : 0;
+  const int64_t r = live ? item - int64_t(h) * a.rows : 0;
+  const RowsTotals tot = rows_totals(a);
+  float M = -INFINITY, L = 0.f, o[EL];
+#pragma unroll
+  for (int e = 0; e < EL; ++e) o[e] = 0.f;
+  bool direct = false;
+  for (int part = 0; part < (a.has_own ? 2 : 1) && live; ++part) {
+    int64_t first, tiles;
+    int id;
+    int64_t rl;
+    if (part == 0) {
+      const int p = int(r / a.rb);
+      rl = r - int64_t(p) * a.rb;
+      tiles = prefix_tiles(a, p);
+      first = int64_t(h) * tot.head + (a.causal ? warp_total(p, [&](int q) { return prefix_tiles(a, q); }) : p * tiles);
+      id = h * a.pp + p;
+    } else {
+      const int64_t mg = int64_t(a.m) * a.group;
+      const int b = int(r / mg);
+      const int64_t rs = r - b * mg;
+      const int p = int(rs / a.rb);
+      rl = rs - int64_t(p) * a.rb;
+      tiles = own_tiles(a, b);
+      const int u = h * a.po + p;
+      first = tot.prefix + int64_t(a.hkv) * a.po * warp_total(b, [&](int q) { return own_tiles(a, q); }) + u * tiles;
+      id = a.hkv * a.pp + b * a.hkv * a.po + u;
+    }
+    if (tiles == 0) continue;
+    const int c_lo = tile_cta(tot.all, a.nc, first), c_hi = tile_cta(tot.all, a.nc, first + tiles - 1);
+    if (!a.has_own && c_lo == c_hi) {
+      direct = true;  // written by its CTA
+      continue;
+    }
+    for (int c = c_lo + w; c <= c_hi; c += W) {
+      const float* P = a.part + (part_row(a, c, part, id, cta_first_tile(tot.all, a.nc, c) >= first) + rl) * (D + 2);
+      const float m_s = __ldcg(P), l_s = __ldcg(P + 1);
+      float v[EL];
+#pragma unroll
+      for (int e = 0; e < EL; ++e) v[e] = a.O ? __ldcg(P + 2 + lane + 32 * e) : 0.f;
+      if (m_s == -INFINITY && l_s == 0.f) continue;  // nothing of this share is visible to the row
+      const float mn = fmaxf(M, m_s), s0 = exp2f(M - mn), s1 = exp2f(m_s - mn);
+      L = L * s0 + l_s * s1;
+#pragma unroll
+      for (int e = 0; e < EL; ++e) o[e] = o[e] * s0 + v[e] * s1;
+      M = mn;
+    }
+  }
+  __shared__ float jm[8], jl[8], jo[8][D];
+  if (W > 1) {
+    if (lane == 0) {
+      jm[wid] = M;
+      jl[wid] = L;
+    }
+#pragma unroll
+    for (int e = 0; e < EL; ++e) jo[wid][lane + 32 * e] = o[e];
+    __syncthreads();
+    if (w == 0) {
+#pragma unroll
+      for (int q = 1; q < W; ++q) {
+        const float m_s = jm[wid + q];
+        if (m_s == -INFINITY && jl[wid + q] == 0.f) continue;
+        const float mn = fmaxf(M, m_s), s0 = exp2f(M - mn), s1 = exp2f(m_s - mn);
+        L = L * s0 + jl[wid + q] * s1;
+#pragma unroll
+        for (int e = 0; e < EL; ++e) o[e] = o[e] * s0 + jo[wid + q][lane + 32 * e] * s1;
+        M = mn;
+      }
+    }
+  }
+  if (live && w == 0 && !direct) {
+    const int64_t ri = row_index(a, h, r);
+    if (a.O) {
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+      for (int e = 0; e < EL; ++e) a.O[ri * D + lane + 32 * e] = o[e] * inv;
+    }
+    if (a.lse && lane == 0) a.lse[ri] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : (L == 0.f ? -INFINITY : L);
+  }
+}
+
+// ------------------------------------------------------------------ column sums of the weights, CUDA cores
+// acc_out[h][k] = acc_in[h][k] + sum over rows of 2^(s c - lse): one CTA per (64 keys, KV head, row split); a
+// lane holds RT rows x 4 keys of S as above and sums over its rows; the eight half-warps are joined in order.
+template <typename T, int D, int RT>
+__global__ void __launch_bounds__(kRowsThreads) weights_scalar_kernel(WeightsArgs a) {
+  constexpr int RB = 8 * RT, LD = D + 4, EPC = 16 / sizeof(T), CPR = D / EPC;
+  extern __shared__ __align__(16) float sm[];
+  float* sq = sm;
+  float* sk = sq + RB * LD;
+  float* sl = sk + kRowsKeys * LD;  // lse of the block's rows, in powers of two
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int half = wid * 2 + (lane >> 4), l16 = lane & 15;
+  const float c2 = a.scale * 1.4426950408889634f;
+  const int64_t k0 = int64_t(blockIdx.x) * kRowsKeys;
+  const int h = blockIdx.y;
+  const T* Kh = static_cast<const T*>(a.K) + int64_t(h) * a.ld * D;
+  for (int i = tid; i < kRowsKeys * CPR; i += kRowsThreads) {
+    const int r = i / CPR, c = i % CPR;
+    float k[EPC];
+#pragma unroll
+    for (int e = 0; e < EPC; ++e) k[e] = 0.f;
+    if (k0 + r < a.n) unpack16<T>(ldg_stream(Kh + (k0 + r) * D + c * EPC), k);
+#pragma unroll
+    for (int e = 0; e < EPC; e += 4)
+      *reinterpret_cast<float4*>(sk + r * LD + c * EPC + e) = make_float4(k[e], k[e + 1], k[e + 2], k[e + 3]);
+  }
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  const int64_t rend = min64(a.rows, int64_t(blockIdx.z + 1) * a.rows_per_split);
+  int64_t rbeg = int64_t(blockIdx.z) * a.rows_per_split;
+  if (a.causal) {  // rows before the first that sees this tile's first key
+    const int64_t first = max64(0, k0 - (a.n - a.m)) * a.group;
+    if (first > rbeg) rbeg = first / RB * RB;
+  }
+  for (int64_t r0 = rbeg; r0 < rend; r0 += RB) {
+    __syncthreads();
+    for (int i = tid; i < RB * CPR; i += kRowsThreads) {
+      const int r = i / CPR, c = i % CPR;
+      float v[EPC];
+#pragma unroll
+      for (int e = 0; e < EPC; ++e) v[e] = 0.f;
+      const int64_t rr = r0 + r;
+      if (rr < rend) {
+        const int64_t t = rr / a.group, ri = t * a.hq + int64_t(h) * a.group + (rr - t * a.group);
+        unpack16<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(a.Q) + ri * D + c * EPC), v);
+        if (c == 0) sl[r] = a.lse[ri] * 1.4426950408889634f;
+      } else if (c == 0) {
+        sl[r] = INFINITY;  // no row: every weight 2^-inf = 0
+      }
+#pragma unroll
+      for (int e = 0; e < EPC; e += 4)
+        *reinterpret_cast<float4*>(sq + r * LD + c * EPC + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+    }
+    __syncthreads();
+    float acc[RT][4];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+#pragma unroll 4
+    for (int e = 0; e < D; e += 4) {
+      float4 kv[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(sk + (l16 + 16 * j) * LD + e);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        const float4 qv = *reinterpret_cast<const float4*>(sq + (half * RT + i) * LD + e);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          acc[i][j] = fmaf(qv.x, kv[j].x, acc[i][j]);
+          acc[i][j] = fmaf(qv.y, kv[j].y, acc[i][j]);
+          acc[i][j] = fmaf(qv.z, kv[j].z, acc[i][j]);
+          acc[i][j] = fmaf(qv.w, kv[j].w, acc[i][j]);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const int64_t rr = r0 + half * RT + i;
+      const int64_t lim = a.causal ? a.n - a.m + rr / a.group + 1 : a.n;
+      const float ls = sl[half * RT + i];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (k0 + l16 + 16 * j < lim) sum[j] += exp2f(fmaf(acc[i][j], c2, -ls));
+    }
+  }
+  __syncthreads();
+  float* red = sq;  // [8][64]
+#pragma unroll
+  for (int j = 0; j < 4; ++j) red[half * kRowsKeys + l16 + 16 * j] = sum[j];
+  __syncthreads();
+  if (tid < kRowsKeys && k0 + tid < a.n) {
+    float s = 0.f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) s += red[q * kRowsKeys + tid];
+    if (a.rsplit > 1) {
+      a.sums[(int64_t(blockIdx.z) * a.hkv + h) * a.n + k0 + tid] = s;
+    } else {
+      a.acc_out[h * a.ld_acc_out + k0 + tid] = (a.acc_in ? a.acc_in[h * a.ld_acc_in + k0 + tid] : 0.f) + s;
+    }
+  }
+}
+
+// acc_out = acc_in + the row splits' sums, in split order.
+__global__ void __launch_bounds__(256) weights_join_kernel(WeightsArgs a) {
+  const int64_t k = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
+  const int h = blockIdx.y;
+  if (k >= a.n) return;
+  float s = 0.f;
+  for (int z = 0; z < a.rsplit; ++z) s += a.sums[(int64_t(z) * a.hkv + h) * a.n + k];
+  a.acc_out[h * a.ld_acc_out + k] = (a.acc_in ? a.acc_in[h * a.ld_acc_in + k] : 0.f) + s;
+}
+
+// ------------------------------------------------------------------ host side
+namespace {
+
+int scalar_rt(int d, int64_t rows) { return rows <= 8 ? 1 : (d == 128 || rows <= 32 ? 4 : 8); }
+
+size_t rows_smem(int d, int rt) {
+  return size_t(8 * rt * (d + 4) + 2 * kRowsKeys * (d + 4) + 8 * rt * (kRowsKeys + 4)) * sizeof(float);
+}
+
+size_t weights_smem(int d, int rt) { return size_t(8 * rt * (d + 4) + kRowsKeys * (d + 4) + 8 * rt) * sizeof(float); }
+
+template <typename K> cudaError_t allow_smem(K kernel, size_t bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+}
+
+template <typename T, int D, int RT> cudaError_t run_rows(const RowsArgs& a, cudaStream_t st) {
+  const size_t sm = rows_smem(D, RT);
+  cudaError_t e = allow_smem(rows_scalar_kernel<T, D, RT>, sm);
+  if (e != cudaSuccess) return e;
+  rows_scalar_kernel<T, D, RT><<<a.nc, kRowsThreads, sm, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T, int D> cudaError_t run_rows_rt(const RowsArgs& a, cudaStream_t st) {
+  switch (a.rb / 8) {
+    case 1: return run_rows<T, D, 1>(a, st);
+    case 4: return run_rows<T, D, 4>(a, st);
+    default: return run_rows<T, D, 8>(a, st);
+  }
+}
+
+template <int D> cudaError_t run_combine(const RowsArgs& a, cudaStream_t st) {
+  const int64_t rows = a.rows * a.hkv;
+  // few rows: eight warps share a row's partials (up to one per CTA); many rows have few partials each
+  if (rows < 2048) rows_combine_kernel<D, 8><<<unsigned(rows), 256, 0, st>>>(a);
+  else rows_combine_kernel<D, 1><<<unsigned((rows + 7) / 8), 256, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T, int D, int RT> cudaError_t run_weights(const WeightsArgs& a, cudaStream_t st) {
+  const size_t sm = weights_smem(D, RT);
+  cudaError_t e = allow_smem(weights_scalar_kernel<T, D, RT>, sm);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(unsigned((a.n + kRowsKeys - 1) / kRowsKeys), unsigned(a.hkv), unsigned(a.rsplit));
+  weights_scalar_kernel<T, D, RT><<<grid, kRowsThreads, sm, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T, int D> cudaError_t run_weights_rt(const WeightsArgs& a, cudaStream_t st) {
+  switch (scalar_rt(D, a.rows)) {
+    case 1: return run_weights<T, D, 1>(a, st);
+    case 4: return run_weights<T, D, 4>(a, st);
+    default: return run_weights<T, D, 8>(a, st);
+  }
+}
+
+}  // namespace
+
+static void scalar_plan(int d, int rt, int hkv, int64_t B, int64_t rows, int64_t mg, int64_t n, int64_t ld_own,
+                        RowsPlan* p) {
+  p->kt = kRowsKeys;
+  p->rb = 8 * rt;
+  const int per_sm = int(220 * 1024 / (rows_smem(d, rt) + 1024));
+  p->pp = int((rows + p->rb - 1) / p->rb);
+  p->po = ld_own > 0 ? int((mg + p->rb - 1) / p->rb) : 0;
+  p->rp = int(rows < p->rb ? rows : p->rb);
+  p->ro = int(mg < p->rb ? mg : p->rb);
+  // at most one CTA per tile (an upper bound: own caches as long as they can be)
+  const double tiles = double(hkv) * p->pp * double((n + p->kt - 1) / p->kt) +
+                       double(B) * hkv * p->po * double((ld_own + p->kt - 1) / p->kt);
+  const int most = 148 * (per_sm < 1 ? 1 : (per_sm > 4 ? 4 : per_sm));
+  p->nc = tiles < 1 ? 1 : (tiles < most ? int(tiles) : most);
+  if (ld_own > 0) {
+    p->part_own = (uint64_t(p->nc) + uint64_t(hkv) * p->pp) * p->rp;
+    p->part_rows = p->part_own + (uint64_t(p->nc) + uint64_t(B) * hkv * p->po) * p->ro;
+  } else {
+    p->part_own = 0;
+    p->part_rows = 2 * uint64_t(p->nc) * p->rp;
+  }
+}
+
+void rows_plan(int dtype, int d, int hkv, int group, int64_t B, int64_t m, int64_t n, int64_t ld_own, RowsPlan* p) {
+  const int64_t rows = B * m * group;
+  scalar_plan(d, scalar_rt(d, rows), hkv, B, rows, m * group, n, ld_own, p);
+}
+
+// Partial rows that cover every call with at most B sequences, m query tokens, n and ld_own tokens.  For one
+// variant the plan's rows grow with each of them; smaller calls may take a variant of fewer rows per block.
+uint64_t rows_part_bound(int dtype, int d, int hkv, int group, int64_t B, int64_t m, int64_t n, int64_t ld_own) {
+  const int64_t rows = B * m * group, mg = m * group;
+  uint64_t most = 0;
+  for (int rt = 1; rt <= 8; rt = rt == 1 ? 4 : 2 * rt) {
+    const int64_t cap = rt == 1 ? 8 : (rt == 4 && d == 64 ? 32 : rows);  // rows that take this variant
+    if (rt > scalar_rt(d, rows)) break;
+    for (int own = 0; own < 2; ++own) {
+      RowsPlan p;
+      scalar_plan(d, rt, hkv, min64(B, cap), min64(rows, cap), min64(mg, cap), n, own ? ld_own : 0, &p);
+      if (p.part_rows > most) most = p.part_rows;
+    }
+  }
+  return most;
+}
+
+cudaError_t launch_rows(const RowsArgs& a, int dtype, int d, cudaStream_t st) {
+  count_launches(2);
+  cudaError_t e;
+  if (dtype == ZHA_BF16) e = d == 128 ? run_rows_rt<__nv_bfloat16, 128>(a, st) : run_rows_rt<__nv_bfloat16, 64>(a, st);
+  else e = d == 128 ? run_rows_rt<float, 128>(a, st) : run_rows_rt<float, 64>(a, st);
+  if (e != cudaSuccess) return e;
+  return d == 128 ? run_combine<128>(a, st) : run_combine<64>(a, st);
+}
+
+void weights_plan(int dtype, int d, int hkv, int64_t rows, int64_t n, WeightsPlan* p) {
+  const int64_t rb = 8 * scalar_rt(d, rows);
+  const int64_t ctas = (n + kRowsKeys - 1) / kRowsKeys * hkv, blocks = (rows + rb - 1) / rb;
+  int64_t s = (kWeightsCtas + ctas - 1) / ctas;  // a few CTAs per SM
+  if (s > blocks) s = blocks;
+  if (s > 64) s = 64;
+  p->rows_per_split = (blocks + s - 1) / s * rb;
+  p->rsplit = int((rows + p->rows_per_split - 1) / p->rows_per_split);
+}
+
+// Floats of column sums that cover every call with at most n tokens: the splits of n' <= n tokens take
+// ceil(kWeightsCtas / ctas) * hkv * n' <= 64 * kWeightsCtas + hkv * n floats.
+uint64_t weights_sums_bound(int hkv, int64_t n) { return uint64_t(kWeightsCtas) * kRowsKeys + uint64_t(hkv) * n; }
+
+cudaError_t launch_weights(const WeightsArgs& a, int dtype, int d, cudaStream_t st) {
+  cudaError_t e;
+  count_launches(a.rsplit > 1 ? 2 : 1);
+  if (dtype == ZHA_BF16)
+    e = d == 128 ? run_weights_rt<__nv_bfloat16, 128>(a, st) : run_weights_rt<__nv_bfloat16, 64>(a, st);
+  else e = d == 128 ? run_weights_rt<float, 128>(a, st) : run_weights_rt<float, 64>(a, st);
+  if (e != cudaSuccess || a.rsplit <= 1) return e;
+  weights_join_kernel<<<dim3(unsigned((a.n + 255) / 256), unsigned(a.hkv)), 256, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace zha

@@ -1,0 +1,236 @@
+// Arguments and work split shared by the kernels that attend many query rows
+// over one KV cache: zha_prefix_decode and zha_dense_weights.
+//
+// Rows.  One KV head serves `group` query heads; the rows of KV head h are the
+// (sequence b, query token i, head g) triples in that order, row index
+// (b * m + i) * group + g.  The shared tokens [0, n) are attended by all rows of
+// the head (row block = up to `rb` rows), a sequence's own tokens by its m * group
+// rows.
+//
+// Work split.  A segment is one row block over one key range: first the
+// prefix segments (h, row block), then the own segments (b, h, row block of the
+// sequence).  A segment is cut into key tiles; all tiles of all segments form
+// one flat list, and CTA c of nc takes tiles [c*T/nc, (c+1)*T/nc).  So every CTA
+// has the same number of tiles whatever the lengths are, lengths that only
+// the device knows included.  A CTA leaves one partial (running max, running sum,
+// numerator) per segment it touches; rows_combine_kernel joins them in CTA order.
+#pragma once
+
+#include "zha_args.cuh"
+
+namespace zha {
+
+struct RowsArgs {
+  const void* K;            // [hkv][ld][d], tokens [0, n) are read
+  const void* V;            // NULL: no outputs, only the rows' log-sum-exp
+  const void* Ko;           // own caches [B][hkv][ld_own][d] (NULL: none)
+  const void* Vo;
+  const int32_t* own_len;   // [B] device
+  const void* Q;            // [B][m][hq][d]
+  float* O;                 // [B][m][hq][d] (NULL with V)
+  float* lse;               // [B][m][hq] natural log, may be NULL
+  float* part;              // partials, (d + 2) floats per row: m, l, o[d]
+  float* logits;            // NULL, or [hkv][rows][n] raw dot products of the prefix to leave for the weights pass
+  int* status;
+  int64_t ld, n, ld_own;
+  int64_t rows;             // rows per KV head over the prefix: B * m * group
+  int64_t part_own;         // first own slot's offset in `part`, in rows
+  int B, m, hq, hkv, group;
+  int causal;               // 1: query i sees prefix tokens [0, n - m + i] (B = 1)
+  int has_own;
+  int rb;                   // rows per row block
+  int kt;                   // keys per tile
+  int pp, po;               // row blocks of a prefix / an own segment
+  int rp, ro;               // rows of a prefix / an own partial slot
+  int nc;                   // CTAs
+  float scale;              // 1 / sqrt(d)
+};
+
+// Tokens of sequence b's own cache (a length outside [0, ld_own] is clamped, so that no read leaves the cache).
+__device__ __forceinline__ int64_t own_tokens(const RowsArgs& a, int b) {
+  const int64_t v = a.own_len[b];
+  return v < 0 ? 0 : min64(v, a.ld_own);
+}
+
+// Keys of the prefix that row r of a KV head sees (causal: its query token's position + 1).
+__device__ __forceinline__ int64_t prefix_limit(const RowsArgs& a, int64_t r) {
+  return a.causal ? a.n - a.m + r / a.group + 1 : a.n;
+}
+
+// Own tokens that row r (within its sequence) sees: the m query tokens are the cache's last m.
+__device__ __forceinline__ int64_t own_limit(const RowsArgs& a, int64_t len, int64_t r) {
+  const int64_t v = len - a.m + 1 + r / a.group;
+  return v < 0 ? 0 : v;
+}
+
+// Tiles of the prefix segment of row block p (of every KV head).
+__device__ __forceinline__ int64_t prefix_tiles(const RowsArgs& a, int p) {
+  const int64_t last = min64(int64_t(p + 1) * a.rb, a.rows) - 1;
+  return (prefix_limit(a, last) + a.kt - 1) / a.kt;
+}
+
+__device__ __forceinline__ int64_t own_tiles(const RowsArgs& a, int b) { return (own_tokens(a, b) + a.kt - 1) / a.kt; }
+
+__device__ __forceinline__ int64_t warp_sum64(int64_t v) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
+
+// Sum of f(i) over i in [0, n), by one full warp.
+template <typename F> __device__ __forceinline__ int64_t warp_total(int n, F f) {
+  int64_t s = 0;
+  for (int i = threadIdx.x & 31; i < n; i += 32) s += f(i);
+  return warp_sum64(s);
+}
+
+// The totals of the flat tile list, by one full warp.
+struct RowsTotals {
+  int64_t head;    // tiles of one KV head's prefix segments
+  int64_t prefix;  // tiles of all prefix segments
+  int64_t all;
+};
+
+__device__ __forceinline__ RowsTotals rows_totals(const RowsArgs& a) {
+  RowsTotals t;
+  t.head = a.causal ? warp_total(a.pp, [&](int p) { return prefix_tiles(a, p); }) : int64_t(a.pp) * prefix_tiles(a, 0);
+  t.prefix = t.head * a.hkv;
+  t.all = t.prefix + (a.has_own ? int64_t(a.hkv) * a.po * warp_total(a.B, [&](int b) { return own_tiles(a, b); }) : 0);
+  return t;
+}
+
+// First item of the list with lengths f(0..n) that holds position x (0 <= x < total), by one full warp; *base
+// receives the position of the item's first element.
+template <typename F> __device__ __forceinline__ int warp_find(int n, F f, int64_t x, int64_t* base) {
+  const int lane = threadIdx.x & 31;
+  int64_t run = 0;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const int64_t v = i0 + lane < n ? f(i0 + lane) : 0;
+    int64_t inc = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, inc, off);
+      if (lane >= off) inc += y;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, run + inc > x);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      *base = __shfl_sync(0xffffffffu, run + inc - v, src);
+      return i0 + src;
+    }
+    run += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  *base = run;
+  return n;  // not reached for x < total
+}
+
+// A position in the flat list: segment seg, its tiles [first, first + tiles) in the list.
+struct RowsSeg {
+  int own;        // 0: prefix, 1: own
+  int b, h, p;    // sequence (own), KV head, row block
+  int id;         // segment number
+  int64_t first, tiles;
+};
+
+// The segment that holds flat tile x, by one full warp.
+__device__ __forceinline__ RowsSeg rows_find(const RowsArgs& a, const RowsTotals& t, int64_t x) {
+  RowsSeg s;
+  if (x < t.prefix) {
+    s.own = 0;
+    s.b = 0;
+    s.h = int(x / t.head);
+    const int64_t r = x - s.h * t.head;
+    int64_t base;
+    if (a.causal) {
+      s.p = warp_find(a.pp, [&](int p) { return prefix_tiles(a, p); }, r, &base);
+      s.tiles = prefix_tiles(a, s.p);
+    } else {
+      s.tiles = prefix_tiles(a, 0);
+      s.p = int(r / s.tiles);
+      base = s.p * s.tiles;
+    }
+    s.first = s.h * t.head + base;
+    s.id = s.h * a.pp + s.p;
+  } else {
+    s.own = 1;
+    const int64_t per = int64_t(a.hkv) * a.po;
+    int64_t base;
+    s.b = warp_find(a.B, [&](int b) { return own_tiles(a, b) * per; }, x - t.prefix, &base);
+    s.tiles = own_tiles(a, s.b);
+    const int64_t r = x - t.prefix - base;
+    const int u = int(r / s.tiles);
+    s.h = u / a.po;
+    s.p = u - s.h * a.po;
+    s.first = t.prefix + base + int64_t(u) * s.tiles;
+    s.id = a.hkv * a.pp + s.b * int(per) + u;
+  }
+  return s;
+}
+
+__device__ __forceinline__ int64_t cta_first_tile(int64_t total, int nc, int c) { return int64_t(c) * total / nc; }
+
+// CTA that owns flat tile x: the c with c*T/nc <= x < (c+1)*T/nc (rounded down).
+__device__ __forceinline__ int tile_cta(int64_t total, int nc, int64_t x) { return int(((x + 1) * nc - 1) / total); }
+
+// Partial slot of CTA c for a segment.  With own caches every row has several partials: slot c + segment number
+// (unique, since along the list either the CTA or the segment advances).  Without, a segment inside one
+// CTA is written out directly and only the CTA's first and last segments need slots: 2c and 2c + 1.
+// Returns the slot's first row in `part`.
+__device__ __forceinline__ int64_t part_row(const RowsArgs& a, int c, int own, int id, bool first_of_cta) {
+  if (!a.has_own) return (2 * int64_t(c) + (first_of_cta ? 0 : 1)) * a.rp;
+  return own ? a.part_own + (int64_t(c) + id - int64_t(a.hkv) * a.pp) * a.ro : (int64_t(c) + id) * a.rp;
+}
+
+// Index of (sequence, query token, query head) of row r of KV head h in Q, O and lse (times d for Q and O).
+__device__ __forceinline__ int64_t row_index(const RowsArgs& a, int h, int64_t r) {
+  const int64_t t = r / a.group;
+  return t * a.hq + int64_t(h) * a.group + (r - t * a.group);
+}
+
+struct WeightsArgs {
+  const void* K;
+  const void* Q;
+  const float* lse;      // [m][hq]
+  const float* acc_in;   // NULL: zeros
+  float* acc_out;        // [hkv][ld_acc_out]
+  float* sums;           // partial column sums [rsplit][hkv][n] (rsplit > 1)
+  const float* logits;   // [hkv][rows][n] raw dot products (NULL: computed again)
+  int* status;
+  int64_t ld, n, ld_acc_in, ld_acc_out, rows;
+  int m, hq, hkv, group, causal, rsplit;
+  int64_t rows_per_split;  // rows of one split (a multiple of the kernel's row block)
+  float scale;
+};
+
+// Host side: the plan of a call (kernel variant, CTAs, partial rows).
+struct RowsPlan {
+  int rb, kt, nc, pp, po, rp, ro;
+  uint64_t part_rows, part_own;
+};
+void rows_plan(int dtype, int d, int hkv, int group, int64_t B, int64_t m, int64_t n, int64_t ld_own, RowsPlan* p);
+uint64_t rows_part_bound(int dtype, int d, int hkv, int group, int64_t B, int64_t m, int64_t n, int64_t ld_own);
+cudaError_t launch_rows(const RowsArgs& a, int dtype, int d, cudaStream_t st);
+
+struct WeightsPlan {
+  int rsplit;
+  int64_t rows_per_split;
+};
+void weights_plan(int dtype, int d, int hkv, int64_t rows, int64_t n, WeightsPlan* p);
+uint64_t weights_sums_bound(int hkv, int64_t n);
+cudaError_t launch_weights(const WeightsArgs& a, int dtype, int d, cudaStream_t st);
+
+struct EvictArgs {
+  const void* K;
+  const void* V;
+  const float* acc;
+  void* K_out;
+  void* V_out;
+  float* acc_out;
+  int32_t* idx;           // [hkv][keep]
+  int64_t ld, ld_acc, ld_out, ld_acc_out, n, keep, first, last;
+  int hkv, row_bytes;     // bytes of one token's row of K or V
+  int in_place;           // some output is its own input: rows move in order
+};
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st);
+
+}  // namespace zha

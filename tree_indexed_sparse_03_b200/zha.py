@@ -48,6 +48,20 @@ _SIGS = {
                                     _c.c_void_p, _c.c_int32, _c.c_void_p, _c.c_void_p]),
     "zha_dense_decode_noalloc": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int64, _c.c_int64,
                                             _c.c_void_p, _c.c_void_p, _c.c_int32, _c.c_void_p]),
+    "zha_prefix_scratch_bytes": (_c.c_size_t, [_c.c_void_p, _c.c_int32, _c.c_int32, _c.c_int64, _c.c_int64]),
+    "zha_prefix_decode": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int64, _c.c_int64, _c.c_void_p,
+                                     _c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p,
+                                     _c.c_int32, _c.c_int32, _c.c_void_p, _c.c_size_t, _c.c_void_p]),
+    "zha_weights_scratch_bytes": (_c.c_size_t, [_c.c_void_p, _c.c_int32, _c.c_int64]),
+    "zha_dense_weights": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int64, _c.c_int64, _c.c_void_p,
+                                     _c.c_void_p, _c.c_int32, _c.c_int32, _c.c_void_p, _c.c_int64, _c.c_void_p,
+                                     _c.c_int64, _c.c_void_p, _c.c_size_t, _c.c_void_p]),
+    "zha_cache_evict": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int64, _c.c_int64, _c.c_void_p,
+                                   _c.c_int64, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_void_p, _c.c_void_p,
+                                   _c.c_int64, _c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_void_p]),
+    "zha_tree_evict": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_int64,
+                                  _c.c_void_p, _c.c_void_p]),
+    "zha_scratch_status": (_c.c_int, [_c.c_void_p, _c.c_void_p]),
     "zha_tree_status": (_c.c_int, [_c.c_void_p, _c.c_void_p]),
     "zha_tree_set_step_p": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_int32]),
     "zha_tree_destroy": (None, [_c.c_void_p]),
@@ -243,6 +257,20 @@ class ZhaTree:
         _check(lib().zha_decode_step_host(self._h, _ptr(k_host), _ptr(v_host), q_host.data_ptr(), o_host.data_ptr(),
                                           B, _stream(stream)))
 
+    def evict(self, acc: torch.Tensor, keep: int, *, first: int = 0, last: int = 0, stream=None) -> torch.Tensor:
+        """Shorten the cache to `keep` tokens per KV head by the sums acc [Hkv, >= size] (fp32, shortened in place;
+        see cache_evict) and rebuild the tree over them.  Returns the kept tokens' positions [Hkv, keep] int32."""
+        c = self.cfg
+        n = self.size
+        ld_acc = _check_sums("acc", acc, c, n)
+        _check_device(("acc", acc), ("K", self.K))
+        if not 1 <= keep <= n:
+            raise ValueError(f"keep must be in [1, {n}]")
+        idx = _empty((c.n_kv_heads, keep), torch.int32, acc.device, stream)
+        _check(lib().zha_tree_evict(self._h, acc.data_ptr(), ld_acc, keep, first, last, idx.data_ptr(),
+                                    _stream(stream)))
+        return idx
+
     def set_step_p(self, p) -> None:
         """Top-p threshold per routing step (p[s] for step s, the last value for later steps); [] or None
         returns to the configuration's p."""
@@ -316,3 +344,227 @@ class DenseDecoder:
 
 def dense_decode(cfg: ZhaConfig, K: torch.Tensor, V: torch.Tensor, n: int, Q: torch.Tensor, stream=None):
     return DenseDecoder(cfg, Q.shape[0], n, device=Q.device)(K, V, n, Q, stream=stream)
+
+
+# ---------------------------------------------------------------- shared prefix, weights, eviction
+# These entry points take tensors as they lie (row strides included) and never copy them; every tensor must be on
+# the current CUDA device.  Outputs they allocate belong to the stream the call runs on.
+
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _check_device(*named) -> None:
+    dev = torch.cuda.current_device()
+    for name, t in named:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name} must be on the current CUDA device (cuda:{dev})")
+
+
+def _check_cache(name: str, t: torch.Tensor, cfg: ZhaConfig, lead: Tuple[int, ...]) -> int:
+    """Row stride in tokens of a cache tensor [*lead, tokens, d] whose heads may be slices of longer ones."""
+    d, dt = cfg.d, TORCH_DTYPE[cfg.dtype]
+    if t.dtype != dt or not t.is_cuda or t.dim() != len(lead) + 2 or t.shape[:-2] != lead or t.shape[-1] != d:
+        raise ValueError(f"{name} must be a CUDA {dt} tensor {[*lead, 'tokens', d]}")
+    if t.is_contiguous():
+        return t.shape[-2]
+    st = t.stride()
+    ld = st[-3] // d if lead[-1] > 1 else (st[0] // (lead[-1] * d) if len(lead) > 1 and lead[0] > 1 else t.shape[-2])
+    if (st[-1] != 1 or st[-2] != d or ld < t.shape[-2] or (lead[-1] > 1 and st[-3] != ld * d)
+            or (len(lead) > 1 and lead[0] > 1 and st[0] != lead[-1] * ld * d)):
+        raise ValueError(f"{name} must have contiguous rows, one after another, and heads a whole number of rows apart")
+    return ld
+
+
+def _check_sums(name: str, t: torch.Tensor, cfg: ZhaConfig, n: int) -> int:
+    """Row stride of per-token sums [Hkv, >= n] fp32."""
+    if t.dtype != torch.float32 or not t.is_cuda or t.dim() != 2 or t.shape[0] != cfg.n_kv_heads or t.shape[1] < n:
+        raise ValueError(f"{name} must be a CUDA float32 tensor [{cfg.n_kv_heads}, >= {n}]")
+    if t.is_contiguous():
+        return t.shape[1]
+    if t.stride(1) != 1 or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _check_out(name: str, t: torch.Tensor, shape) -> None:
+    if t.shape != shape or t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA float32 tensor {list(shape)}")
+
+
+def _new_scratch(nbytes: int, device) -> torch.Tensor:
+    if nbytes == 0:
+        raise ZhaError(ZHA_ERR_INVALID, lib().zha_last_error().decode())
+    scratch = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+    torch.cuda.current_stream(scratch.device).synchronize()  # cleared before any stream uses it
+    return scratch
+
+
+class PrefixDecoder:
+    """Attention of up to B sequences x m query tokens over a shared prefix of up to n_max tokens and own caches of up
+    to own_max tokens (zha_prefix_decode), with a workspace of its own.
+
+    Calls of one PrefixDecoder must be issued in order on one stream, and graphs captured with one must not replay at
+    the same time: they share its workspace.
+    """
+
+    def __init__(self, cfg: ZhaConfig, B: int, n_max: int, own_max: int = 0, m: int = 1, device="cuda"):
+        self.cfg = cfg
+        self._cfg = ctypes.byref(cfg)
+        self.scratch = _new_scratch(int(lib().zha_prefix_scratch_bytes(self._cfg, B, m, n_max, own_max)), device)
+        self.B, self.m, self.n_max, self.own_max = B, m, n_max, own_max
+
+    def __call__(self, K: Optional[torch.Tensor], V: Optional[torch.Tensor], n: int, Q: torch.Tensor,
+                 K_own: Optional[torch.Tensor] = None, V_own: Optional[torch.Tensor] = None,
+                 own_len: Optional[torch.Tensor] = None, *, out=None, want_lse: bool = False, stream=None):
+        """Q [B, m, Hq, d] (or [B, Hq, d]); K, V [Hkv, >= n, d] (None for n = 0); K_own, V_own [B, Hkv, >= own_len, d]
+        with own_len [B] int32, or all three None.  Returns O fp32 of Q's shape, or (O, lse of Q's shape but d)."""
+        c = self.cfg
+        shape = Q.shape
+        if (Q.dtype != TORCH_DTYPE[c.dtype] or not Q.is_cuda or not Q.is_contiguous() or Q.dim() not in (3, 4)
+                or shape[-1] != c.d or shape[-2] != c.n_q_heads):
+            raise ValueError(f"Q must be a contiguous CUDA {TORCH_DTYPE[c.dtype]} tensor [B, m, {c.n_q_heads}, {c.d}] "
+                             f"or [B, {c.n_q_heads}, {c.d}]")
+        B, m = shape[0], shape[1] if len(shape) == 4 else 1
+        ld = ld_own = 0
+        if n:
+            if K is None or V is None:
+                raise ValueError("n > 0 needs K and V")
+            ld = _check_cache("K", K, c, (c.n_kv_heads,))
+            if _check_cache("V", V, c, (c.n_kv_heads,)) != ld or K.shape != V.shape:
+                raise ValueError("K and V must have the same shape and strides")
+            if not 0 <= n <= K.shape[1]:
+                raise ValueError(f"n must be in [0, {K.shape[1]}]")
+        if K_own is not None and K_own.shape[-2] > 0:
+            if V_own is None or own_len is None:
+                raise ValueError("K_own, V_own and own_len go together")
+            ld_own = _check_cache("K_own", K_own, c, (B, c.n_kv_heads))
+            if _check_cache("V_own", V_own, c, (B, c.n_kv_heads)) != ld_own or K_own.shape != V_own.shape:
+                raise ValueError("K_own and V_own must have the same shape and strides")
+            if ld_own != K_own.shape[-2]:
+                raise ValueError("K_own and V_own must be contiguous: own_len bounds them")
+            if own_len.shape != (B,) or own_len.dtype != torch.int32 or not own_len.is_cuda or not own_len.is_contiguous():
+                raise ValueError(f"own_len must be a contiguous CUDA int32 tensor [{B}]")
+        elif (K_own is None) != (V_own is None) or (K_own is None) != (own_len is None):
+            raise ValueError("K_own, V_own and own_len go together")
+        if B > self.B or m > self.m or n > self.n_max or ld_own > self.own_max:
+            raise ValueError(f"the decoder was made for B <= {self.B}, m <= {self.m}, n <= {self.n_max} and own caches "
+                             f"of at most {self.own_max} tokens")
+        if out is not None:
+            _check_out("out", out, shape)
+        _check_device(("Q", Q), ("K", K), ("V", V), ("K_own", K_own), ("V_own", V_own), ("own_len", own_len),
+                      ("out", out), ("the workspace", self.scratch))
+        O = out if out is not None else _empty(shape, torch.float32, Q.device, stream)
+        lse = _empty(shape[:-1], torch.float32, Q.device, stream) if want_lse else None
+        if Q.numel() == 0:
+            return (O, lse) if want_lse else O
+        own = ld_own > 0
+        _check(lib().zha_prefix_decode(self._cfg, K.data_ptr() if n else None, V.data_ptr() if n else None, ld, n,
+                                       K_own.data_ptr() if own else None, V_own.data_ptr() if own else None, ld_own,
+                                       own_len.data_ptr() if own else None, Q.data_ptr(), O.data_ptr(), _ptr(lse), B, m,
+                                       self.scratch.data_ptr(), self.scratch.numel(), _stream(stream)))
+        return (O, lse) if want_lse else O
+
+    def status(self, stream=None) -> None:
+        _check(lib().zha_scratch_status(self.scratch.data_ptr(), _stream(stream)))
+
+
+def prefix_decode(cfg: ZhaConfig, K, V, n: int, Q: torch.Tensor, K_own=None, V_own=None, own_len=None, *,
+                  want_lse: bool = False, stream=None):
+    """One call of a PrefixDecoder made for it."""
+    dec = PrefixDecoder(cfg, Q.shape[0], n, 0 if K_own is None else K_own.shape[-2], Q.shape[1] if Q.dim() == 4 else 1,
+                        device=Q.device)
+    res = dec(K, V, n, Q, K_own, V_own, own_len, want_lse=want_lse, stream=stream)
+    if stream is not None:
+        dec.scratch.record_stream(stream)
+    return res
+
+
+class DenseWeights:
+    """Dense attention of up to m query tokens over up to n_max tokens that adds up every token's attention weight
+    (zha_dense_weights), with a workspace of its own (as for PrefixDecoder)."""
+
+    def __init__(self, cfg: ZhaConfig, m: int, n_max: int, device="cuda"):
+        self.cfg = cfg
+        self._cfg = ctypes.byref(cfg)
+        self.m, self.n_max = m, n_max
+        self.scratch = _new_scratch(int(lib().zha_weights_scratch_bytes(self._cfg, m, n_max)), device)
+
+    def __call__(self, K: torch.Tensor, V: Optional[torch.Tensor], n: int, Q: torch.Tensor,
+                 acc: Optional[torch.Tensor] = None, *, causal: bool = False, acc_out: Optional[torch.Tensor] = None,
+                 out=None, stream=None):
+        """Q [m, Hq, d]; K, V [Hkv, >= n, d]; acc [Hkv, >= n] fp32 the sums so far (None: zeros).  Returns (O fp32 of
+        Q's shape, acc_out [Hkv, n] = acc + the weights); V None leaves O out (None).  acc_out may be acc."""
+        c = self.cfg
+        if (Q.dtype != TORCH_DTYPE[c.dtype] or not Q.is_cuda or not Q.is_contiguous() or Q.dim() != 3
+                or Q.shape[-1] != c.d or Q.shape[-2] != c.n_q_heads):
+            raise ValueError(f"Q must be a contiguous CUDA {TORCH_DTYPE[c.dtype]} tensor [m, {c.n_q_heads}, {c.d}]")
+        m = Q.shape[0]
+        ld = _check_cache("K", K, c, (c.n_kv_heads,))
+        if V is not None and (_check_cache("V", V, c, (c.n_kv_heads,)) != ld or K.shape != V.shape):
+            raise ValueError("K and V must have the same shape and strides")
+        if not 1 <= n <= K.shape[1]:
+            raise ValueError(f"n must be in [1, {K.shape[1]}]")
+        if not 1 <= m <= self.m or n > self.n_max:
+            raise ValueError(f"the workspace was made for 1 <= m <= {self.m} and n <= {self.n_max}")
+        ld_in = _check_sums("acc", acc, c, n) if acc is not None else 0
+        if acc_out is None:
+            acc_out = _empty((c.n_kv_heads, n), torch.float32, Q.device, stream)
+        ld_out = _check_sums("acc_out", acc_out, c, n)
+        if V is None:
+            if out is not None:
+                raise ValueError("out needs V")
+        elif out is not None:
+            _check_out("out", out, Q.shape)
+        _check_device(("Q", Q), ("K", K), ("V", V), ("acc", acc), ("acc_out", acc_out), ("out", out),
+                      ("the workspace", self.scratch))
+        O = out
+        if V is not None and out is None:
+            O = _empty(Q.shape, torch.float32, Q.device, stream)
+        _check(lib().zha_dense_weights(self._cfg, K.data_ptr(), _ptr(V), ld, n, Q.data_ptr(), _ptr(O), m,
+                                       1 if causal else 0, _ptr(acc), ld_in, acc_out.data_ptr(), ld_out,
+                                       self.scratch.data_ptr(), self.scratch.numel(), _stream(stream)))
+        return O, acc_out
+
+    def status(self, stream=None) -> None:
+        _check(lib().zha_scratch_status(self.scratch.data_ptr(), _stream(stream)))
+
+
+def cache_evict(cfg: ZhaConfig, K: torch.Tensor, V: torch.Tensor, n: int, acc: torch.Tensor, keep: int, *,
+                first: int = 0, last: int = 0, K_out: Optional[torch.Tensor] = None,
+                V_out: Optional[torch.Tensor] = None, acc_out: Optional[torch.Tensor] = None, stream=None):
+    """Shorten a cache K, V [Hkv, >= n, d] to `keep` tokens per head: the first `first`, the last `last` and those with
+    the largest sums acc [Hkv, >= n] between (zha_cache_evict).  K_out and V_out [Hkv, >= keep, d] both None: in
+    place, the sums too unless acc_out is given.  Returns (kept positions [Hkv, keep] int32, acc_out)."""
+    ld = _check_cache("K", K, cfg, (cfg.n_kv_heads,))
+    if _check_cache("V", V, cfg, (cfg.n_kv_heads,)) != ld or K.shape != V.shape:
+        raise ValueError("K and V must have the same shape and strides")
+    if not 1 <= n <= K.shape[1]:
+        raise ValueError(f"n must be in [1, {K.shape[1]}]")
+    if not 1 <= keep <= n:
+        raise ValueError(f"keep must be in [1, {n}]")
+    ld_acc = _check_sums("acc", acc, cfg, n)
+    if (K_out is None) != (V_out is None):
+        raise ValueError("K_out and V_out go together")
+    if K_out is None:
+        K_out, V_out, ld_out = K, V, ld
+        if acc_out is None:
+            acc_out = acc
+    else:
+        ld_out = _check_cache("K_out", K_out, cfg, (cfg.n_kv_heads,))
+        if _check_cache("V_out", V_out, cfg, (cfg.n_kv_heads,)) != ld_out or K_out.shape != V_out.shape:
+            raise ValueError("K_out and V_out must have the same shape and strides")
+        if K_out.shape[1] < keep:
+            raise ValueError(f"K_out and V_out must hold {keep} tokens per head")
+        if acc_out is None:
+            acc_out = _empty((cfg.n_kv_heads, keep), torch.float32, acc.device, stream)
+    ld_acc_out = _check_sums("acc_out", acc_out, cfg, keep)
+    _check_device(("K", K), ("V", V), ("acc", acc), ("K_out", K_out), ("V_out", V_out), ("acc_out", acc_out))
+    idx = _empty((cfg.n_kv_heads, keep), torch.int32, acc.device, stream)
+    _check(lib().zha_cache_evict(ctypes.byref(cfg), K.data_ptr(), V.data_ptr(), ld, n, acc.data_ptr(), ld_acc, keep,
+                                 first, last, K_out.data_ptr(), V_out.data_ptr(), ld_out, acc_out.data_ptr(),
+                                 ld_acc_out, idx.data_ptr(), _stream(stream)))
+    return idx, acc_out
