@@ -606,7 +606,9 @@ static void fill_rows(const zha_config* cfg, const RowsPlan& p, void* scratch, R
   a->part_own = int64_t(p.part_own);
   a->scale = 1.0f / std::sqrt(float(cfg->d));
   a->status = static_cast<int*>(scratch);
+  a->tc = p.tc;
   a->part = reinterpret_cast<float*>(static_cast<char*>(scratch) + kScratchHead);
+  a->part_ml = reinterpret_cast<float2*>(a->part + p.part_rows * cfg->d);
 }
 
 size_t zha_prefix_scratch_bytes(const zha_config* cfg, int32_t B, int32_t m, int64_t n, int64_t ld_own) {

@@ -173,23 +173,17 @@ __global__ void __launch_bounds__(kRowsThreads) rows_scalar_kernel(RowsArgs a) {
       for (int off = 8; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
       if (rl < nrows) {
         const int64_t ri = row_index(a, s.h, row_off + r0 + rl);
-        float* P = whole ? nullptr : a.part + (slot + rl) * (D + 2);
         if (l16 == 0) {
-          if (!whole) {
-            P[0] = m_run[i];
-            P[1] = l;
-          } else if (a.lse) {
-            a.lse[ri] = l > 0.f ? (m_run[i] + log2f(l)) * 0.6931471805599453f : (l == 0.f ? -INFINITY : l);
-          }
+          if (!whole) a.part_ml[slot + rl] = make_float2(m_run[i], l);
+          else if (a.lse) a.lse[ri] = l > 0.f ? (m_run[i] + log2f(l)) * 0.6931471805599453f : (l == 0.f ? -INFINITY : l);
         }
-        if (a.V || s.own) {
+        if (a.O) {
           const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+          float* dst = whole ? a.O + ri * D : a.part + (slot + rl) * D;
 #pragma unroll
-          for (int j = 0; j < CT; ++j) {
-            const int col = l16 * 4 + 16 * (j & ~3) + (j & 3);
-            if (whole) a.O[ri * D + col] = o[i][j] * inv;
-            else P[2 + col] = o[i][j];
-          }
+          for (int j = 0; j < CT; j += 4)
+            *reinterpret_cast<float4*>(dst + l16 * 4 + 16 * j) =
+                make_float4(o[i][j] * inv, o[i][j + 1] * inv, o[i][j + 2] * inv, o[i][j + 3] * inv);
         }
       }
     }
@@ -240,19 +234,23 @@ __global__ void __launch_bounds__(256) rows_combine_kernel(RowsArgs a) {
     }
     if (tiles == 0) continue;
     const int c_lo = tile_cta(tot.all, a.nc, first), c_hi = tile_cta(tot.all, a.nc, first + tiles - 1);
-    if (!a.has_own && c_lo == c_hi) {
+    const int64_t blk_rows = (part ? int64_t(a.m) * a.group : a.rows) - (part ? r % (int64_t(a.m) * a.group) - rl : r - rl);
+    const int subs = a.tc && blk_rows <= 128 ? 2 : 1;  // partials of this row per CTA
+    if (!a.has_own && c_lo == c_hi && subs == 1) {
       direct = true;  // written by its CTA
       continue;
     }
-    for (int c = c_lo + w; c <= c_hi; c += W) {
-      const float* P = a.part + (part_row(a, c, part, id, cta_first_tile(tot.all, a.nc, c) >= first) + rl) * (D + 2);
-      const float m_s = __ldcg(P), l_s = __ldcg(P + 1);
+    for (int q = w; q < (c_hi - c_lo + 1) * subs; q += W) {
+      const int c = c_lo + q / subs;
+      const int64_t pr = part_row(a, c, part, id, cta_first_tile(tot.all, a.nc, c) >= first) + rl +
+                         (q % subs) * ((part ? a.ro : a.rp) / 2);
+      const float2 ml = __ldcg(a.part_ml + pr);
       float v[EL];
 #pragma unroll
-      for (int e = 0; e < EL; ++e) v[e] = a.O ? __ldcg(P + 2 + lane + 32 * e) : 0.f;
-      if (m_s == -INFINITY && l_s == 0.f) continue;  // nothing of this share is visible to the row
-      const float mn = fmaxf(M, m_s), s0 = exp2f(M - mn), s1 = exp2f(m_s - mn);
-      L = L * s0 + l_s * s1;
+      for (int e = 0; e < EL; ++e) v[e] = a.O ? __ldcg(a.part + pr * D + lane + 32 * e) : 0.f;
+      if (ml.x == -INFINITY && ml.y == 0.f) continue;  // nothing of this share is visible to the row
+      const float mn = fmaxf(M, ml.x), s0 = exp2f(M - mn), s1 = exp2f(ml.x - mn);
+      L = L * s0 + ml.y * s1;
 #pragma unroll
       for (int e = 0; e < EL; ++e) o[e] = o[e] * s0 + v[e] * s1;
       M = mn;
@@ -459,6 +457,17 @@ template <typename T, int D> cudaError_t run_weights_rt(const WeightsArgs& a, cu
 
 }  // namespace
 
+// Partial rows of a plan whose row blocks, CTAs and slot rows are set.
+static void plan_parts(int hkv, int64_t B, int64_t ld_own, RowsPlan* p) {
+  if (ld_own > 0) {
+    p->part_own = (uint64_t(p->nc) + uint64_t(hkv) * p->pp) * p->rp;
+    p->part_rows = p->part_own + (uint64_t(p->nc) + uint64_t(B) * hkv * p->po) * p->ro;
+  } else {
+    p->part_own = 0;
+    p->part_rows = 2 * uint64_t(p->nc) * p->rp;
+  }
+}
+
 static void scalar_plan(int d, int rt, int hkv, int64_t B, int64_t rows, int64_t mg, int64_t n, int64_t ld_own,
                         RowsPlan* p) {
   p->kt = kRowsKeys;
@@ -473,18 +482,19 @@ static void scalar_plan(int d, int rt, int hkv, int64_t B, int64_t rows, int64_t
                        double(B) * hkv * p->po * double((ld_own + p->kt - 1) / p->kt);
   const int most = 148 * (per_sm < 1 ? 1 : (per_sm > 4 ? 4 : per_sm));
   p->nc = tiles < 1 ? 1 : (tiles < most ? int(tiles) : most);
-  if (ld_own > 0) {
-    p->part_own = (uint64_t(p->nc) + uint64_t(hkv) * p->pp) * p->rp;
-    p->part_rows = p->part_own + (uint64_t(p->nc) + uint64_t(B) * hkv * p->po) * p->ro;
-  } else {
-    p->part_own = 0;
-    p->part_rows = 2 * uint64_t(p->nc) * p->rp;
-  }
+  p->tc = 0;
+  plan_parts(hkv, B, ld_own, p);
 }
 
 void rows_plan(int dtype, int d, int hkv, int group, int64_t B, int64_t m, int64_t n, int64_t ld_own, RowsPlan* p) {
   const int64_t rows = B * m * group;
-  scalar_plan(d, scalar_rt(d, rows), hkv, B, rows, m * group, n, ld_own, p);
+  if (dtype == ZHA_BF16) {
+    tc_plan(hkv, B, rows, m * group, n, ld_own, p);
+    p->tc = 1;
+    plan_parts(hkv, B, ld_own, p);
+  } else {
+    scalar_plan(d, scalar_rt(d, rows), hkv, B, rows, m * group, n, ld_own, p);
+  }
 }
 
 // Partial rows that cover every call with at most B sequences, m query tokens, n and ld_own tokens.  For one
@@ -494,10 +504,15 @@ uint64_t rows_part_bound(int dtype, int d, int hkv, int group, int64_t B, int64_
   uint64_t most = 0;
   for (int rt = 1; rt <= 8; rt = rt == 1 ? 4 : 2 * rt) {
     const int64_t cap = rt == 1 ? 8 : (rt == 4 && d == 64 ? 32 : rows);  // rows that take this variant
-    if (rt > scalar_rt(d, rows)) break;
+    if (dtype != ZHA_BF16 && rt > scalar_rt(d, rows)) break;
     for (int own = 0; own < 2; ++own) {
       RowsPlan p;
-      scalar_plan(d, rt, hkv, min64(B, cap), min64(rows, cap), min64(mg, cap), n, own ? ld_own : 0, &p);
+      if (dtype == ZHA_BF16) {
+        tc_plan(hkv, B, rows, mg, n, own ? ld_own : 0, &p);
+        plan_parts(hkv, B, own ? ld_own : 0, &p);
+      } else {
+        scalar_plan(d, rt, hkv, min64(B, cap), min64(rows, cap), min64(mg, cap), n, own ? ld_own : 0, &p);
+      }
       if (p.part_rows > most) most = p.part_rows;
     }
   }
@@ -507,7 +522,7 @@ uint64_t rows_part_bound(int dtype, int d, int hkv, int group, int64_t B, int64_
 cudaError_t launch_rows(const RowsArgs& a, int dtype, int d, cudaStream_t st) {
   count_launches(2);
   cudaError_t e;
-  if (dtype == ZHA_BF16) e = d == 128 ? run_rows_rt<__nv_bfloat16, 128>(a, st) : run_rows_rt<__nv_bfloat16, 64>(a, st);
+  if (dtype == ZHA_BF16) e = launch_rows_tc(a, d, st);
   else e = d == 128 ? run_rows_rt<float, 128>(a, st) : run_rows_rt<float, 64>(a, st);
   if (e != cudaSuccess) return e;
   return d == 128 ? run_combine<128>(a, st) : run_combine<64>(a, st);

@@ -29,7 +29,8 @@ struct RowsArgs {
   const void* Q;            // [B][m][hq][d]
   float* O;                 // [B][m][hq][d] (NULL with V)
   float* lse;               // [B][m][hq] natural log, may be NULL
-  float* part;              // partials, (d + 2) floats per row: m, l, o[d]
+  float* part;              // partials: numerators, d floats per row
+  float2* part_ml;          // and (running max in powers of two, running sum) per row
   float* logits;            // NULL, or [hkv][rows][n] raw dot products of the prefix to leave for the weights pass
   int* status;
   int64_t ld, n, ld_own;
@@ -43,6 +44,7 @@ struct RowsArgs {
   int pp, po;               // row blocks of a prefix / an own segment
   int rp, ro;               // rows of a prefix / an own partial slot
   int nc;                   // CTAs
+  int tc;                   // 1: the tensor-core kernel, whose row blocks of at most 128 rows leave two partials
   float scale;              // 1 / sqrt(d)
 };
 
@@ -204,11 +206,13 @@ struct WeightsArgs {
 
 // Host side: the plan of a call (kernel variant, CTAs, partial rows).
 struct RowsPlan {
-  int rb, kt, nc, pp, po, rp, ro;
+  int rb, kt, nc, pp, po, rp, ro, tc;
   uint64_t part_rows, part_own;
 };
 void rows_plan(int dtype, int d, int hkv, int group, int64_t B, int64_t m, int64_t n, int64_t ld_own, RowsPlan* p);
 uint64_t rows_part_bound(int dtype, int d, int hkv, int group, int64_t B, int64_t m, int64_t n, int64_t ld_own);
+void tc_plan(int hkv, int64_t B, int64_t rows, int64_t mg, int64_t n, int64_t ld_own, RowsPlan* p);
+cudaError_t launch_rows_tc(const RowsArgs& a, int d, cudaStream_t st);
 cudaError_t launch_rows(const RowsArgs& a, int dtype, int d, cudaStream_t st);
 
 struct WeightsPlan {
