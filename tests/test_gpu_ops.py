@@ -139,6 +139,24 @@ def test_prefix_lengths_outside_the_cache_are_clamped():
     assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_prefix_workspace_reused_by_smaller_calls(dtype):
+    """Long own caches first, then short ones (fewer tiles than the plan has CTAs for) in the same workspace: nothing
+    that the first call left there is taken up."""
+    hkv, B, d, own = 2, 3, 64, 1024
+    cfg = cfg_of(dtype, d, hkv, 2)
+    Q = rnd(1, B, 1, 4, d, dtype=dtype, scale=2.0)
+    K, V = rnd(2, hkv, 300, d, dtype=dtype), rnd(3, hkv, 300, d, dtype=dtype)
+    Ko, Vo = rnd(4, B, hkv, own, d, dtype=dtype), rnd(5, B, hkv, own, d, dtype=dtype)
+    dec = z.PrefixDecoder(cfg, B, 300, own)
+    for n, lens in ((300, [1024, 900, 1000]), (0, [130, 300, 1]), (5, [1, 0, 257]), (300, [0, 0, 0]), (0, [0, 700, 0])):
+        want, lse = prefix_ref(K, V, n, Q, Ko, Vo, lens)
+        o, l = dec(K.cuda(), V.cuda(), n, Q.cuda(), Ko.cuda(), Vo.cuda(),
+                   torch.tensor(lens, dtype=torch.int32, device="cuda"), want_lse=True)
+        close(o, want, REL * float(V.abs().max()) + 1e-6, f"{n} {lens}")
+        close(l, lse, 3e-5, f"{n} {lens}")
+
+
 def test_prefix_large_logits_and_shifted_rows():
     """Logits of several hundred, one key far above the rest late in the prefix: the running maximum moves."""
     d, n = 128, 3000
@@ -242,6 +260,20 @@ def test_weights(dtype, d, hkv, group, m, n, causal):
     dec.status()
     # the weights of one query head sum to one
     assert abs(float(alone.double().sum()) - m * hkv * group) <= REL * m * hkv * group
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_weights_workspace_reused_and_wide_groups(dtype):
+    """One workspace for calls of many shapes, and more query heads per KV head than a tile has rows."""
+    d, n, group = 64, 1300, 150
+    dec = z.DenseWeights(cfg_of(dtype, d, 1, group), 40, n)
+    K, V = rnd(1, 1, n, d, dtype=dtype), rnd(2, 1, n, d, dtype=dtype)
+    Q = rnd(3, 40, group, d, dtype=dtype, scale=2.0)
+    for m, nn, causal in ((40, 1300, False), (40, 40, True), (1, 1, False), (7, 700, True), (40, 300, True), (2, 257, False)):
+        want_o, want_a = weights_ref(K, V, nn, Q[:m], None, causal)
+        o, a = dec(K.cuda(), V.cuda(), nn, Q[:m].cuda(), causal=causal)
+        close(o, want_o, REL * float(V.abs().max()) + 1e-6, f"{m} {nn}")
+        close(a, want_a, REL * want_a + 1e-6, f"{m} {nn}")
 
 
 def test_weights_graph_and_stream():

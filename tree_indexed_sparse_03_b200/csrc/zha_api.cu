@@ -666,7 +666,7 @@ static int weights_layout(const zha_config* cfg, int32_t m, int64_t n, RowsPlan*
   weights_plan(cfg->dtype, cfg->d, cfg->n_kv_heads, rows, n, wp);
   *lse_off = kScratchHead + rows_part_bytes(cfg, *rp);
   *sums_off = align256(*lse_off + uint64_t(m) * cfg->n_q_heads * 4);
-  *bytes = align256(*sums_off + (wp->rsplit > 1 ? uint64_t(wp->rsplit) * cfg->n_kv_heads * uint64_t(n) * 4 : 0));
+  *bytes = align256(*sums_off + wp->sum_floats * 4);
   return ZHA_OK;
 }
 
@@ -676,7 +676,7 @@ size_t zha_weights_scratch_bytes(const zha_config* cfg, int32_t m, int64_t n) {
   uint64_t lse_off, sums_off, bytes;
   if (weights_layout(cfg, m, n, &rp, &wp, &lse_off, &sums_off, &bytes)) return 0;
   return size_t(kScratchHead + rows_bound_bytes(cfg, 1, m, n, 0) + align256(uint64_t(m) * cfg->n_q_heads * 4) +
-                align256(weights_sums_bound(cfg->n_kv_heads, n) * 4));
+                align256(weights_sums_bound(cfg->dtype, cfg->n_kv_heads, n) * 4));
 }
 
 int zha_dense_weights(const zha_config* cfg, const void* K, const void* V, int64_t ld, int64_t n, const void* Q,

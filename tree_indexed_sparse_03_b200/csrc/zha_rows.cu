@@ -242,6 +242,7 @@ __global__ void __launch_bounds__(256) rows_combine_kernel(RowsArgs a) {
     }
     for (int q = w; q < (c_hi - c_lo + 1) * subs; q += W) {
       const int c = c_lo + q / subs;
+      if (cta_empty(tot.all, a.nc, c)) continue;  // fewer tiles than CTAs
       const int64_t pr = part_row(a, c, part, id, cta_first_tile(tot.all, a.nc, c) >= first) + rl +
                          (q % subs) * ((part ? a.ro : a.rp) / 2);
       const float2 ml = __ldcg(a.part_ml + pr);
@@ -529,6 +530,12 @@ cudaError_t launch_rows(const RowsArgs& a, int dtype, int d, cudaStream_t st) {
 }
 
 void weights_plan(int dtype, int d, int hkv, int64_t rows, int64_t n, WeightsPlan* p) {
+  if (dtype == ZHA_BF16) {
+    p->rsplit = 1;
+    p->rows_per_split = rows;
+    p->sum_floats = weights_tc_floats();
+    return;
+  }
   const int64_t rb = 8 * scalar_rt(d, rows);
   const int64_t ctas = (n + kRowsKeys - 1) / kRowsKeys * hkv, blocks = (rows + rb - 1) / rb;
   int64_t s = (kWeightsCtas + ctas - 1) / ctas;  // a few CTAs per SM
@@ -536,18 +543,19 @@ void weights_plan(int dtype, int d, int hkv, int64_t rows, int64_t n, WeightsPla
   if (s > 64) s = 64;
   p->rows_per_split = (blocks + s - 1) / s * rb;
   p->rsplit = int((rows + p->rows_per_split - 1) / p->rows_per_split);
+  p->sum_floats = p->rsplit > 1 ? uint64_t(p->rsplit) * hkv * uint64_t(n) : 0;
 }
 
 // Floats of column sums that cover every call with at most n tokens: the splits of n' <= n tokens take
 // ceil(kWeightsCtas / ctas) * hkv * n' <= 64 * kWeightsCtas + hkv * n floats.
-uint64_t weights_sums_bound(int hkv, int64_t n) { return uint64_t(kWeightsCtas) * kRowsKeys + uint64_t(hkv) * n; }
+uint64_t weights_sums_bound(int dtype, int hkv, int64_t n) {
+  return dtype == ZHA_BF16 ? weights_tc_floats() : uint64_t(kWeightsCtas) * kRowsKeys + uint64_t(hkv) * n;
+}
 
 cudaError_t launch_weights(const WeightsArgs& a, int dtype, int d, cudaStream_t st) {
-  cudaError_t e;
+  if (dtype == ZHA_BF16) return launch_weights_tc(a, d, st);
   count_launches(a.rsplit > 1 ? 2 : 1);
-  if (dtype == ZHA_BF16)
-    e = d == 128 ? run_weights_rt<__nv_bfloat16, 128>(a, st) : run_weights_rt<__nv_bfloat16, 64>(a, st);
-  else e = d == 128 ? run_weights_rt<float, 128>(a, st) : run_weights_rt<float, 64>(a, st);
+  const cudaError_t e = d == 128 ? run_weights_rt<float, 128>(a, st) : run_weights_rt<float, 64>(a, st);
   if (e != cudaSuccess || a.rsplit <= 1) return e;
   weights_join_kernel<<<dim3(unsigned((a.n + 255) / 256), unsigned(a.hkv)), 256, 0, st>>>(a);
   return cudaGetLastError();

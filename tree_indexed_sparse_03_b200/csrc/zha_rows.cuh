@@ -171,6 +171,11 @@ __device__ __forceinline__ RowsSeg rows_find(const RowsArgs& a, const RowsTotals
 
 __device__ __forceinline__ int64_t cta_first_tile(int64_t total, int nc, int c) { return int64_t(c) * total / nc; }
 
+// Whether CTA c has no tile (more CTAs than tiles): it leaves no partial, whatever lies in its slots.
+__device__ __forceinline__ bool cta_empty(int64_t total, int nc, int c) {
+  return cta_first_tile(total, nc, c) == cta_first_tile(total, nc, c + 1);
+}
+
 // CTA that owns flat tile x: the c with c*T/nc <= x < (c+1)*T/nc (rounded down).
 __device__ __forceinline__ int tile_cta(int64_t total, int nc, int64_t x) { return int(((x + 1) * nc - 1) / total); }
 
@@ -195,7 +200,7 @@ struct WeightsArgs {
   const float* lse;      // [m][hq]
   const float* acc_in;   // NULL: zeros
   float* acc_out;        // [hkv][ld_acc_out]
-  float* sums;           // partial column sums [rsplit][hkv][n] (rsplit > 1)
+  float* sums;           // partial column sums: [rsplit][hkv][n] (rsplit > 1), tensor cores: [CTA][2][256]
   const float* logits;   // [hkv][rows][n] raw dot products (NULL: computed again)
   int* status;
   int64_t ld, n, ld_acc_in, ld_acc_out, rows;
@@ -218,9 +223,12 @@ cudaError_t launch_rows(const RowsArgs& a, int dtype, int d, cudaStream_t st);
 struct WeightsPlan {
   int rsplit;
   int64_t rows_per_split;
+  uint64_t sum_floats;  // partial sums in the scratch
 };
 void weights_plan(int dtype, int d, int hkv, int64_t rows, int64_t n, WeightsPlan* p);
-uint64_t weights_sums_bound(int hkv, int64_t n);
+uint64_t weights_sums_bound(int dtype, int hkv, int64_t n);
+uint64_t weights_tc_floats();
+cudaError_t launch_weights_tc(const WeightsArgs& a, int d, cudaStream_t st);
 cudaError_t launch_weights(const WeightsArgs& a, int dtype, int d, cudaStream_t st);
 
 struct EvictArgs {

@@ -1,0 +1,404 @@
+// Column sums of the softmax weights on the tensor cores (bf16 configurations), the second half of
+// zha_dense_weights: acc_out[h][k] = acc_in[h][k] + sum over rows r of 2^(c q_r.k - lse_r).
+//
+// The products are computed again with keys as the rows: S^T = K Q^T, 128 keys x 128 query rows per
+// product, so that a column sum is one thread's sum over its own accumulator row
+// and no exchange between threads is needed.  Two streams of 128 keys share every
+// tile of query rows; each has two accumulators in tensor memory, so that one tile's product runs under the other's
+// exponentials.  Per tile and stream 512 cycles of products (d = 128) against 1024 of
+// exponentials (16 per cycle and SM): the exponentials bound it for many rows, the second read
+// of K for few.
+//
+// Work split: a segment is 256 keys of one KV head against the row tiles that see
+// them; all row tiles of all segments form one flat list that is cut evenly over
+// the CTAs.  A segment inside one CTA is written out directly, one cut by
+// a CTA border leaves partial sums that weights_tc_join_kernel adds in CTA order.
+//
+// Roles: warps 0-3 and 4-7 the two streams' keys, warp 8 the loads (K pairs, row tiles with their
+// log-sum-exps), warp 9 the products.
+#include <cstring>
+
+#include "zha_rows.cuh"
+#include "zha_tc.cuh"
+
+namespace zha {
+
+constexpr int kWtThreads = 320;
+constexpr int kWtKeys = 256;   // keys per segment
+constexpr int kWtCols = 128;   // query rows per tile (columns of the product)
+constexpr int kWtSlots = 3;    // row tiles in flight
+constexpr int kWtFloats = 148 * 2 * kWtKeys;  // partial sums: two slots per CTA
+
+template <int D> struct WtShape {
+  static constexpr int kHalf = 128 * D * 2;                 // bytes of 128 keys, or of a row tile
+  static constexpr int kSmem = 2 * 2 * kHalf + kWtSlots * kHalf + 1024;
+};
+
+// Geometry of the flat list.  Up to 128 query heads of one KV head: a tile is `tok` whole tokens; more: 128 heads
+// of one token.
+struct WtPlan {
+  int tok, per_tok;    // tokens per tile, or tiles per token
+  int64_t tiles;       // row tiles of all m tokens
+  int64_t segs, full;  // segments per head; of these, the first `full` are seen by every row
+  int64_t head, all;   // list length of one head, of all
+};
+
+__device__ __forceinline__ int64_t wt_first_tile(const WeightsArgs& a, const WtPlan& p, int64_t seg) {
+  if (!a.causal) return 0;
+  const int64_t tok = max64(0, seg * kWtKeys - (a.n - a.m));  // first token that sees the segment's first key
+  return p.tok > 0 ? tok / p.tok : tok * p.per_tok;
+}
+
+__device__ __forceinline__ WtPlan wt_plan(const WeightsArgs& a) {
+  WtPlan p;
+  p.tok = a.group <= kWtCols ? kWtCols / a.group : 0;
+  p.per_tok = a.group <= kWtCols ? 1 : (a.group + kWtCols - 1) / kWtCols;
+  p.tiles = p.tok > 0 ? (a.m + p.tok - 1) / p.tok : int64_t(a.m) * p.per_tok;
+  p.segs = (a.n + kWtKeys - 1) / kWtKeys;
+  p.full = a.causal ? min64(p.segs, (a.n - a.m) / kWtKeys + 1) : p.segs;
+  p.head = p.full * p.tiles +
+           warp_total(int(p.segs - p.full), [&](int i) { return p.tiles - wt_first_tile(a, p, p.full + i); });
+  p.all = p.head * a.hkv;
+  return p;
+}
+
+struct WtSeg {
+  int h;
+  int64_t seg;
+  int64_t first, tiles;  // flat position and number of its tiles
+  int64_t t_first;       // its first row tile
+};
+
+__device__ __forceinline__ WtSeg wt_find(const WeightsArgs& a, const WtPlan& p, int64_t x) {
+  WtSeg s;
+  s.h = int(x / p.head);
+  const int64_t r = x - s.h * p.head;
+  int64_t base;
+  if (r < p.full * p.tiles) {
+    s.seg = r / p.tiles;
+    base = s.seg * p.tiles;
+  } else {
+    const int i = warp_find(int(p.segs - p.full), [&](int q) { return p.tiles - wt_first_tile(a, p, p.full + q); },
+                            r - p.full * p.tiles, &base);
+    s.seg = p.full + i;
+    base += p.full * p.tiles;
+  }
+  s.t_first = wt_first_tile(a, p, s.seg);
+  s.tiles = p.tiles - s.t_first;
+  s.first = s.h * p.head + base;
+  return s;
+}
+
+// Tokens, heads and number of rows of row tile t: column c is token tok0 + c / gw, head g0 + c % gw.
+struct WtTile {
+  int64_t tok0;
+  int g0, gw, cols;
+};
+__device__ __forceinline__ WtTile wt_tile(const WeightsArgs& a, const WtPlan& p, int64_t t) {
+  WtTile w;
+  if (p.tok > 0) {
+    w.tok0 = t * p.tok;
+    w.g0 = 0;
+    w.gw = a.group;
+    w.cols = int(min64(p.tok, a.m - w.tok0)) * a.group;
+  } else {
+    w.tok0 = t / p.per_tok;
+    w.g0 = int(t - w.tok0 * p.per_tok) * kWtCols;
+    w.gw = kWtCols;
+    w.cols = a.group - w.g0 < kWtCols ? a.group - w.g0 : kWtCols;
+  }
+  return w;
+}
+
+// Rows that one copy of a row tile writes.
+__device__ __forceinline__ int wt_box_rows(int group) { return group <= kWtCols ? kWtCols / group * group : kWtCols; }
+
+struct WtMaps {
+  CUtensorMap k, q;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a, const __grid_constant__ WtMaps maps) {
+  using Sh = WtShape<D>;
+  constexpr int NS = kWtSlots, PANELS = D / 64;
+  extern __shared__ uint8_t raw[];
+  __shared__ __align__(8) uint64_t bars[2 * NS + 13];
+  __shared__ __align__(16) float lse2[NS][kWtCols];
+  __shared__ uint32_t tmem_base;
+  __shared__ volatile int gave_up;
+  const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+  const uint32_t k_sm = base, ring = base + 4 * Sh::kHalf;  // K: [pair slot][stream]
+  const uint32_t b0 = smem_u32(bars);
+  auto full = [&](int s) { return b0 + 8 * s; };
+  auto empty = [&](int s) { return b0 + 8 * (NS + s); };
+  auto k_full = [&](int s) { return b0 + 8 * (2 * NS + s); };
+  auto k_empty = [&](int s) { return b0 + 8 * (2 * NS + 2 + s); };
+  auto s_full = [&](int st, int b) { return b0 + 8 * (2 * NS + 4 + 2 * st + b); };
+  auto s_free = [&](int st, int b) { return b0 + 8 * (2 * NS + 8 + 2 * st + b); };
+  const uint32_t done = b0 + 8 * (2 * NS + 12);
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+
+  if (tid == 0) {
+    for (int s = 0; s < NS; ++s) {
+      bar_init(full(s), 2);    // the copy's bytes, the log-sum-exps
+      bar_init(empty(s), 9);   // the products of both streams, and the eight warps that read the log-sum-exps
+    }
+    for (int s = 0; s < 2; ++s) {
+      bar_init(k_full(s), 1);
+      bar_init(k_empty(s), 1);
+      for (int b = 0; b < 2; ++b) {
+        bar_init(s_full(s, b), 1);
+        bar_init(s_free(s, b), 4);
+      }
+    }
+    bar_init(done, 1);
+    gave_up = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  // rows of a tile that no copy writes (heads that do not divide 128) stay zero
+  for (int i = tid; i < NS * Sh::kHalf / 16; i += kWtThreads)
+    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(ring + i * 16), "r"(0) : "memory");
+  fence_async_smem();
+  if (wid == 9) tmem_alloc(smem_u32(&tmem_base), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = tmem_base;
+  const WtPlan plan = wt_plan(a);
+  int64_t x = cta_first_tile(plan.all, gridDim.x, blockIdx.x);
+  const int64_t x_end = cta_first_tile(plan.all, gridDim.x, blockIdx.x + 1);
+
+  if (wid == 8) {  // ---------------------------------------------------------------- loads
+    int slot = 0, ks = 0;
+    uint32_t round = 0, k_round = 0;
+    bool ok = true;
+    const uint32_t tile_bytes = uint32_t(wt_box_rows(a.group)) * D * 2;
+    while (x < x_end && ok) {
+      const WtSeg s = wt_find(a, plan, x);
+      const int64_t t1 = min64(s.first + s.tiles, x_end) - s.first;
+      if (!(ok = bar_wait(k_empty(ks), (k_round & 1) ^ 1, &gave_up))) break;
+      if (lane == 0) {
+        bar_expect(k_full(ks), 2 * Sh::kHalf);
+#pragma unroll
+        for (int st = 0; st < 2; ++st)
+#pragma unroll
+          for (int p = 0; p < PANELS; ++p)
+            tma_load(k_sm + (2 * ks + st) * Sh::kHalf + p * 128 * 128, &maps.k, k_full(ks), p * 64,
+                     int(s.seg * kWtKeys + st * 128), s.h);
+      }
+      if (++ks == 2) {
+        ks = 0;
+        ++k_round;
+      }
+      for (int64_t t = x - s.first; t < t1; ++t) {
+        const WtTile w = wt_tile(a, plan, s.t_first + t);
+        if (!(ok = bar_wait(empty(slot), (round & 1) ^ 1, &gave_up))) break;
+        if (lane == 0) {
+          bar_expect(full(slot), tile_bytes);
+#pragma unroll
+          for (int p = 0; p < PANELS; ++p)
+            tma_load(ring + slot * Sh::kHalf + p * 128 * 128, &maps.q, full(slot), p * 64,
+                     s.h * a.group + w.g0, int(w.tok0));
+        }
+        for (int c = lane; c < kWtCols; c += 32)  // no row: every weight 2^-inf = 0
+          lse2[slot][c] = c < w.cols ? a.lse[(w.tok0 + c / w.gw) * a.hq + int64_t(s.h) * a.group + w.g0 + c % w.gw] *
+                                           1.4426950408889634f
+                                     : INFINITY;
+        __syncwarp();
+        if (lane == 0) bar_arrive(full(slot));
+        if (++slot == NS) {
+          slot = 0;
+          ++round;
+        }
+      }
+      x = s.first + t1;
+    }
+    if (gave_up) {  // copies in flight land before the CTA's shared memory goes away
+      int never = 0;
+      for (int q = 0; q < NS; ++q)
+        if (q < slot || round > 0) bar_wait(full(q), (q < slot ? round : round - 1) & 1, &never);
+      for (int q = 0; q < 2; ++q)
+        if (q < ks || k_round > 0) bar_wait(k_full(q), (q < ks ? k_round : k_round - 1) & 1, &never);
+    }
+  } else if (wid == 9) {  // ---------------------------------------------------------------- products
+    int slot = 0, ks = 0, buf = 0;
+    uint32_t round = 0, k_round = 0, b_round = 0;
+    bool ok = true;
+    while (x < x_end && ok) {
+      const WtSeg s = wt_find(a, plan, x);
+      const int64_t t1 = min64(s.first + s.tiles, x_end) - s.first;
+      ok = bar_wait(k_full(ks), k_round & 1, &gave_up);
+      for (int64_t t = x - s.first; t < t1 && ok; ++t) {
+        const WtTile w = wt_tile(a, plan, s.t_first + t);
+        const uint32_t idesc = mma_idesc((w.cols + 15) / 16 * 16, false);
+        ok = bar_wait(full(slot), round & 1, &gave_up);
+        for (int st = 0; st < 2 && ok; ++st) {
+          if (!(ok = bar_wait(s_free(st, buf), (b_round & 1) ^ 1, &gave_up))) break;
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t k = k_sm + (2 * ks + st) * Sh::kHalf, q = ring + slot * Sh::kHalf;
+#pragma unroll
+            for (int e = 0; e < D / 16; ++e) {
+              const uint32_t off = (e / 4) * (128 * 128) + (e % 4) * 32;
+              mma_ss(tm + st * 256 + buf * 128, mma_desc(k + off, 16), mma_desc(q + off, 16), idesc, e > 0);
+            }
+            mma_commit(s_full(st, buf));
+            if (st == 1) {
+              mma_commit(empty(slot));
+              if (t + 1 == t1) mma_commit(k_empty(ks));
+            }
+          }
+          __syncwarp();
+        }
+        if (++slot == NS) {
+          slot = 0;
+          ++round;
+        }
+        if (++buf == 2) {
+          buf = 0;
+          ++b_round;
+        }
+      }
+      if (++ks == 2) {
+        ks = 0;
+        ++k_round;
+      }
+      x = s.first + t1;
+    }
+    int never = 0;  // nothing of the tensor pipe may be in flight when tensor memory is given back
+    if (lane == 0) mma_commit(done);
+    __syncwarp();
+    bar_wait(done, 0, &never);
+  } else {  // ---------------------------------------------------------------- the streams' keys
+    const int st = wid >> 2, key = tid & 127;
+    const uint32_t lane_base = uint32_t((wid & 3) * 32) << 16;
+    const float c2 = a.scale * 1.4426950408889634f;
+    int slot = 0, buf = 0;
+    uint32_t round = 0, b_round = 0;
+    bool ok = true, first_of_cta = true;
+    while (x < x_end && ok) {
+      const WtSeg s = wt_find(a, plan, x);
+      const int64_t t1 = min64(s.first + s.tiles, x_end) - s.first;
+      const int64_t k = s.seg * kWtKeys + st * 128 + key;
+      const int64_t tok_min = a.causal ? k - (a.n - a.m) : 0;  // first token that sees this key
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int64_t t = x - s.first; t < t1; ++t) {
+        const WtTile w = wt_tile(a, plan, s.t_first + t);
+        // the log-sum-exps come with the tile's own barrier, the products with theirs
+        if (!(ok = bar_wait(full(slot), round & 1, &gave_up))) break;
+        if (!(ok = bar_wait(s_full(st, buf), b_round & 1, &gave_up))) break;
+        tc_fence_after();
+        const int64_t hid = (tok_min - w.tok0) * w.gw;  // columns before this one do not see the key
+        const int c_min = hid < 0 ? 0 : (hid > kWtCols ? kWtCols : int(hid));
+        const bool mask = __any_sync(0xffffffffu, c_min > 0);
+        const uint32_t ts = tm + lane_base + st * 256 + buf * 128;
+        const int chunks = (w.cols + 31) / 32;
+#pragma unroll 1
+        for (int j = 0; j < chunks; ++j) {
+          float v[32];
+          tmem_ld32(ts + 32 * j, v);
+          tmem_wait_ld();
+          const float4* l4 = reinterpret_cast<const float4*>(&lse2[slot][32 * j]);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const float4 l = l4[q];
+            float p[4] = {ex2(fmaf(v[4 * q], c2, -l.x)), ex2(fmaf(v[4 * q + 1], c2, -l.y)),
+                          ex2(fmaf(v[4 * q + 2], c2, -l.z)), ex2(fmaf(v[4 * q + 3], c2, -l.w))};
+            if (mask) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (32 * j + 4 * q + e < c_min) p[e] = 0.f;
+            }
+            if (32 * j + 4 * q + 3 >= w.cols) {  // columns that no product wrote
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (32 * j + 4 * q + e >= w.cols) p[e] = 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[e] += p[e];
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          bar_arrive(s_free(st, buf));
+          bar_arrive(empty(slot));
+        }
+        if (++slot == NS) {
+          slot = 0;
+          ++round;
+        }
+        if (++buf == 2) {
+          buf = 0;
+          ++b_round;
+        }
+      }
+      if (!ok) break;
+      const float total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      if (x == s.first && t1 == s.tiles) {
+        if (k < a.n) a.acc_out[s.h * a.ld_acc_out + k] = (a.acc_in ? a.acc_in[s.h * a.ld_acc_in + k] : 0.f) + total;
+      } else {
+        a.sums[(int64_t(blockIdx.x) * 2 + (first_of_cta ? 0 : 1)) * kWtKeys + st * 128 + key] = total;
+      }
+      first_of_cta = false;
+      x = s.first + t1;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (gave_up && tid == 0) raise_status(a.status, ZHA_ERR_TIMEOUT);
+  if (wid == 9) tmem_free(tm, 512);
+}
+
+// Segments cut by CTA borders: block c joins the one that begins in CTA c and ends in a later one.
+__global__ void __launch_bounds__(kWtKeys) weights_tc_join_kernel(WeightsArgs a) {
+  const WtPlan plan = wt_plan(a);
+  const int nc = gridDim.x, c = blockIdx.x;
+  const int64_t x0 = cta_first_tile(plan.all, nc, c), x1 = cta_first_tile(plan.all, nc, c + 1);
+  if (x0 >= x1) return;
+  const WtSeg s = wt_find(a, plan, x1 - 1);
+  if (s.first < x0 || s.first + s.tiles <= x1) return;
+  const int64_t k = s.seg * kWtKeys + threadIdx.x;
+  if (k >= a.n) return;
+  const int last = tile_cta(plan.all, nc, s.first + s.tiles - 1);
+  float sum = 0.f;
+  for (int q = c; q <= last; ++q)  // it is every later CTA's first segment
+    if (!cta_empty(plan.all, nc, q)) sum += a.sums[(int64_t(q) * 2 + (q > c || s.first == x0 ? 0 : 1)) * kWtKeys + threadIdx.x];
+  a.acc_out[s.h * a.ld_acc_out + k] = (a.acc_in ? a.acc_in[s.h * a.ld_acc_in + k] : 0.f) + sum;
+}
+
+// ------------------------------------------------------------------ host side
+namespace {
+
+template <int D> cudaError_t run_weights_tc(const WeightsArgs& a, const WtMaps& maps, int nc, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(weights_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       WtShape<D>::kSmem);
+  if (e != cudaSuccess) return e;
+  weights_tc_kernel<D><<<nc, kWtThreads, WtShape<D>::kSmem, st>>>(a, maps);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  weights_tc_join_kernel<<<nc, kWtKeys, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+uint64_t weights_tc_floats() { return kWtFloats; }
+
+cudaError_t launch_weights_tc(const WeightsArgs& a, int d, cudaStream_t st) {
+  WtMaps maps;
+  std::memset(&maps, 0, sizeof(maps));
+  cudaError_t e = make_rows_map(&maps.k, a.K, d, a.n, a.ld, a.hkv, 128, 1);
+  // row tiles: `group` heads of 128 / group tokens, or 128 heads of one token
+  if (e == cudaSuccess)
+    e = make_rows_map(&maps.q, a.Q, d, a.hq, a.hq, a.m, a.group <= kWtCols ? a.group : kWtCols,
+                      a.group <= kWtCols ? kWtCols / a.group : 1);
+  if (e != cudaSuccess) return e;
+  const int64_t segs = (a.n + kWtKeys - 1) / kWtKeys * a.hkv;
+  const int64_t tiles = a.group <= kWtCols ? (a.m + kWtCols / a.group - 1) / (kWtCols / a.group)
+                                           : int64_t(a.m) * ((a.group + kWtCols - 1) / kWtCols);
+  const int nc = int(min64(148, segs * tiles));
+  count_launches(2);
+  return d == 128 ? run_weights_tc<128>(a, maps, nc, st) : run_weights_tc<64>(a, maps, nc, st);
+}
+
+}  // namespace zha
