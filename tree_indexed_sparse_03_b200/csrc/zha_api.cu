@@ -582,17 +582,25 @@ static int prefix_plan(const zha_config* cfg, int32_t B, int32_t m, int64_t n, i
   return ZHA_OK;
 }
 
-static uint64_t rows_part_bytes(const zha_config* cfg, const RowsPlan& p) {
-  return align256(p.part_rows * uint64_t(cfg->d + 2) * 4);
+// The tile list's words: row blocks of at least 8 rows.
+static uint64_t rows_plan_bytes(const zha_config* cfg, int64_t B, int64_t m) {
+  const int64_t rows = B * m * (cfg->n_q_heads / cfg->n_kv_heads);
+  return align256(uint64_t(rows_plan_words(int((rows + 7) / 8), int(B))) * 8);
+}
+
+static uint64_t rows_part_bytes(const zha_config* cfg, int64_t B, int64_t m, const RowsPlan& p) {
+  return rows_plan_bytes(cfg, B, m) + align256(p.part_rows * uint64_t(cfg->d + 2) * 4);
 }
 
 static uint64_t rows_bound_bytes(const zha_config* cfg, int64_t B, int64_t m, int64_t n, int64_t ld_own) {
-  return align256(rows_part_bound(cfg->dtype, cfg->d, cfg->n_kv_heads, cfg->n_q_heads / cfg->n_kv_heads, B, m, n,
+  return rows_plan_bytes(cfg, B, m) + align256(rows_part_bound(cfg->dtype, cfg->d, cfg->n_kv_heads, cfg->n_q_heads / cfg->n_kv_heads, B, m, n,
                                   ld_own) * uint64_t(cfg->d + 2) * 4);
 }
 
-static void fill_rows(const zha_config* cfg, const RowsPlan& p, void* scratch, RowsArgs* a) {
+static void fill_rows(const zha_config* cfg, const RowsPlan& p, int32_t B, int32_t m, void* scratch, RowsArgs* a) {
   std::memset(a, 0, sizeof(*a));
+  a->B = B;
+  a->m = m;
   a->hq = cfg->n_q_heads;
   a->hkv = cfg->n_kv_heads;
   a->group = cfg->n_q_heads / cfg->n_kv_heads;
@@ -607,7 +615,8 @@ static void fill_rows(const zha_config* cfg, const RowsPlan& p, void* scratch, R
   a->scale = 1.0f / std::sqrt(float(cfg->d));
   a->status = static_cast<int*>(scratch);
   a->tc = p.tc;
-  a->part = reinterpret_cast<float*>(static_cast<char*>(scratch) + kScratchHead);
+  a->plan = reinterpret_cast<int64_t*>(static_cast<char*>(scratch) + kScratchHead);
+  a->part = reinterpret_cast<float*>(static_cast<char*>(scratch) + kScratchHead + rows_plan_bytes(cfg, B, m));
   a->part_ml = reinterpret_cast<float2*>(a->part + p.part_rows * cfg->d);
 }
 
@@ -632,10 +641,10 @@ int zha_prefix_decode(const zha_config* cfg, const void* K, const void* V, int64
       !aligned(O, 16) || !aligned(lse, 4) || !aligned(own_len, 4))
     return fail(ZHA_ERR_INVALID, "K, V, K_own, V_own, Q and O must be 16-byte aligned, lse and own_len 4-byte");
   if (!aligned(scratch, 256)) return fail(ZHA_ERR_INVALID, "scratch must be 256-byte aligned");
-  if (scratch_bytes < kScratchHead + rows_part_bytes(cfg, p))
+  if (scratch_bytes < kScratchHead + rows_part_bytes(cfg, B, m, p))
     return fail(ZHA_ERR_CAPACITY, "scratch is smaller than zha_prefix_scratch_bytes");
   RowsArgs a;
-  fill_rows(cfg, p, scratch, &a);
+  fill_rows(cfg, p, B, m, scratch, &a);
   a.K = K;
   a.V = V;
   a.Ko = K_own;
@@ -647,9 +656,7 @@ int zha_prefix_decode(const zha_config* cfg, const void* K, const void* V, int64
   a.ld = ld;
   a.n = n;
   a.ld_own = ld_own;
-  a.B = B;
-  a.m = m;
-  a.rows = int64_t(B) * m * a.group;
+  a.rows = B * m * a.group;
   a.has_own = ld_own > 0 ? 1 : 0;
   cudaError_t e = launch_rows(a, cfg->dtype, cfg->d, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail_cuda(e, "zha_prefix_decode");
@@ -664,7 +671,7 @@ static int weights_layout(const zha_config* cfg, int32_t m, int64_t n, RowsPlan*
   if (n < 1) return fail(ZHA_ERR_INVALID, "n must be >= 1");
   const int64_t rows = int64_t(m) * (cfg->n_q_heads / cfg->n_kv_heads);
   weights_plan(cfg->dtype, cfg->d, cfg->n_kv_heads, rows, n, wp);
-  *lse_off = kScratchHead + rows_part_bytes(cfg, *rp);
+  *lse_off = kScratchHead + rows_part_bytes(cfg, 1, m, *rp);
   *sums_off = align256(*lse_off + uint64_t(m) * cfg->n_q_heads * 4);
   *bytes = align256(*sums_off + wp->sum_floats * 4);
   return ZHA_OK;
@@ -703,7 +710,7 @@ int zha_dense_weights(const zha_config* cfg, const void* K, const void* V, int64
   if (!aligned(scratch, 256)) return fail(ZHA_ERR_INVALID, "scratch must be 256-byte aligned");
   if (scratch_bytes < bytes) return fail(ZHA_ERR_CAPACITY, "scratch is smaller than zha_weights_scratch_bytes");
   RowsArgs a;
-  fill_rows(cfg, rp, scratch, &a);
+  fill_rows(cfg, rp, 1, m, scratch, &a);
   a.K = K;
   a.V = V;
   a.Q = Q;
@@ -711,9 +718,7 @@ int zha_dense_weights(const zha_config* cfg, const void* K, const void* V, int64
   a.lse = reinterpret_cast<float*>(static_cast<char*>(scratch) + lse_off);
   a.ld = ld;
   a.n = n;
-  a.B = 1;
-  a.m = m;
-  a.rows = int64_t(m) * a.group;
+  a.rows = m * a.group;
   a.causal = causal;
   WeightsArgs w;
   std::memset(&w, 0, sizeof(w));

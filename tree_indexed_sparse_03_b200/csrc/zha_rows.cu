@@ -30,16 +30,18 @@ __global__ void __launch_bounds__(kRowsThreads) rows_scalar_kernel(RowsArgs a) {
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int half = wid * 2 + (lane >> 4), l16 = lane & 15;
   const float c2 = a.scale * 1.4426950408889634f;  // weights as powers of two
+  pdl_trigger();
   const RowsTotals tot = rows_totals(a);
+  if (blockIdx.x == 0 && wid == 0) rows_publish(a, tot);
   int64_t x = cta_first_tile(tot.all, a.nc, blockIdx.x);
   const int64_t x_end = cta_first_tile(tot.all, a.nc, blockIdx.x + 1);
   bool first_of_cta = true;
   while (x < x_end) {
     const RowsSeg s = rows_find(a, tot, x);
-    const int64_t seg_rows = s.own ? int64_t(a.m) * a.group : a.rows;
-    const int64_t r0 = int64_t(s.p) * RB;
-    const int nrows = int(min64(RB, seg_rows - r0));
-    const int64_t row_off = s.own ? int64_t(s.b) * a.m * a.group : 0;  // the sequence's first row of the head
+    const int seg_rows = s.own ? a.m * a.group : a.rows;
+    const int r0 = s.p * RB;
+    const int nrows = min(RB, seg_rows - r0);
+    const int row_off = s.own ? s.b * a.m * a.group : 0;  // the sequence's first row of the head
     const int64_t len = s.own ? own_tokens(a, s.b) : a.n;
     const T* Kh = s.own ? static_cast<const T*>(a.Ko) + (int64_t(s.b) * a.hkv + s.h) * a.ld_own * D
                         : static_cast<const T*>(a.K) + int64_t(s.h) * a.ld * D;
@@ -62,7 +64,7 @@ __global__ void __launch_bounds__(kRowsThreads) rows_scalar_kernel(RowsArgs a) {
     float m_run[RT], l_run[RT], o[RT][CT];
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
-      const int64_t r = r0 + half * RT + i;
+      const int r = r0 + half * RT + i;
       lim[i] = r >= seg_rows ? 0 : (s.own ? own_limit(a, len, r) : prefix_limit(a, r));
       m_run[i] = -INFINITY;
       l_run[i] = 0.f;
@@ -200,50 +202,50 @@ template <int D, int W>
 __global__ void __launch_bounds__(256) rows_combine_kernel(RowsArgs a) {
   constexpr int EL = D / 32;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  const int64_t item = int64_t(blockIdx.x) * (8 / W) + wid / W;  // row of all heads
+  const int h = blockIdx.y, r = int(blockIdx.x) * (8 / W) + wid / W;  // KV head, row
   const int w = wid % W;
-  const int64_t total_rows = a.rows * a.hkv;
-  const bool live = item < total_rows;
-  const int h = live ? int(item / a.rows) : 0;
-  const int64_t r = live ? item - int64_t(h) * a.rows : 0;
-  const RowsTotals tot = rows_totals(a);
+  const bool live = r < a.rows;
+  pdl_trigger();
+  pdl_wait();
   float M = -INFINITY, L = 0.f, o[EL];
 #pragma unroll
   for (int e = 0; e < EL; ++e) o[e] = 0.f;
   bool direct = false;
+  const int64_t all = a.plan[0], head = a.plan[1], prefix = a.plan[2];
   for (int part = 0; part < (a.has_own ? 2 : 1) && live; ++part) {
     int64_t first, tiles;
-    int id;
-    int64_t rl;
+    int id, rl, left;  // segment, row within its block, rows from the block's first on
     if (part == 0) {
-      const int p = int(r / a.rb);
-      rl = r - int64_t(p) * a.rb;
-      tiles = prefix_tiles(a, p);
-      first = int64_t(h) * tot.head + (a.causal ? warp_total(p, [&](int q) { return prefix_tiles(a, q); }) : p * tiles);
+      const int p = r / a.rb;
+      rl = r - p * a.rb;
+      left = a.rows - p * a.rb;
+      first = a.plan[3 + p];
+      tiles = a.plan[4 + p] - first;
+      first += h * head;
       id = h * a.pp + p;
     } else {
-      const int64_t mg = int64_t(a.m) * a.group;
-      const int b = int(r / mg);
-      const int64_t rs = r - b * mg;
-      const int p = int(rs / a.rb);
-      rl = rs - int64_t(p) * a.rb;
-      tiles = own_tiles(a, b);
+      const int mg = a.m * a.group;
+      const int b = r / mg, rs = r - b * mg;
+      const int p = rs / a.rb;
+      rl = rs - p * a.rb;
+      left = mg - p * a.rb;
+      const int64_t base = a.plan[4 + a.pp + b];
+      tiles = a.plan[5 + a.pp + b] - base;
       const int u = h * a.po + p;
-      first = tot.prefix + int64_t(a.hkv) * a.po * warp_total(b, [&](int q) { return own_tiles(a, q); }) + u * tiles;
+      first = prefix + base * (a.hkv * a.po) + u * tiles;
       id = a.hkv * a.pp + b * a.hkv * a.po + u;
     }
     if (tiles == 0) continue;
-    const int c_lo = tile_cta(tot.all, a.nc, first), c_hi = tile_cta(tot.all, a.nc, first + tiles - 1);
-    const int64_t blk_rows = (part ? int64_t(a.m) * a.group : a.rows) - (part ? r % (int64_t(a.m) * a.group) - rl : r - rl);
-    const int subs = a.tc && blk_rows <= 128 ? 2 : 1;  // partials of this row per CTA
+    const int c_lo = tile_cta(all, a.nc, first), c_hi = tile_cta(all, a.nc, first + tiles - 1);
+    const int subs = a.tc && left <= 128 ? 2 : 1;  // partials of this row per CTA
     if (!a.has_own && c_lo == c_hi && subs == 1) {
       direct = true;  // written by its CTA
       continue;
     }
     for (int q = w; q < (c_hi - c_lo + 1) * subs; q += W) {
       const int c = c_lo + q / subs;
-      if (cta_empty(tot.all, a.nc, c)) continue;  // fewer tiles than CTAs
-      const int64_t pr = part_row(a, c, part, id, cta_first_tile(tot.all, a.nc, c) >= first) + rl +
+      if (cta_empty(all, a.nc, c)) continue;  // fewer tiles than CTAs
+      const int64_t pr = part_row(a, c, part, id, cta_first_tile(all, a.nc, c) >= first) + rl +
                          (q % subs) * ((part ? a.ro : a.rp) / 2);
       const float2 ml = __ldcg(a.part_ml + pr);
       float v[EL];
@@ -305,6 +307,8 @@ __global__ void __launch_bounds__(kRowsThreads) weights_scalar_kernel(WeightsArg
   const float c2 = a.scale * 1.4426950408889634f;
   const int64_t k0 = int64_t(blockIdx.x) * kRowsKeys;
   const int h = blockIdx.y;
+  pdl_trigger();
+  pdl_wait();
   const T* Kh = static_cast<const T*>(a.K) + int64_t(h) * a.ld * D;
   for (int i = tid; i < kRowsKeys * CPR; i += kRowsThreads) {
     const int r = i / CPR, c = i % CPR;
@@ -317,22 +321,23 @@ __global__ void __launch_bounds__(kRowsThreads) weights_scalar_kernel(WeightsArg
       *reinterpret_cast<float4*>(sk + r * LD + c * EPC + e) = make_float4(k[e], k[e + 1], k[e + 2], k[e + 3]);
   }
   float sum[4] = {0.f, 0.f, 0.f, 0.f};
-  const int64_t rend = min64(a.rows, int64_t(blockIdx.z + 1) * a.rows_per_split);
-  int64_t rbeg = int64_t(blockIdx.z) * a.rows_per_split;
+  const int rend = int(min64(a.rows, int64_t(blockIdx.z + 1) * a.rows_per_split));
+  int rbeg = int(int64_t(blockIdx.z) * a.rows_per_split);
   if (a.causal) {  // rows before the first that sees this tile's first key
-    const int64_t first = max64(0, k0 - (a.n - a.m)) * a.group;
+    const int first = int(max64(0, k0 - (a.n - a.m))) * a.group;
     if (first > rbeg) rbeg = first / RB * RB;
   }
-  for (int64_t r0 = rbeg; r0 < rend; r0 += RB) {
+  for (int r0 = rbeg; r0 < rend; r0 += RB) {
     __syncthreads();
     for (int i = tid; i < RB * CPR; i += kRowsThreads) {
       const int r = i / CPR, c = i % CPR;
       float v[EPC];
 #pragma unroll
       for (int e = 0; e < EPC; ++e) v[e] = 0.f;
-      const int64_t rr = r0 + r;
+      const int rr = r0 + r;
       if (rr < rend) {
-        const int64_t t = rr / a.group, ri = t * a.hq + int64_t(h) * a.group + (rr - t * a.group);
+        const int t = rr / a.group;
+        const int64_t ri = int64_t(t) * a.hq + h * a.group + (rr - t * a.group);
         unpack16<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(a.Q) + ri * D + c * EPC), v);
         if (c == 0) sl[r] = a.lse[ri] * 1.4426950408889634f;
       } else if (c == 0) {
@@ -365,7 +370,7 @@ __global__ void __launch_bounds__(kRowsThreads) weights_scalar_kernel(WeightsArg
     }
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
-      const int64_t rr = r0 + half * RT + i;
+      const int rr = r0 + half * RT + i;
       const int64_t lim = a.causal ? a.n - a.m + rr / a.group + 1 : a.n;
       const float ls = sl[half * RT + i];
 #pragma unroll
@@ -394,6 +399,7 @@ __global__ void __launch_bounds__(kRowsThreads) weights_scalar_kernel(WeightsArg
 __global__ void __launch_bounds__(256) weights_join_kernel(WeightsArgs a) {
   const int64_t k = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
   const int h = blockIdx.y;
+  pdl_wait();
   if (k >= a.n) return;
   float s = 0.f;
   for (int z = 0; z < a.rsplit; ++z) s += a.sums[(int64_t(z) * a.hkv + h) * a.n + k];
@@ -410,10 +416,6 @@ size_t rows_smem(int d, int rt) {
 }
 
 size_t weights_smem(int d, int rt) { return size_t(8 * rt * (d + 4) + kRowsKeys * (d + 4) + 8 * rt) * sizeof(float); }
-
-template <typename K> cudaError_t allow_smem(K kernel, size_t bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
-}
 
 template <typename T, int D, int RT> cudaError_t run_rows(const RowsArgs& a, cudaStream_t st) {
   const size_t sm = rows_smem(D, RT);
@@ -432,11 +434,9 @@ template <typename T, int D> cudaError_t run_rows_rt(const RowsArgs& a, cudaStre
 }
 
 template <int D> cudaError_t run_combine(const RowsArgs& a, cudaStream_t st) {
-  const int64_t rows = a.rows * a.hkv;
-  // few rows: eight warps share a row's partials (up to one per CTA); many rows have few partials each
-  if (rows < 2048) rows_combine_kernel<D, 8><<<unsigned(rows), 256, 0, st>>>(a);
-  else rows_combine_kernel<D, 1><<<unsigned((rows + 7) / 8), 256, 0, st>>>(a);
-  return cudaGetLastError();
+  // few rows: eight warps share a row's partials (up to two per CTA); many rows have few partials each
+  if (a.rows * a.hkv < 2048) return launch_after(rows_combine_kernel<D, 8>, dim3(a.rows, a.hkv), 256, 0, st, a);
+  return launch_after(rows_combine_kernel<D, 1>, dim3((a.rows + 7) / 8, a.hkv), 256, 0, st, a);
 }
 
 template <typename T, int D, int RT> cudaError_t run_weights(const WeightsArgs& a, cudaStream_t st) {
@@ -444,8 +444,7 @@ template <typename T, int D, int RT> cudaError_t run_weights(const WeightsArgs& 
   cudaError_t e = allow_smem(weights_scalar_kernel<T, D, RT>, sm);
   if (e != cudaSuccess) return e;
   const dim3 grid(unsigned((a.n + kRowsKeys - 1) / kRowsKeys), unsigned(a.hkv), unsigned(a.rsplit));
-  weights_scalar_kernel<T, D, RT><<<grid, kRowsThreads, sm, st>>>(a);
-  return cudaGetLastError();
+  return launch_after(weights_scalar_kernel<T, D, RT>, grid, kRowsThreads, sm, st, a);
 }
 
 template <typename T, int D> cudaError_t run_weights_rt(const WeightsArgs& a, cudaStream_t st) {
@@ -557,8 +556,7 @@ cudaError_t launch_weights(const WeightsArgs& a, int dtype, int d, cudaStream_t 
   count_launches(a.rsplit > 1 ? 2 : 1);
   const cudaError_t e = d == 128 ? run_weights_rt<float, 128>(a, st) : run_weights_rt<float, 64>(a, st);
   if (e != cudaSuccess || a.rsplit <= 1) return e;
-  weights_join_kernel<<<dim3(unsigned((a.n + 255) / 256), unsigned(a.hkv)), 256, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_after(weights_join_kernel, dim3(unsigned((a.n + 255) / 256), unsigned(a.hkv)), 256, 0, st, a);
 }
 
 }  // namespace zha

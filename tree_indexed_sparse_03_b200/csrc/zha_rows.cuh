@@ -16,6 +16,8 @@
 // numerator) per segment it touches; rows_combine_kernel joins them in CTA order.
 #pragma once
 
+#include <atomic>
+
 #include "zha_args.cuh"
 
 namespace zha {
@@ -33,8 +35,10 @@ struct RowsArgs {
   float2* part_ml;          // and (running max in powers of two, running sum) per row
   float* logits;            // NULL, or [hkv][rows][n] raw dot products of the prefix to leave for the weights pass
   int* status;
+  int64_t* plan;            // the tile list as the attention kernel's first CTA found it, for the join:
+                            // totals, then rows_plan_words() - see rows_publish
   int64_t ld, n, ld_own;
-  int64_t rows;             // rows per KV head over the prefix: B * m * group
+  int rows;                 // rows per KV head over the prefix: B * m * group
   int64_t part_own;         // first own slot's offset in `part`, in rows
   int B, m, hq, hkv, group;
   int causal;               // 1: query i sees prefix tokens [0, n - m + i] (B = 1)
@@ -55,19 +59,19 @@ __device__ __forceinline__ int64_t own_tokens(const RowsArgs& a, int b) {
 }
 
 // Keys of the prefix that row r of a KV head sees (causal: its query token's position + 1).
-__device__ __forceinline__ int64_t prefix_limit(const RowsArgs& a, int64_t r) {
+__device__ __forceinline__ int64_t prefix_limit(const RowsArgs& a, int r) {
   return a.causal ? a.n - a.m + r / a.group + 1 : a.n;
 }
 
 // Own tokens that row r (within its sequence) sees: the m query tokens are the cache's last m.
-__device__ __forceinline__ int64_t own_limit(const RowsArgs& a, int64_t len, int64_t r) {
+__device__ __forceinline__ int64_t own_limit(const RowsArgs& a, int64_t len, int r) {
   const int64_t v = len - a.m + 1 + r / a.group;
   return v < 0 ? 0 : v;
 }
 
 // Tiles of the prefix segment of row block p (of every KV head).
 __device__ __forceinline__ int64_t prefix_tiles(const RowsArgs& a, int p) {
-  const int64_t last = min64(int64_t(p + 1) * a.rb, a.rows) - 1;
+  const int last = min((p + 1) * a.rb, a.rows) - 1;
   return (prefix_limit(a, last) + a.kt - 1) / a.kt;
 }
 
@@ -189,9 +193,73 @@ __device__ __forceinline__ int64_t part_row(const RowsArgs& a, int c, int own, i
 }
 
 // Index of (sequence, query token, query head) of row r of KV head h in Q, O and lse (times d for Q and O).
-__device__ __forceinline__ int64_t row_index(const RowsArgs& a, int h, int64_t r) {
-  const int64_t t = r / a.group;
-  return t * a.hq + int64_t(h) * a.group + (r - t * a.group);
+__device__ __forceinline__ int64_t row_index(const RowsArgs& a, int h, int r) {
+  const int t = r / a.group;
+  return int64_t(t) * a.hq + h * a.group + (r - t * a.group);
+}
+
+// The list's layout for the join, written once by one warp of the first CTA: totals, then the first tile of every
+// row block of a head and of every sequence's own segments (both with their end).
+__host__ __device__ __forceinline__ int64_t rows_plan_words(int pp, int B) { return 3 + pp + 1 + B + 1; }
+
+template <typename F> __device__ __forceinline__ void warp_prefix(int n, F f, int64_t* out) {
+  const int lane = threadIdx.x & 31;
+  int64_t run = 0;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const int64_t v = i0 + lane < n ? f(i0 + lane) : 0;
+    int64_t inc = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, inc, off);
+      if (lane >= off) inc += y;
+    }
+    if (i0 + lane < n) out[i0 + lane] = run + inc - v;
+    run += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  if (lane == 0) out[n] = run;
+}
+
+__device__ __forceinline__ void rows_publish(const RowsArgs& a, const RowsTotals& t) {
+  if ((threadIdx.x & 31) == 0) {
+    a.plan[0] = t.all;
+    a.plan[1] = t.head;
+    a.plan[2] = t.prefix;
+  }
+  warp_prefix(a.pp, [&](int p) { return prefix_tiles(a, p); }, a.plan + 3);
+  if (a.has_own) warp_prefix(a.B, [&](int b) { return own_tiles(a, b); }, a.plan + 4 + a.pp);
+}
+
+// Launch of a kernel that may start while its predecessor in the stream still runs; it waits with pdl_wait() before
+// it reads anything that the predecessor wrote.  pdl_trigger() in the predecessor lets it start.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Dynamic shared memory above 48 KB, allowed once per kernel and device.
+template <typename... P> cudaError_t allow_smem(void (*kernel)(P...), size_t bytes) {
+  static std::atomic<const void*> done[kMaxDevices];  // per kernel type and device: the last kernel allowed
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || dev < 0 || dev >= kMaxDevices) return e != cudaSuccess ? e : cudaErrorInvalidDevice;
+  const void* k = reinterpret_cast<const void*>(kernel);
+  if (done[dev].load(std::memory_order_relaxed) == k) return cudaSuccess;
+  e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+  if (e == cudaSuccess) done[dev].store(k, std::memory_order_relaxed);
+  return e;
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, args...);
 }
 
 struct WeightsArgs {
@@ -203,7 +271,8 @@ struct WeightsArgs {
   float* sums;           // partial column sums: [rsplit][hkv][n] (rsplit > 1), tensor cores: [CTA][2][256]
   const float* logits;   // [hkv][rows][n] raw dot products (NULL: computed again)
   int* status;
-  int64_t ld, n, ld_acc_in, ld_acc_out, rows;
+  int64_t ld, n, ld_acc_in, ld_acc_out;
+  int rows;              // m * group
   int m, hq, hkv, group, causal, rsplit;
   int64_t rows_per_split;  // rows of one split (a multiple of the kernel's row block)
   float scale;

@@ -20,7 +20,8 @@
 // weights stay below 2^8 and the usual tile rescales nothing.
 //
 // Roles: warps 0-3 and 4-7 the two streams' rows, warp 8 the TMA loads into a ring of K / V
-// tiles, warp 9 issues the products.  Order of the products per stream: P V of the previous tile, then
+// tiles, warp 9 issues the products.  A row's 128 logits stay in one thread's registers, so the streams' warps take
+// registers over from the others.  Order of the products per stream: P V of the previous tile, then
 // S of the next; a commit after S therefore also says that the earlier P V is complete.
 #include <cstring>
 
@@ -30,7 +31,8 @@
 namespace zha {
 
 constexpr int kTcKeys = 128;               // keys per tile
-constexpr int kTcThreads = 320;
+constexpr int kTcThreads = 384;            // three warpgroups, the third one's last two warps idle
+constexpr int kRowRegs = 224, kFewRegs = 56;  // registers a thread: 2 * 128 * 224 + 128 * 56 = 384 * 168, the launch's own
 constexpr int kTcRows = 256;               // rows of a row block: two streams of 128
 constexpr float kLazyMax = 8.f;            // growth of the maximum (log2) that rescales O
 
@@ -50,7 +52,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
   using Sh = TcShape<D>;
   constexpr int NS = Sh::kSlots, PANELS = D / 64;
   extern __shared__ uint8_t raw[];
-  __shared__ __align__(8) uint64_t bars[2 * NS + 10];
+  __shared__ __align__(8) uint64_t bars[2 * NS + 12];
   __shared__ uint32_t tmem_base;
   __shared__ volatile int gave_up;
   const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
@@ -60,10 +62,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
   auto full = [&](int s) { return b0 + 8 * s; };
   auto empty = [&](int s) { return b0 + 8 * (NS + s); };
   auto s_full = [&](int s) { return b0 + 8 * (2 * NS + s); };
-  auto p_full = [&](int s) { return b0 + 8 * (2 * NS + 2 + s); };
-  auto o_full = [&](int s) { return b0 + 8 * (2 * NS + 4 + s); };
-  auto q_full = [&](int s) { return b0 + 8 * (2 * NS + 6 + s); };
-  const uint32_t fix = b0 + 8 * (2 * NS + 8), done = fix + 8;
+  auto o_full = [&](int s) { return b0 + 8 * (2 * NS + 2 + s); };
+  auto q_full = [&](int s) { return b0 + 8 * (2 * NS + 4 + s); };
+  auto p_full = [&](int s, int half) { return b0 + 8 * (2 * NS + 6 + 2 * s + half); };
+  const uint32_t fix = b0 + 8 * (2 * NS + 10), done = fix + 8;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
 
   if (tid == 0) {
@@ -73,7 +75,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
     }
     for (int s = 0; s < 2; ++s) {
       bar_init(s_full(s), 1);
-      bar_init(p_full(s), 4);
+      bar_init(p_full(s, 0), 4);
+      bar_init(p_full(s, 1), 4);
       bar_init(o_full(s), 1);
       bar_init(q_full(s), 4);
     }
@@ -88,21 +91,42 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = tmem_base;
+  pdl_trigger();
   const RowsTotals tot = rows_totals(a);
   int64_t x = cta_first_tile(tot.all, a.nc, blockIdx.x);
   const int64_t x_end = cta_first_tile(tot.all, a.nc, blockIdx.x + 1);
   bool first_of_cta = true;
 
+  if (wid >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
   if (wid == 8) {  // ---------------------------------------------------------------- loads
     int slot = 0;
     uint32_t round = 0, fix_phase = 0;
     bool ok = true;
+    int pend_slot = -1, pend_row = 0;  // a V tile whose rows from pend_row on are still to be cleared
+    auto clear_pending = [&]() {
+      if (pend_slot < 0) return true;
+      if (!bar_wait(fix, fix_phase, &gave_up)) return false;
+      fix_phase ^= 1;
+      const uint32_t dst = ring + pend_slot * Sh::kTile;
+      const int per = (kTcKeys - pend_row) * 8;
+      for (int j = lane; j < per * PANELS; j += 32) {
+        const int p = j / per, q = j - p * per;
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst + p * kTcKeys * 128 + pend_row * 128 + q * 16), "r"(0)
+                     : "memory");
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) bar_arrive(full(pend_slot));
+      pend_slot = -1;
+      return true;
+    };
     while (x < x_end && ok) {
       const RowsSeg s = rows_find(a, tot, x);
       const int64_t t0 = x - s.first, t1 = min64(s.first + s.tiles, x_end) - s.first;
       const int cnt = int(t1 - t0);
-      const int64_t seg_rows = s.own ? int64_t(a.m) * a.group : a.rows;
-      const int lag = seg_rows - int64_t(s.p) * kTcRows > 128 ? 1 : 2;
+      const int seg_rows = s.own ? a.m * a.group : a.rows;
+      const int lag = seg_rows - s.p * kTcRows > 128 ? 1 : 2;
       const CUtensorMap* mk = s.own ? &maps.ko : &maps.k;
       const CUtensorMap* mv = s.own ? &maps.vo : &maps.v;
       const int plane = s.own ? s.b * a.hkv + s.h : s.h;
@@ -112,11 +136,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
         for (int kv = 1; kv >= 0; --kv) {  // V of tile i - lag, then K of tile i: the order of their use
           if (kv ? (!PV || i < lag) : i >= cnt) continue;
           const int64_t k0 = (t0 + (kv ? i - lag : i)) * kTcKeys;
+          // rows of V past a sequence's end hold anything (0 * NaN is NaN): cleared before the product sees them, once the
+          // copy has landed; meanwhile the next copies start, as long as none has to wait.  Past the prefix's end the
+          // tensor map ends, so the copy itself fills zeros.
+          const bool clear = kv && s.own && k0 + kTcKeys > len;
+          if ((clear || !bar_done(empty(slot), (round & 1) ^ 1)) && !(ok = clear_pending())) break;
           if (!(ok = bar_wait(empty(slot), (round & 1) ^ 1, &gave_up))) break;
           const uint32_t dst = ring + slot * Sh::kTile;
-          // rows of V past a sequence's end hold anything (0 * NaN is NaN): cleared before the product sees them.  Past
-          // the prefix's end the tensor map ends, so the copy itself fills zeros.
-          const bool clear = kv && s.own && k0 + kTcKeys > len;
           const uint32_t bar = clear ? fix : full(slot);
           if (lane == 0) {
             bar_expect(bar, Sh::kTile);
@@ -125,18 +151,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
               tma_load(dst + p * kTcKeys * 128, kv ? mv : mk, bar, p * 64, int(k0), plane);
           }
           if (clear) {
-            ok = bar_wait(fix, fix_phase, &gave_up);
-            fix_phase ^= 1;
-            const int r0 = int(len - k0);
-            for (int j = lane; j < (kTcKeys - r0) * PANELS * 8; j += 32) {
-              const int p = j / ((kTcKeys - r0) * 8), q = j - p * (kTcKeys - r0) * 8;
-              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst + p * kTcKeys * 128 + r0 * 128 + q * 16),
-                           "r"(0)
-                           : "memory");
-            }
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) bar_arrive(full(slot));
+            pend_slot = slot;
+            pend_row = int(len - k0);
           }
           if (++slot == NS) {
             slot = 0;
@@ -146,6 +162,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
       }
       x = s.first + t1;
     }
+    if (ok) clear_pending();
     // copies in flight when a wait gave up: let them land before the CTA's shared memory goes away
     if (gave_up) {
       int never = 0;
@@ -164,8 +181,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
       const RowsSeg s = rows_find(a, tot, x);
       const int64_t t0 = x - s.first, t1 = min64(s.first + s.tiles, x_end) - s.first;
       const int cnt = int(t1 - t0);
-      const int64_t seg_rows = s.own ? int64_t(a.m) * a.group : a.rows;
-      const bool both = seg_rows - int64_t(s.p) * kTcRows > 128;  // each stream its own rows
+      const int seg_rows = s.own ? a.m * a.group : a.rows;
+      const bool both = seg_rows - s.p * kTcRows > 128;  // each stream its own rows
       const int lag = both ? 1 : 2;
       for (int st = 0; st < 2 && ok; ++st) ok = bar_wait(q_full(st), q_phase, &gave_up);
       q_phase ^= 1;
@@ -193,24 +210,31 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
         for (int st = s_lo; st <= s_hi && ok; ++st) {
           const uint32_t ts = tm + st * 128, to = tm + 256 + st * D;
           if (has_o) {
-            ok = bar_wait(p_full(st), p_phase[st], &gave_up);
+            // the weights come in two halves of 64 keys: the products of the first run under the exponentials of the second
+            const uint32_t v = ring + v_slot * Sh::kTile;
+            const bool fresh = i == lag + (both ? 0 : (i & 1));  // the stream's first tile of the segment
+#pragma unroll
+            for (int half = 0; half < (PV ? 2 : 1); ++half) {
+              if (!(ok = bar_wait(p_full(st, half), p_phase[st], &gave_up))) break;
+              tc_fence_after();
+              if (PV && lane == 0) {
+#pragma unroll
+                for (int k = half * 4; k < half * 4 + 4; ++k)
+#pragma unroll
+                  for (int part = 0; part < 2; ++part)
+                    mma_ts(to, ts + (k / 2) * 32 + part * 16 + (k & 1) * 8, mma_desc(v + k * 2048, kTcKeys * 128), id_o,
+                           !fresh || part || k);
+              }
+            }
             p_phase[st] ^= 1;
             if (!ok) break;
-          }
-          tc_fence_after();
-          if (lane == 0) {
-            if (has_o && PV) {
-              const uint32_t v = ring + v_slot * Sh::kTile;
-              const bool fresh = i == lag + (both ? 0 : (i & 1));  // the stream's first tile of the segment
-#pragma unroll
-              for (int part = 0; part < 2; ++part)
-#pragma unroll
-                for (int k = 0; k < kTcKeys / 16; ++k)
-                  mma_ts(to, ts + part * 64 + k * 8, mma_desc(v + k * 2048, kTcKeys * 128), id_o,
-                         !fresh || part || k);
+            if (PV && lane == 0) {
               if (st == s_hi) mma_commit(empty(v_slot));
               if (i + (both ? 1 : 2) >= cnt + lag) mma_commit(o_full(st));
             }
+          }
+          tc_fence_after();
+          if (lane == 0) {
             if (has_s) {
               const uint32_t k = ring + k_slot * Sh::kTile;
 #pragma unroll
@@ -232,7 +256,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
     if (lane == 0) mma_commit(done);
     __syncwarp();
     bar_wait(done, 0, &never);
+  } else if (wid == 10) {
+    if (blockIdx.x == 0) rows_publish(a, tot);
+  }
   } else {  // ---------------------------------------------------------------- the streams' rows
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowRegs));
     const int st = wid >> 2, row = tid & 127, wrow = (wid & 3) * 32;
     const uint32_t lane_base = uint32_t(wrow) << 16;
     const uint32_t ts = tm + lane_base + st * 128, to = tm + lane_base + 256 + st * D;
@@ -243,21 +271,34 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
       const RowsSeg s = rows_find(a, tot, x);
       const int64_t t0 = x - s.first, t1 = min64(s.first + s.tiles, x_end) - s.first;
       const int cnt = int(t1 - t0);
-      const int64_t seg_rows = s.own ? int64_t(a.m) * a.group : a.rows;
-      const int64_t blk = int64_t(s.p) * kTcRows;
+      const int seg_rows = s.own ? a.m * a.group : a.rows;
+      const int blk = s.p * kTcRows;
       const bool both = seg_rows - blk > 128;
-      const int64_t r0 = blk + (both ? st * 128 : 0);  // the stream's first row
-      const int nrows = int(min64(128, seg_rows - r0));
-      const int64_t row_off = s.own ? int64_t(s.b) * a.m * a.group : 0;
-      for (int i = row; i < 128 * (D / 8); i += 128) {
-        const int r = i / (D / 8), c = i % (D / 8);
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (r < nrows)
-          v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.Q) +
-                                              row_index(a, s.h, row_off + r0 + r) * D + c * 8);
-        const uint32_t dst = q_sm[st] + (c / 8) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                     : "memory");
+      const int r0 = blk + (both ? st * 128 : 0);  // the stream's first row
+      const int nrows = min(128, seg_rows - r0);
+      const int row_off = s.own ? s.b * a.m * a.group : 0;
+      constexpr int CH = D / 8, RP = 128 / CH;  // 16-byte pieces of a row, rows per pass of the stream's threads
+      {
+        const int c = row % CH, rq = row / CH;
+        const __nv_bfloat16* Qp = static_cast<const __nv_bfloat16*>(a.Q) + c * 8;
+        const uint32_t dst = q_sm[st] + (c / 8) * (128 * 128);
+#pragma unroll
+        for (int g = 0; g < CH; g += 8) {  // eight loads in flight
+          uint4 v[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const int r = (g + q) * RP + rq;
+            v[q] = r < nrows ? *reinterpret_cast<const uint4*>(Qp + row_index(a, s.h, row_off + r0 + r) * D)
+                             : make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const int r = (g + q) * RP + rq;
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4)),
+                         "r"(v[q].x), "r"(v[q].y), "r"(v[q].z), "r"(v[q].w)
+                         : "memory");
+          }
+        }
       }
       fence_async_smem();
       __syncwarp();
@@ -285,9 +326,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
           }
           float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
 #pragma unroll
-          for (int j = 4; j < kTcKeys; j += 4)
+          for (int j = 4; j + 8 <= kTcKeys; j += 8)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], sv[j + q]);
+            for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], sv[j + q], sv[j + 4 + q]);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], sv[kTcKeys - 4 + q]);
           const float m_new = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;
           const bool grow = m_new > m_ref + kLazyMax || (m_ref == -INFINITY && m_new > -INFINITY);
           if (__any_sync(0xffffffffu, grow)) {
@@ -313,31 +356,47 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
             }
           }
           const float mb = m_ref == -INFINITY ? 0.f : m_ref;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint64_t cc = pair(c2, c2), mm = pair(-mb, -mb), minus = pair(-1.f, -1.f);
+          uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            uint32_t hi[16], lo[16];
+            uint32_t w[32];  // 32 keys: their hi parts, then their lo parts
 #pragma unroll
             for (int q = 0; q < 16; ++q) {
-              const float p0 = ex2(fmaf(sv[32 * j + 2 * q], c2, -mb)), p1 = ex2(fmaf(sv[32 * j + 2 * q + 1], c2, -mb));
-              sum[(2 * q) & 3] += p0;
-              sum[(2 * q + 1) & 3] += p1;
+              float e0, e1;
+              unpair(fma2(pair(sv[32 * j + 2 * q], sv[32 * j + 2 * q + 1]), cc, mm), &e0, &e1);
+              const uint64_t p = pair(ex2(e0), ex2(e1));
+              sum[q & 1] = add2(sum[q & 1], p);
               if (PV) {
-                hi[q] = pack_bf16(p0, p1);
-                lo[q] = pack_bf16(p0 - __uint_as_float(hi[q] << 16), p1 - __uint_as_float(hi[q] & 0xffff0000u));
+                float p0, p1;
+                unpair(p, &p0, &p1);
+                w[q] = pack_bf16(p0, p1);
+                unpair(fma2(pair(__uint_as_float(w[q] << 16), __uint_as_float(w[q] & 0xffff0000u)), minus, p), &p0, &p1);
+                w[16 + q] = pack_bf16(p0, p1);
               }
             }
             if (PV) {
-              tmem_st16(ts + 16 * j, hi);
-              tmem_st16(ts + 64 + 16 * j, lo);
+              tmem_st32(ts + 32 * j, w);
+              if (j & 1) {
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(p_full(st, j >> 1));
+              }
             }
           }
-          l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-          if (PV) tmem_wait_st();
+          float s0, s1;
+          unpair(add2(sum[0], sum[1]), &s0, &s1);
+          l_run += s0 + s1;
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) bar_arrive(p_full(st));
+        if (!PV || !active) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            bar_arrive(p_full(st, 0));
+            if (PV) bar_arrive(p_full(st, 1));
+          }
+        }
       }
       if (!ok) break;
       const bool any = i0 < cnt;  // a single tile leaves stream 1 without work
@@ -425,8 +484,7 @@ cudaError_t make_rows_map(CUtensorMap* map, const void* base, int d, int64_t row
 namespace {
 
 template <int D, bool PV> cudaError_t run_tc(const RowsArgs& a, const TcMaps& maps, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(rows_tc_kernel<D, PV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       TcShape<D>::kSmem);
+  const cudaError_t e = allow_smem(rows_tc_kernel<D, PV>, TcShape<D>::kSmem);
   if (e != cudaSuccess) return e;
   rows_tc_kernel<D, PV><<<a.nc, kTcThreads, TcShape<D>::kSmem, st>>>(a, maps);
   return cudaGetLastError();

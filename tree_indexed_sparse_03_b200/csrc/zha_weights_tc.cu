@@ -164,6 +164,8 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = tmem_base;
+  pdl_trigger();
+  pdl_wait();
   const WtPlan plan = wt_plan(a);
   int64_t x = cta_first_tile(plan.all, gridDim.x, blockIdx.x);
   const int64_t x_end = cta_first_tile(plan.all, gridDim.x, blockIdx.x + 1);
@@ -352,6 +354,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
 
 // Segments cut by CTA borders: block c joins the one that begins in CTA c and ends in a later one.
 __global__ void __launch_bounds__(kWtKeys) weights_tc_join_kernel(WeightsArgs a) {
+  pdl_wait();
   const WtPlan plan = wt_plan(a);
   const int nc = gridDim.x, c = blockIdx.x;
   const int64_t x0 = cta_first_tile(plan.all, nc, c), x1 = cta_first_tile(plan.all, nc, c + 1);
@@ -371,13 +374,11 @@ __global__ void __launch_bounds__(kWtKeys) weights_tc_join_kernel(WeightsArgs a)
 namespace {
 
 template <int D> cudaError_t run_weights_tc(const WeightsArgs& a, const WtMaps& maps, int nc, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(weights_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       WtShape<D>::kSmem);
+  cudaError_t e = allow_smem(weights_tc_kernel<D>, WtShape<D>::kSmem);
   if (e != cudaSuccess) return e;
-  weights_tc_kernel<D><<<nc, kWtThreads, WtShape<D>::kSmem, st>>>(a, maps);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  weights_tc_join_kernel<<<nc, kWtKeys, 0, st>>>(a);
-  return cudaGetLastError();
+  e = launch_after(weights_tc_kernel<D>, dim3(nc), kWtThreads, WtShape<D>::kSmem, st, a, maps);
+  if (e != cudaSuccess) return e;
+  return launch_after(weights_tc_join_kernel, dim3(nc), kWtKeys, 0, st, a);
 }
 
 }  // namespace
