@@ -276,6 +276,20 @@ def test_weights_workspace_reused_and_wide_groups(dtype):
         close(a, want_a, REL * want_a + 1e-6, f"{m} {nn}")
 
 
+@pytest.mark.parametrize("dtype,d,hkv,group,m,n", [("bf16", 64, 5, 3, 95, 300), ("bf16", 128, 40, 1, 2, 130),
+                                                   ("bf16", 64, 200, 1, 1, 90), ("f32", 64, 200, 2, 1, 70)])
+def test_weights_many_short_segments(dtype, d, hkv, group, m, n):
+    """Several segments per CTA: whole ones between two that its neighbours share, blocks of a few rows among them."""
+    K, V, Q = rnd(1, hkv, n, d, dtype=dtype), rnd(2, hkv, n, d, dtype=dtype), rnd(3, m, hkv * group, d, dtype=dtype, scale=2.0)
+    dec = z.DenseWeights(cfg_of(dtype, d, hkv, group), m, n)
+    for causal in (True, False):
+        want_o, want_a = weights_ref(K, V, n, Q, None, causal)
+        o, a = dec(K.cuda(), V.cuda(), n, Q.cuda(), causal=causal)
+        close(o, want_o, REL * float(V.abs().max()) + 1e-6, "O")
+        close(a, want_a, REL * want_a + 1e-6, "acc")
+    dec.status()
+
+
 def test_weights_graph_and_stream():
     n, m, d = 700, 9, 64
     K, V, Q = rnd(1, 2, n, d).cuda(), rnd(2, 2, n, d).cuda(), rnd(3, m, 6, d, scale=2.0).cuda()

@@ -579,13 +579,14 @@ static int prefix_plan(const zha_config* cfg, int32_t B, int32_t m, int64_t n, i
   if (n < 0 || n >= kMaxTokens || ld_own < 0 || ld_own >= kMaxTokens)
     return fail(ZHA_ERR_INVALID, "n and ld_own must be in [0, 2^31)");
   rows_plan(cfg->dtype, cfg->d, cfg->n_kv_heads, cfg->n_q_heads / cfg->n_kv_heads, B, m, n, ld_own, p);
+  if (p->places >= double(1 << 30)) return fail(ZHA_ERR_UNSUPPORTED, "too many (query, key) pairs for one call");
   return ZHA_OK;
 }
 
 // The tile list's words: row blocks of at least 8 rows.
 static uint64_t rows_plan_bytes(const zha_config* cfg, int64_t B, int64_t m) {
   const int64_t rows = B * m * (cfg->n_q_heads / cfg->n_kv_heads);
-  return align256(uint64_t(rows_plan_words(int((rows + 7) / 8), int(B))) * 8);
+  return align256(uint64_t(rows_plan_words(int((rows + 7) / 8), int(B))) * 4);
 }
 
 static uint64_t rows_part_bytes(const zha_config* cfg, int64_t B, int64_t m, const RowsPlan& p) {
@@ -604,8 +605,9 @@ static void fill_rows(const zha_config* cfg, const RowsPlan& p, int32_t B, int32
   a->hq = cfg->n_q_heads;
   a->hkv = cfg->n_kv_heads;
   a->group = cfg->n_q_heads / cfg->n_kv_heads;
-  a->rb = p.rb;
-  a->kt = p.kt;
+  a->rb_log = p.rb_log;
+  a->kt_log = p.kt_log;
+  a->extra = p.extra;
   a->pp = p.pp;
   a->po = p.po;
   a->rp = p.rp;
@@ -614,8 +616,7 @@ static void fill_rows(const zha_config* cfg, const RowsPlan& p, int32_t B, int32
   a->part_own = int64_t(p.part_own);
   a->scale = 1.0f / std::sqrt(float(cfg->d));
   a->status = static_cast<int*>(scratch);
-  a->tc = p.tc;
-  a->plan = reinterpret_cast<int64_t*>(static_cast<char*>(scratch) + kScratchHead);
+  a->plan = reinterpret_cast<int*>(static_cast<char*>(scratch) + kScratchHead);
   a->part = reinterpret_cast<float*>(static_cast<char*>(scratch) + kScratchHead + rows_plan_bytes(cfg, B, m));
   a->part_ml = reinterpret_cast<float2*>(a->part + p.part_rows * cfg->d);
 }
@@ -671,6 +672,7 @@ static int weights_layout(const zha_config* cfg, int32_t m, int64_t n, RowsPlan*
   if (n < 1) return fail(ZHA_ERR_INVALID, "n must be >= 1");
   const int64_t rows = int64_t(m) * (cfg->n_q_heads / cfg->n_kv_heads);
   weights_plan(cfg->dtype, cfg->d, cfg->n_kv_heads, rows, n, wp);
+  if (wp->places >= double(1 << 30)) return fail(ZHA_ERR_UNSUPPORTED, "too many (query, key) pairs for one call");
   *lse_off = kScratchHead + rows_part_bytes(cfg, 1, m, *rp);
   *sums_off = align256(*lse_off + uint64_t(m) * cfg->n_q_heads * 4);
   *bytes = align256(*sums_off + wp->sum_floats * 4);

@@ -33,11 +33,12 @@ __global__ void __launch_bounds__(kRowsThreads) rows_scalar_kernel(RowsArgs a) {
   pdl_trigger();
   const RowsTotals tot = rows_totals(a);
   if (blockIdx.x == 0 && wid == 0) rows_publish(a, tot);
-  int64_t x = cta_first_tile(tot.all, a.nc, blockIdx.x);
-  const int64_t x_end = cta_first_tile(tot.all, a.nc, blockIdx.x + 1);
-  bool first_of_cta = true;
-  while (x < x_end) {
+  const int x_begin = tot.sh.begin(blockIdx.x), x_end = tot.sh.begin(blockIdx.x + 1);
+  for (int x = x_begin; x < x_end;) {
     const RowsSeg s = rows_find(a, tot, x);
+    const int t_begin = x - s.first, t_end = min(s.first + s.tiles, x_end) - s.first;
+    x = s.next;
+    if (t_begin >= t_end) continue;
     const int seg_rows = s.own ? a.m * a.group : a.rows;
     const int r0 = s.p * RB;
     const int nrows = min(RB, seg_rows - r0);
@@ -71,9 +72,8 @@ __global__ void __launch_bounds__(kRowsThreads) rows_scalar_kernel(RowsArgs a) {
 #pragma unroll
       for (int j = 0; j < CT; ++j) o[i][j] = 0.f;
     }
-    const int64_t t_end = min64(s.first + s.tiles, x_end) - s.first;
-    for (int64_t t = x - s.first; t < t_end; ++t) {
-      const int64_t k0 = t * kRowsKeys;
+    for (int t = t_begin; t < t_end; ++t) {
+      const int64_t k0 = int64_t(t) * kRowsKeys;
       __syncthreads();
       for (int i = tid; i < kRowsKeys * CPR; i += kRowsThreads) {
         const int r = i / CPR, c = i % CPR;
@@ -165,8 +165,8 @@ __global__ void __launch_bounds__(kRowsThreads) rows_scalar_kernel(RowsArgs a) {
       }
     }
     // the segment's share of this CTA: a partial, or the row's result where the CTA holds the whole segment
-    const bool whole = !a.has_own && x == s.first && t_end == s.tiles;
-    const int64_t slot = part_row(a, blockIdx.x, s.own, s.id, first_of_cta);
+    const bool whole = !a.has_own && t_begin == 0 && t_end == s.tiles;
+    const int64_t slot = part_row(a, blockIdx.x, s.own, s.id, x_begin < s.first);
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
       const int rl = half * RT + i;
@@ -189,8 +189,6 @@ __global__ void __launch_bounds__(kRowsThreads) rows_scalar_kernel(RowsArgs a) {
         }
       }
     }
-    first_of_cta = false;
-    x = s.first + t_end;
   }
 }
 
@@ -207,56 +205,73 @@ __global__ void __launch_bounds__(256) rows_combine_kernel(RowsArgs a) {
   const bool live = r < a.rows;
   pdl_trigger();
   pdl_wait();
+  Shares sh;
+  sh.set(a.plan[0], a.nc);
+  // the row's prefix partials: CTAs c_lo[0] .. + cnt[0] - 1, its own ones likewise
+  int c_lo[2] = {0, 0}, cnt[2] = {0, 0}, id[2], rl[2], first[2];
+  bool direct = false;
+  if (live) {
+    const int p = r >> a.rb_log, base = a.plan[3 + p], tiles = a.plan[4 + p] - base - a.extra;
+    rl[0] = r - (p << a.rb_log);
+    first[0] = h * a.plan[1] + base;
+    id[0] = h * a.pp + p;
+    if (tiles > 0) {
+      c_lo[0] = sh.owner(first[0]);
+      cnt[0] = sh.owner(first[0] + tiles - 1) - c_lo[0] + 1;
+      direct = !a.has_own && cnt[0] == 1;  // written by its CTA
+    }
+    if (a.has_own) {
+      const int mg = a.m * a.group, b = r / mg, rs = r - b * mg, q = rs >> a.rb_log;
+      const int ob = a.plan[4 + a.pp + b], span = a.plan[5 + a.pp + b] - ob, u = h * a.po + q;
+      rl[1] = rs - (q << a.rb_log);
+      first[1] = a.plan[2] + ob * (a.hkv * a.po) + u * span;
+      id[1] = a.hkv * a.pp + b * a.hkv * a.po + u;
+      if (span > 0) {
+        c_lo[1] = sh.owner(first[1]);
+        cnt[1] = sh.owner(first[1] + span - a.extra - 1) - c_lo[1] + 1;
+      }
+    }
+  }
+  const int total = direct ? 0 : cnt[0] + cnt[1];
+  // a warp takes a contiguous run, 32 partials at a time: their scales lane by lane, their rows four in flight
+  const int run = (total + W - 1) / W, q_end = min(total, (w + 1) * run);
   float M = -INFINITY, L = 0.f, o[EL];
 #pragma unroll
   for (int e = 0; e < EL; ++e) o[e] = 0.f;
-  bool direct = false;
-  const int64_t all = a.plan[0], head = a.plan[1], prefix = a.plan[2];
-  for (int part = 0; part < (a.has_own ? 2 : 1) && live; ++part) {
-    int64_t first, tiles;
-    int id, rl, left;  // segment, row within its block, rows from the block's first on
-    if (part == 0) {
-      const int p = r / a.rb;
-      rl = r - p * a.rb;
-      left = a.rows - p * a.rb;
-      first = a.plan[3 + p];
-      tiles = a.plan[4 + p] - first;
-      first += h * head;
-      id = h * a.pp + p;
-    } else {
-      const int mg = a.m * a.group;
-      const int b = r / mg, rs = r - b * mg;
-      const int p = rs / a.rb;
-      rl = rs - p * a.rb;
-      left = mg - p * a.rb;
-      const int64_t base = a.plan[4 + a.pp + b];
-      tiles = a.plan[5 + a.pp + b] - base;
-      const int u = h * a.po + p;
-      first = prefix + base * (a.hkv * a.po) + u * tiles;
-      id = a.hkv * a.pp + b * a.hkv * a.po + u;
+  for (int q0 = w * run; q0 < q_end; q0 += 32) {
+    const int q = q0 + lane, have = min(32, q_end - q0);
+    int64_t pr = 0;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (lane < have) {
+      const int k = q >= cnt[0], c = c_lo[k] + (k ? q - cnt[0] : q);
+      pr = part_row(a, c, k, id[k], sh.begin(c) < first[k]) + rl[k];
+      ml = __ldcg(a.part_ml + pr);
     }
-    if (tiles == 0) continue;
-    const int c_lo = tile_cta(all, a.nc, first), c_hi = tile_cta(all, a.nc, first + tiles - 1);
-    const int subs = a.tc && left <= 128 ? 2 : 1;  // partials of this row per CTA
-    if (!a.has_own && c_lo == c_hi && subs == 1) {
-      direct = true;  // written by its CTA
-      continue;
-    }
-    for (int q = w; q < (c_hi - c_lo + 1) * subs; q += W) {
-      const int c = c_lo + q / subs;
-      if (cta_empty(all, a.nc, c)) continue;  // fewer tiles than CTAs
-      const int64_t pr = part_row(a, c, part, id, cta_first_tile(all, a.nc, c) >= first) + rl +
-                         (q % subs) * ((part ? a.ro : a.rp) / 2);
-      const float2 ml = __ldcg(a.part_ml + pr);
-      float v[EL];
+    float mn = fmaxf(M, ml.x);
 #pragma unroll
-      for (int e = 0; e < EL; ++e) v[e] = a.O ? __ldcg(a.part + pr * D + lane + 32 * e) : 0.f;
-      if (ml.x == -INFINITY && ml.y == 0.f) continue;  // nothing of this share is visible to the row
-      const float mn = fmaxf(M, ml.x), s0 = exp2f(M - mn), s1 = exp2f(ml.x - mn);
-      L = L * s0 + ml.y * s1;
+    for (int off = 16; off > 0; off >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, off));
+    const float base = mn == -INFINITY ? 0.f : mn;
+    const bool none = ml.x == -INFINITY && ml.y == 0.f;  // nothing of this share is visible to the row
+    const float sc = none ? 0.f : exp2f(ml.x - base), keep = exp2f(M - base);
+    float l = none ? 0.f : ml.y * sc;
 #pragma unroll
-      for (int e = 0; e < EL; ++e) o[e] = o[e] * s0 + v[e] * s1;
-      M = mn;
+    for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+    L = L * keep + l;
+#pragma unroll
+    for (int e = 0; e < EL; ++e) o[e] *= keep;
+    M = mn;
+    if (a.O) {
+#pragma unroll 4
+      for (int j = 0; j < have; ++j) {
+        const float s = __shfl_sync(0xffffffffu, sc, j);
+        const int64_t row = __shfl_sync(0xffffffffu, pr, j);
+        const bool skip = __shfl_sync(0xffffffffu, int(none), j);
+#pragma unroll
+        for (int e = 0; e < EL; ++e) {
+          const float v = __ldcg(a.part + row * D + lane + 32 * e);
+          if (!skip) o[e] = fmaf(v, s, o[e]);
+        }
+      }
     }
   }
   __shared__ float jm[8], jl[8], jo[8][D];
@@ -273,7 +288,7 @@ __global__ void __launch_bounds__(256) rows_combine_kernel(RowsArgs a) {
       for (int q = 1; q < W; ++q) {
         const float m_s = jm[wid + q];
         if (m_s == -INFINITY && jl[wid + q] == 0.f) continue;
-        const float mn = fmaxf(M, m_s), s0 = exp2f(M - mn), s1 = exp2f(m_s - mn);
+        const float mn = fmaxf(M, m_s), s0 = M == -INFINITY ? 0.f : exp2f(M - mn), s1 = exp2f(m_s - mn);
         L = L * s0 + jl[wid + q] * s1;
 #pragma unroll
         for (int e = 0; e < EL; ++e) o[e] = o[e] * s0 + jo[wid + q][lane + 32 * e] * s1;
@@ -426,7 +441,7 @@ template <typename T, int D, int RT> cudaError_t run_rows(const RowsArgs& a, cud
 }
 
 template <typename T, int D> cudaError_t run_rows_rt(const RowsArgs& a, cudaStream_t st) {
-  switch (a.rb / 8) {
+  switch (1 << a.rb_log >> 3) {
     case 1: return run_rows<T, D, 1>(a, st);
     case 4: return run_rows<T, D, 4>(a, st);
     default: return run_rows<T, D, 8>(a, st);
@@ -457,8 +472,14 @@ template <typename T, int D> cudaError_t run_weights_rt(const WeightsArgs& a, cu
 
 }  // namespace
 
-// Partial rows of a plan whose row blocks, CTAs and slot rows are set.
-static void plan_parts(int hkv, int64_t B, int64_t ld_own, RowsPlan* p) {
+// CTAs (at most `most`, and no more than tiles) and partial rows of a plan whose row blocks and tiles are set.  Own caches
+// are taken as long as they can be.
+static void plan_parts(int hkv, int64_t B, int64_t n, int64_t ld_own, int most, RowsPlan* p) {
+  const double pt = double((n + (1 << p->kt_log) - 1) >> p->kt_log), ot = double((ld_own + (1 << p->kt_log) - 1) >> p->kt_log);
+  const double ps = double(hkv) * p->pp, os = double(B) * hkv * p->po;
+  const double tiles = ps * pt + os * ot;
+  p->places = tiles + (ps + os) * p->extra;
+  p->nc = tiles < 1 ? 1 : (tiles < most ? int(tiles) : most);
   if (ld_own > 0) {
     p->part_own = (uint64_t(p->nc) + uint64_t(hkv) * p->pp) * p->rp;
     p->part_rows = p->part_own + (uint64_t(p->nc) + uint64_t(B) * hkv * p->po) * p->ro;
@@ -470,28 +491,23 @@ static void plan_parts(int hkv, int64_t B, int64_t ld_own, RowsPlan* p) {
 
 static void scalar_plan(int d, int rt, int hkv, int64_t B, int64_t rows, int64_t mg, int64_t n, int64_t ld_own,
                         RowsPlan* p) {
-  p->kt = kRowsKeys;
-  p->rb = 8 * rt;
+  const int rb = 8 * rt;
+  p->rb_log = rt == 1 ? 3 : (rt == 4 ? 5 : 6);
+  p->kt_log = 6;
+  p->extra = 1;  // queries, first loads and the write-out of a segment take about as long as a tile
+  p->pp = int((rows + rb - 1) / rb);
+  p->po = ld_own > 0 ? int((mg + rb - 1) / rb) : 0;
+  p->rp = int(rows < rb ? rows : rb);
+  p->ro = int(mg < rb ? mg : rb);
   const int per_sm = int(220 * 1024 / (rows_smem(d, rt) + 1024));
-  p->pp = int((rows + p->rb - 1) / p->rb);
-  p->po = ld_own > 0 ? int((mg + p->rb - 1) / p->rb) : 0;
-  p->rp = int(rows < p->rb ? rows : p->rb);
-  p->ro = int(mg < p->rb ? mg : p->rb);
-  // at most one CTA per tile (an upper bound: own caches as long as they can be)
-  const double tiles = double(hkv) * p->pp * double((n + p->kt - 1) / p->kt) +
-                       double(B) * hkv * p->po * double((ld_own + p->kt - 1) / p->kt);
-  const int most = 148 * (per_sm < 1 ? 1 : (per_sm > 4 ? 4 : per_sm));
-  p->nc = tiles < 1 ? 1 : (tiles < most ? int(tiles) : most);
-  p->tc = 0;
-  plan_parts(hkv, B, ld_own, p);
+  plan_parts(hkv, B, n, ld_own, 148 * (per_sm < 1 ? 1 : (per_sm > 4 ? 4 : per_sm)), p);
 }
 
 void rows_plan(int dtype, int d, int hkv, int group, int64_t B, int64_t m, int64_t n, int64_t ld_own, RowsPlan* p) {
   const int64_t rows = B * m * group;
   if (dtype == ZHA_BF16) {
-    tc_plan(hkv, B, rows, m * group, n, ld_own, p);
-    p->tc = 1;
-    plan_parts(hkv, B, ld_own, p);
+    tc_plan(rows, m * group, ld_own, p);
+    plan_parts(hkv, B, n, ld_own, 148, p);
   } else {
     scalar_plan(d, scalar_rt(d, rows), hkv, B, rows, m * group, n, ld_own, p);
   }
@@ -508,8 +524,8 @@ uint64_t rows_part_bound(int dtype, int d, int hkv, int group, int64_t B, int64_
     for (int own = 0; own < 2; ++own) {
       RowsPlan p;
       if (dtype == ZHA_BF16) {
-        tc_plan(hkv, B, rows, mg, n, own ? ld_own : 0, &p);
-        plan_parts(hkv, B, own ? ld_own : 0, &p);
+        tc_plan(rows, mg, own ? ld_own : 0, &p);
+        plan_parts(hkv, B, n, own ? ld_own : 0, 148, &p);
       } else {
         scalar_plan(d, rt, hkv, min64(B, cap), min64(rows, cap), min64(mg, cap), n, own ? ld_own : 0, &p);
       }
@@ -533,8 +549,10 @@ void weights_plan(int dtype, int d, int hkv, int64_t rows, int64_t n, WeightsPla
     p->rsplit = 1;
     p->rows_per_split = rows;
     p->sum_floats = weights_tc_floats();
+    p->places = double(hkv) * double((n + 255) / 256) * double(rows / 64 + 1);  // 64 rows per tile at least
     return;
   }
+  p->places = 0;
   const int64_t rb = 8 * scalar_rt(d, rows);
   const int64_t ctas = (n + kRowsKeys - 1) / kRowsKeys * hkv, blocks = (rows + rb - 1) / rb;
   int64_t s = (kWeightsCtas + ctas - 1) / ctas;  // a few CTAs per SM

@@ -9,11 +9,11 @@
 //
 // Work split.  A segment is one row block over one key range: first the
 // prefix segments (h, row block), then the own segments (b, h, row block of the
-// sequence).  A segment is cut into key tiles; all tiles of all segments form
-// one flat list, and CTA c of nc takes tiles [c*T/nc, (c+1)*T/nc).  So every CTA
-// has the same number of tiles whatever the lengths are, lengths that only
-// the device knows included.  A CTA leaves one partial (running max, running sum,
-// numerator) per segment it touches; rows_combine_kernel joins them in CTA order.
+// sequence).  A segment is cut into key tiles; the tiles of all segments, each
+// segment followed by `extra` empty places for what starting one costs, form one flat list, and the CTAs take equal
+// contiguous shares of it (the first T % nc one place more), so every CTA has the same work whatever
+// the lengths are, lengths that only the device knows included.  A CTA leaves one partial (running max, running
+// sum, numerator) per segment it shares with others; rows_combine_kernel joins them in CTA order.
 #pragma once
 
 #include <atomic>
@@ -35,20 +35,19 @@ struct RowsArgs {
   float2* part_ml;          // and (running max in powers of two, running sum) per row
   float* logits;            // NULL, or [hkv][rows][n] raw dot products of the prefix to leave for the weights pass
   int* status;
-  int64_t* plan;            // the tile list as the attention kernel's first CTA found it, for the join:
-                            // totals, then rows_plan_words() - see rows_publish
+  int* plan;                // the flat list as the attention kernel's first CTA found it, for the join (rows_publish)
   int64_t ld, n, ld_own;
   int rows;                 // rows per KV head over the prefix: B * m * group
   int64_t part_own;         // first own slot's offset in `part`, in rows
   int B, m, hq, hkv, group;
   int causal;               // 1: query i sees prefix tokens [0, n - m + i] (B = 1)
   int has_own;
-  int rb;                   // rows per row block
-  int kt;                   // keys per tile
+  int rb_log;               // rows per row block, a power of two
+  int kt_log;               // keys per tile, a power of two
+  int extra;                // empty places behind a segment's tiles
   int pp, po;               // row blocks of a prefix / an own segment
   int rp, ro;               // rows of a prefix / an own partial slot
   int nc;                   // CTAs
-  int tc;                   // 1: the tensor-core kernel, whose row blocks of at most 128 rows leave two partials
   float scale;              // 1 / sqrt(d)
 };
 
@@ -70,52 +69,70 @@ __device__ __forceinline__ int64_t own_limit(const RowsArgs& a, int64_t len, int
 }
 
 // Tiles of the prefix segment of row block p (of every KV head).
-__device__ __forceinline__ int64_t prefix_tiles(const RowsArgs& a, int p) {
-  const int last = min((p + 1) * a.rb, a.rows) - 1;
-  return (prefix_limit(a, last) + a.kt - 1) / a.kt;
+__device__ __forceinline__ int prefix_tiles(const RowsArgs& a, int p) {
+  const int last = min((p + 1) << a.rb_log, a.rows) - 1;
+  return int((prefix_limit(a, last) + (1 << a.kt_log) - 1) >> a.kt_log);
 }
 
-__device__ __forceinline__ int64_t own_tiles(const RowsArgs& a, int b) { return (own_tokens(a, b) + a.kt - 1) / a.kt; }
-
-__device__ __forceinline__ int64_t warp_sum64(int64_t v) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  return v;
+__device__ __forceinline__ int own_tiles(const RowsArgs& a, int b) {
+  return int((own_tokens(a, b) + (1 << a.kt_log) - 1) >> a.kt_log);
 }
+
+// Places of a segment of t tiles in the flat list.
+__device__ __forceinline__ int seg_span(const RowsArgs& a, int t) { return t ? t + a.extra : 0; }
 
 // Sum of f(i) over i in [0, n), by one full warp.
-template <typename F> __device__ __forceinline__ int64_t warp_total(int n, F f) {
-  int64_t s = 0;
+template <typename F> __device__ __forceinline__ int warp_total(int n, F f) {
+  int s = 0;
   for (int i = threadIdx.x & 31; i < n; i += 32) s += f(i);
-  return warp_sum64(s);
+  return __reduce_add_sync(0xffffffffu, s);
 }
 
-// The totals of the flat tile list, by one full warp.
+// Contiguous shares of a list of `all` places for nc CTAs; the first `more` shares have one place more.  Where there
+// are fewer places than CTAs the last CTAs have none.
+struct Shares {
+  int all, per, more;
+  __device__ __forceinline__ void set(int total, int nc) {
+    all = total;
+    per = total / nc;
+    more = total - per * nc;
+  }
+  __device__ __forceinline__ int begin(int c) const { return c * per + min(c, more); }
+  __device__ __forceinline__ int owner(int x) const {
+    const int big = more * (per + 1);
+    return x < big ? x / (per + 1) : more + (x - big) / per;
+  }
+};
+
+// The totals of the flat list, by one full warp.
 struct RowsTotals {
-  int64_t head;    // tiles of one KV head's prefix segments
-  int64_t prefix;  // tiles of all prefix segments
-  int64_t all;
+  int head;    // places of one KV head's prefix segments
+  int prefix;  // places of all prefix segments
+  Shares sh;
 };
 
 __device__ __forceinline__ RowsTotals rows_totals(const RowsArgs& a) {
   RowsTotals t;
-  t.head = a.causal ? warp_total(a.pp, [&](int p) { return prefix_tiles(a, p); }) : int64_t(a.pp) * prefix_tiles(a, 0);
+  t.head = a.causal ? warp_total(a.pp, [&](int p) { return seg_span(a, prefix_tiles(a, p)); })
+                    : a.pp * seg_span(a, prefix_tiles(a, 0));
   t.prefix = t.head * a.hkv;
-  t.all = t.prefix + (a.has_own ? int64_t(a.hkv) * a.po * warp_total(a.B, [&](int b) { return own_tiles(a, b); }) : 0);
+  t.sh.set(t.prefix + (a.has_own ? a.hkv * a.po * warp_total(a.B, [&](int b) { return seg_span(a, own_tiles(a, b)); }) : 0),
+           a.nc);
   return t;
 }
 
 // First item of the list with lengths f(0..n) that holds position x (0 <= x < total), by one full warp; *base
 // receives the position of the item's first element.
-template <typename F> __device__ __forceinline__ int warp_find(int n, F f, int64_t x, int64_t* base) {
+template <typename F> __device__ __forceinline__ int warp_find(int n, F f, int x, int* base) {
   const int lane = threadIdx.x & 31;
-  int64_t run = 0;
+  int run = 0;
+#pragma unroll 1
   for (int i0 = 0; i0 < n; i0 += 32) {
-    const int64_t v = i0 + lane < n ? f(i0 + lane) : 0;
-    int64_t inc = v;
+    const int v = i0 + lane < n ? f(i0 + lane) : 0;
+    int inc = v;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, inc, off);
+      const int y = __shfl_up_sync(0xffffffffu, inc, off);
       if (lane >= off) inc += y;
     }
     const unsigned hit = __ballot_sync(0xffffffffu, run + inc > x);
@@ -130,66 +147,56 @@ template <typename F> __device__ __forceinline__ int warp_find(int n, F f, int64
   return n;  // not reached for x < total
 }
 
-// A position in the flat list: segment seg, its tiles [first, first + tiles) in the list.
+// A segment: its tiles are places [first, first + tiles) of the list, its empty places follow up to `next`.
 struct RowsSeg {
   int own;        // 0: prefix, 1: own
   int b, h, p;    // sequence (own), KV head, row block
   int id;         // segment number
-  int64_t first, tiles;
+  int first, tiles, next;
 };
 
-// The segment that holds flat tile x, by one full warp.
-__device__ __forceinline__ RowsSeg rows_find(const RowsArgs& a, const RowsTotals& t, int64_t x) {
+// The segment that holds place x, by one full warp.
+__device__ __forceinline__ RowsSeg rows_find(const RowsArgs& a, const RowsTotals& t, int x) {
   RowsSeg s;
   if (x < t.prefix) {
     s.own = 0;
     s.b = 0;
-    s.h = int(x / t.head);
-    const int64_t r = x - s.h * t.head;
-    int64_t base;
+    s.h = x / t.head;
+    const int r = x - s.h * t.head;
+    int base;
     if (a.causal) {
-      s.p = warp_find(a.pp, [&](int p) { return prefix_tiles(a, p); }, r, &base);
+      s.p = warp_find(a.pp, [&](int p) { return seg_span(a, prefix_tiles(a, p)); }, r, &base);
       s.tiles = prefix_tiles(a, s.p);
     } else {
       s.tiles = prefix_tiles(a, 0);
-      s.p = int(r / s.tiles);
-      base = s.p * s.tiles;
+      s.p = r / seg_span(a, s.tiles);
+      base = s.p * seg_span(a, s.tiles);
     }
     s.first = s.h * t.head + base;
     s.id = s.h * a.pp + s.p;
   } else {
     s.own = 1;
-    const int64_t per = int64_t(a.hkv) * a.po;
-    int64_t base;
-    s.b = warp_find(a.B, [&](int b) { return own_tiles(a, b) * per; }, x - t.prefix, &base);
+    const int per = a.hkv * a.po;
+    int base;
+    s.b = warp_find(a.B, [&](int b) { return seg_span(a, own_tiles(a, b)) * per; }, x - t.prefix, &base);
     s.tiles = own_tiles(a, s.b);
-    const int64_t r = x - t.prefix - base;
-    const int u = int(r / s.tiles);
+    const int u = (x - t.prefix - base) / seg_span(a, s.tiles);
     s.h = u / a.po;
     s.p = u - s.h * a.po;
-    s.first = t.prefix + base + int64_t(u) * s.tiles;
-    s.id = a.hkv * a.pp + s.b * int(per) + u;
+    s.first = t.prefix + base + u * seg_span(a, s.tiles);
+    s.id = a.hkv * a.pp + s.b * per + u;
   }
+  s.next = s.first + seg_span(a, s.tiles);
   return s;
 }
 
-__device__ __forceinline__ int64_t cta_first_tile(int64_t total, int nc, int c) { return int64_t(c) * total / nc; }
-
-// Whether CTA c has no tile (more CTAs than tiles): it leaves no partial, whatever lies in its slots.
-__device__ __forceinline__ bool cta_empty(int64_t total, int nc, int c) {
-  return cta_first_tile(total, nc, c) == cta_first_tile(total, nc, c + 1);
-}
-
-// CTA that owns flat tile x: the c with c*T/nc <= x < (c+1)*T/nc (rounded down).
-__device__ __forceinline__ int tile_cta(int64_t total, int nc, int64_t x) { return int(((x + 1) * nc - 1) / total); }
-
 // Partial slot of CTA c for a segment.  With own caches every row has several partials: slot c + segment number
-// (unique, since along the list either the CTA or the segment advances).  Without, a segment inside one
-// CTA is written out directly and only the CTA's first and last segments need slots: 2c and 2c + 1.
-// Returns the slot's first row in `part`.
-__device__ __forceinline__ int64_t part_row(const RowsArgs& a, int c, int own, int id, bool first_of_cta) {
-  if (!a.has_own) return (2 * int64_t(c) + (first_of_cta ? 0 : 1)) * a.rp;
-  return own ? a.part_own + (int64_t(c) + id - int64_t(a.hkv) * a.pp) * a.ro : (int64_t(c) + id) * a.rp;
+// (unique, since along the list either the CTA or the segment advances).  Without, a segment whose tiles lie
+// inside one CTA's share is written out directly, and a share cuts at most two: slot 2c for one that holds the share's
+// begin, 2c + 1 for a later one.  Returns the slot's first row in `part`.
+__device__ __forceinline__ int64_t part_row(const RowsArgs& a, int c, int own, int id, bool later) {
+  if (!a.has_own) return (2 * int64_t(c) + (later ? 1 : 0)) * a.rp;
+  return own ? a.part_own + (int64_t(c) + id - a.hkv * a.pp) * a.ro : (int64_t(c) + id) * a.rp;
 }
 
 // Index of (sequence, query token, query head) of row r of KV head h in Q, O and lse (times d for Q and O).
@@ -198,19 +205,21 @@ __device__ __forceinline__ int64_t row_index(const RowsArgs& a, int h, int r) {
   return int64_t(t) * a.hq + h * a.group + (r - t * a.group);
 }
 
-// The list's layout for the join, written once by one warp of the first CTA: totals, then the first tile of every
-// row block of a head and of every sequence's own segments (both with their end).
+// The list for the join, written once by one warp of the first CTA: places in all, of a head's prefix segments and of
+// all of them; then the first place of every row block of a head and of every sequence's own segments (of one
+// KV head and row block), both with their end.
 __host__ __device__ __forceinline__ int64_t rows_plan_words(int pp, int B) { return 3 + pp + 1 + B + 1; }
 
-template <typename F> __device__ __forceinline__ void warp_prefix(int n, F f, int64_t* out) {
+template <typename F> __device__ __forceinline__ void warp_prefix(int n, F f, int* out) {
   const int lane = threadIdx.x & 31;
-  int64_t run = 0;
+  int run = 0;
+#pragma unroll 1
   for (int i0 = 0; i0 < n; i0 += 32) {
-    const int64_t v = i0 + lane < n ? f(i0 + lane) : 0;
-    int64_t inc = v;
+    const int v = i0 + lane < n ? f(i0 + lane) : 0;
+    int inc = v;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, inc, off);
+      const int y = __shfl_up_sync(0xffffffffu, inc, off);
       if (lane >= off) inc += y;
     }
     if (i0 + lane < n) out[i0 + lane] = run + inc - v;
@@ -221,12 +230,12 @@ template <typename F> __device__ __forceinline__ void warp_prefix(int n, F f, in
 
 __device__ __forceinline__ void rows_publish(const RowsArgs& a, const RowsTotals& t) {
   if ((threadIdx.x & 31) == 0) {
-    a.plan[0] = t.all;
+    a.plan[0] = t.sh.all;
     a.plan[1] = t.head;
     a.plan[2] = t.prefix;
   }
-  warp_prefix(a.pp, [&](int p) { return prefix_tiles(a, p); }, a.plan + 3);
-  if (a.has_own) warp_prefix(a.B, [&](int b) { return own_tiles(a, b); }, a.plan + 4 + a.pp);
+  warp_prefix(a.pp, [&](int p) { return seg_span(a, prefix_tiles(a, p)); }, a.plan + 3);
+  if (a.has_own) warp_prefix(a.B, [&](int b) { return seg_span(a, own_tiles(a, b)); }, a.plan + 4 + a.pp);
 }
 
 // Launch of a kernel that may start while its predecessor in the stream still runs; it waits with pdl_wait() before
@@ -280,12 +289,13 @@ struct WeightsArgs {
 
 // Host side: the plan of a call (kernel variant, CTAs, partial rows).
 struct RowsPlan {
-  int rb, kt, nc, pp, po, rp, ro, tc;
+  int rb_log, kt_log, extra, nc, pp, po, rp, ro;
+  double places;  // most places the flat list can have
   uint64_t part_rows, part_own;
 };
 void rows_plan(int dtype, int d, int hkv, int group, int64_t B, int64_t m, int64_t n, int64_t ld_own, RowsPlan* p);
 uint64_t rows_part_bound(int dtype, int d, int hkv, int group, int64_t B, int64_t m, int64_t n, int64_t ld_own);
-void tc_plan(int hkv, int64_t B, int64_t rows, int64_t mg, int64_t n, int64_t ld_own, RowsPlan* p);
+void tc_plan(int64_t rows, int64_t mg, int64_t ld_own, RowsPlan* p);
 cudaError_t launch_rows_tc(const RowsArgs& a, int d, cudaStream_t st);
 cudaError_t launch_rows(const RowsArgs& a, int dtype, int d, cudaStream_t st);
 
@@ -293,6 +303,7 @@ struct WeightsPlan {
   int rsplit;
   int64_t rows_per_split;
   uint64_t sum_floats;  // partial sums in the scratch
+  double places;        // places of the tensor-core kernel's list
 };
 void weights_plan(int dtype, int d, int hkv, int64_t rows, int64_t n, WeightsPlan* p);
 uint64_t weights_sums_bound(int dtype, int hkv, int64_t n);

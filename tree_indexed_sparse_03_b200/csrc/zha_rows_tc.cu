@@ -14,15 +14,19 @@
 // run - the tensor pipe is the limit for many rows, HBM for few.
 // A segment of more than 128 rows gives each stream its own rows and both the same tiles (each K and V
 // tile is loaded once for 256 rows); a smaller one gives both streams the same rows and every other tile,
-// and their two results are joined with the other partials.
+// and stream 0 joins the two results.
 //
 // The maximum is lazy: O is rescaled in tensor memory only when a row's maximum has grown by more than 2^8, so
 // weights stay below 2^8 and the usual tile rescales nothing.
 //
 // Roles: warps 0-3 and 4-7 the two streams' rows, warp 8 the TMA loads into a ring of K / V
-// tiles, warp 9 issues the products.  A row's 128 logits stay in one thread's registers, so the streams' warps take
-// registers over from the others.  Order of the products per stream: P V of the previous tile, then
-// S of the next; a commit after S therefore also says that the earlier P V is complete.
+// tiles, warps 9 and 10 issue the two streams' products (a product's operands are five registers that one thread has to
+// provide: one warp for both streams took 100 cycles a product, above the 64 it runs).
+// Order of the products per stream: P V of the previous tile, then S of the next; a commit after S
+// therefore also says that the earlier P V is complete.
+//
+// The code of a role runs a few times per launch when lengths are short, and its first run waits for its
+// instructions: loops over a row's 128 logits go in two rounds of 2 x 32 columns rather than unrolled.
 #include <cstring>
 
 #include "zha_rows.cuh"
@@ -31,8 +35,7 @@
 namespace zha {
 
 constexpr int kTcKeys = 128;               // keys per tile
-constexpr int kTcThreads = 384;            // three warpgroups, the third one's last two warps idle
-constexpr int kRowRegs = 224, kFewRegs = 56;  // registers a thread: 2 * 128 * 224 + 128 * 56 = 384 * 168, the launch's own
+constexpr int kTcThreads = 384;
 constexpr int kTcRows = 256;               // rows of a row block: two streams of 128
 constexpr float kLazyMax = 8.f;            // growth of the maximum (log2) that rescales O
 
@@ -47,16 +50,40 @@ struct TcMaps {
   CUtensorMap k, v, ko, vo;
 };
 
+// One share of a segment as every role sees it.
+struct TcWork {
+  RowsSeg s;
+  int t0, cnt;    // its first tile within the segment, its tiles
+  int seg_rows;   // rows of the segment's head (prefix) or sequence (own)
+  bool both;      // each stream has rows of its own
+};
+
+// The next share at or after place *x of the CTA's places, by one full warp; false at their end.
+__device__ __forceinline__ bool next_work(const RowsArgs& a, const RowsTotals& tot, int* x, int x_end, TcWork* w) {
+  while (*x < x_end) {
+    w->s = rows_find(a, tot, *x);
+    w->t0 = *x - w->s.first;
+    w->cnt = min(w->s.first + w->s.tiles, x_end) - *x;
+    *x = w->s.next;
+    if (w->cnt > 0) {
+      w->seg_rows = w->s.own ? a.m * a.group : a.rows;
+      w->both = w->seg_rows - w->s.p * kTcRows > 128;
+      return true;
+    }
+  }
+  return false;
+}
+
 template <int D, bool PV>
 __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, const __grid_constant__ TcMaps maps) {
   using Sh = TcShape<D>;
-  constexpr int NS = Sh::kSlots, PANELS = D / 64;
+  constexpr int NS = Sh::kSlots, PANELS = D / 64, PANEL = kTcKeys * 128;  // bytes of a 64-wide panel of a tile
   extern __shared__ uint8_t raw[];
-  __shared__ __align__(8) uint64_t bars[2 * NS + 12];
+  __shared__ __align__(8) uint64_t bars[2 * NS + 15];
+  __shared__ float2 x_ml[128];  // stream 1's sums for the join
   __shared__ uint32_t tmem_base;
   __shared__ volatile int gave_up;
   const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
-  const uint32_t q_sm[2] = {base, base + Sh::kQ};
   const uint32_t ring = base + 2 * Sh::kQ;
   const uint32_t b0 = smem_u32(bars);
   auto full = [&](int s) { return b0 + 8 * s; };
@@ -65,40 +92,43 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
   auto o_full = [&](int s) { return b0 + 8 * (2 * NS + 2 + s); };
   auto q_full = [&](int s) { return b0 + 8 * (2 * NS + 4 + s); };
   auto p_full = [&](int s, int half) { return b0 + 8 * (2 * NS + 6 + 2 * s + half); };
-  const uint32_t fix = b0 + 8 * (2 * NS + 10), done = fix + 8;
+  const uint32_t fix = b0 + 8 * (2 * NS + 10), done = fix + 8, x_full = fix + 16, x_free = fix + 24, x_may = fix + 32;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
 
-  if (tid == 0) {
-    for (int s = 0; s < NS; ++s) {
-      bar_init(full(s), 1);
-      bar_init(empty(s), 1);
+  if (wid == 11) {
+    if (lane == 0) {
+      for (int s = 0; s < NS; ++s) {
+        bar_init(full(s), 1);
+        bar_init(empty(s), 2);  // both streams
+      }
+      for (int s = 0; s < 2; ++s) {
+        bar_init(s_full(s), 1);
+        bar_init(o_full(s), 1);
+        bar_init(q_full(s), 4);
+        bar_init(p_full(s, 0), 4);
+        bar_init(p_full(s, 1), 4);
+      }
+      bar_init(fix, 1);
+      bar_init(done, 2);
+      bar_init(x_full, 4);
+      bar_init(x_free, 4);
+      bar_init(x_may, 4);
+      gave_up = 0;
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    for (int s = 0; s < 2; ++s) {
-      bar_init(s_full(s), 1);
-      bar_init(p_full(s, 0), 4);
-      bar_init(p_full(s, 1), 4);
-      bar_init(o_full(s), 1);
-      bar_init(q_full(s), 4);
-    }
-    bar_init(fix, 1);
-    bar_init(done, 1);
-    gave_up = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    fence_async_smem();
+    __syncwarp();
+    tmem_alloc(smem_u32(&tmem_base), 512);
   }
-  if (wid == 9) tmem_alloc(smem_u32(&tmem_base), 512);
+  pdl_trigger();
+  const RowsTotals tot = rows_totals(a);
+  const int x_begin = tot.sh.begin(blockIdx.x), x_end = tot.sh.begin(blockIdx.x + 1);
+  int x = x_begin;
+  TcWork w;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = tmem_base;
-  pdl_trigger();
-  const RowsTotals tot = rows_totals(a);
-  int64_t x = cta_first_tile(tot.all, a.nc, blockIdx.x);
-  const int64_t x_end = cta_first_tile(tot.all, a.nc, blockIdx.x + 1);
-  bool first_of_cta = true;
 
-  if (wid >= 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
   if (wid == 8) {  // ---------------------------------------------------------------- loads
     int slot = 0;
     uint32_t round = 0, fix_phase = 0;
@@ -108,59 +138,53 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
       if (pend_slot < 0) return true;
       if (!bar_wait(fix, fix_phase, &gave_up)) return false;
       fix_phase ^= 1;
-      const uint32_t dst = ring + pend_slot * Sh::kTile;
+      const uint32_t dst = ring + pend_slot * Sh::kTile + pend_row * 128;
       const int per = (kTcKeys - pend_row) * 8;
-      for (int j = lane; j < per * PANELS; j += 32) {
-        const int p = j / per, q = j - p * per;
-        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst + p * kTcKeys * 128 + pend_row * 128 + q * 16), "r"(0)
-                     : "memory");
-      }
+#pragma unroll 1
+      for (int p = 0; p < PANELS; ++p)
+#pragma unroll 1
+        for (int q = lane; q < per; q += 32)
+          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst + p * PANEL + q * 16), "r"(0) : "memory");
       fence_async_smem();
       __syncwarp();
       if (lane == 0) bar_arrive(full(pend_slot));
       pend_slot = -1;
       return true;
     };
-    while (x < x_end && ok) {
-      const RowsSeg s = rows_find(a, tot, x);
-      const int64_t t0 = x - s.first, t1 = min64(s.first + s.tiles, x_end) - s.first;
-      const int cnt = int(t1 - t0);
-      const int seg_rows = s.own ? a.m * a.group : a.rows;
-      const int lag = seg_rows - s.p * kTcRows > 128 ? 1 : 2;
-      const CUtensorMap* mk = s.own ? &maps.ko : &maps.k;
-      const CUtensorMap* mv = s.own ? &maps.vo : &maps.v;
-      const int plane = s.own ? s.b * a.hkv + s.h : s.h;
-      const int64_t len = s.own ? own_tokens(a, s.b) : a.n;
-      for (int i = 0; i < cnt + lag && ok; ++i) {
+    while (ok && next_work(a, tot, &x, x_end, &w)) {
+      const int lag = w.both ? 1 : 2;
+      const CUtensorMap* mk = w.s.own ? &maps.ko : &maps.k;
+      const CUtensorMap* mv = w.s.own ? &maps.vo : &maps.v;
+      const int plane = w.s.own ? w.s.b * a.hkv + w.s.h : w.s.h;
+      const int len = int(w.s.own ? own_tokens(a, w.s.b) : a.n);
+#pragma unroll 1
+      for (int i = 0; i < 2 * (w.cnt + lag) && ok; ++i) {
+        const bool kv = !(i & 1);  // V of tile i/2 - lag, then K of tile i/2: the order of their use
+        const int t = (i >> 1) - (kv ? lag : 0);
+        if (kv ? (!PV || t < 0) : t >= w.cnt) continue;
+        const int k0 = (w.t0 + t) * kTcKeys;
+        // rows of V past a sequence's end hold anything (0 * NaN is NaN): cleared before the product sees them, once the
+        // copy has landed; meanwhile the next copies start, as long as none has to wait.  Past the prefix's end the
+        // tensor map ends, so the copy itself fills zeros.
+        const bool clear = kv && w.s.own && k0 + kTcKeys > len;
+        if ((clear || !bar_done(empty(slot), (round & 1) ^ 1)) && !(ok = clear_pending())) break;
+        if (!(ok = bar_wait(empty(slot), (round & 1) ^ 1, &gave_up))) break;
+        const uint32_t dst = ring + slot * Sh::kTile;
+        const uint32_t bar = clear ? fix : full(slot);
+        if (lane == 0) {
+          bar_expect(bar, Sh::kTile);
 #pragma unroll
-        for (int kv = 1; kv >= 0; --kv) {  // V of tile i - lag, then K of tile i: the order of their use
-          if (kv ? (!PV || i < lag) : i >= cnt) continue;
-          const int64_t k0 = (t0 + (kv ? i - lag : i)) * kTcKeys;
-          // rows of V past a sequence's end hold anything (0 * NaN is NaN): cleared before the product sees them, once the
-          // copy has landed; meanwhile the next copies start, as long as none has to wait.  Past the prefix's end the
-          // tensor map ends, so the copy itself fills zeros.
-          const bool clear = kv && s.own && k0 + kTcKeys > len;
-          if ((clear || !bar_done(empty(slot), (round & 1) ^ 1)) && !(ok = clear_pending())) break;
-          if (!(ok = bar_wait(empty(slot), (round & 1) ^ 1, &gave_up))) break;
-          const uint32_t dst = ring + slot * Sh::kTile;
-          const uint32_t bar = clear ? fix : full(slot);
-          if (lane == 0) {
-            bar_expect(bar, Sh::kTile);
-#pragma unroll
-            for (int p = 0; p < PANELS; ++p)
-              tma_load(dst + p * kTcKeys * 128, kv ? mv : mk, bar, p * 64, int(k0), plane);
-          }
-          if (clear) {
-            pend_slot = slot;
-            pend_row = int(len - k0);
-          }
-          if (++slot == NS) {
-            slot = 0;
-            ++round;
-          }
+          for (int p = 0; p < PANELS; ++p) tma_load(dst + p * PANEL, kv ? mv : mk, bar, p * 64, k0, plane);
+        }
+        if (clear) {
+          pend_slot = slot;
+          pend_row = len - k0;
+        }
+        if (++slot == NS) {
+          slot = 0;
+          ++round;
         }
       }
-      x = s.first + t1;
     }
     if (ok) clear_pending();
     // copies in flight when a wait gave up: let them land before the CTA's shared memory goes away
@@ -168,127 +192,121 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
       int never = 0;
       for (int q = 0; q < NS; ++q) {
         const uint32_t r = q < slot ? round : round - 1;  // the slot's last use
-        if (q < slot || round > 0) bar_wait(full(q), r & 1, &never);
+        if (q < slot || round > 0) bar_wait(q == pend_slot ? fix : full(q), q == pend_slot ? fix_phase : r & 1, &never);
       }
     }
-  } else if (wid == 9) {  // ---------------------------------------------------------------- products
-    int slot = 0;
-    uint32_t round = 0;
-    uint32_t p_phase[2] = {0, 0}, q_phase = 0;
-    bool ok = true;
+  } else if (wid == 9 || wid == 10) {  // ---------------------------------------------------------------- products
+    const int st = wid - 9;
     constexpr uint32_t id_s = mma_idesc(kTcKeys, false), id_o = mma_idesc(D, true);
-    while (x < x_end && ok) {
-      const RowsSeg s = rows_find(a, tot, x);
-      const int64_t t0 = x - s.first, t1 = min64(s.first + s.tiles, x_end) - s.first;
-      const int cnt = int(t1 - t0);
-      const int seg_rows = s.own ? a.m * a.group : a.rows;
-      const bool both = seg_rows - s.p * kTcRows > 128;  // each stream its own rows
-      const int lag = both ? 1 : 2;
-      for (int st = 0; st < 2 && ok; ++st) ok = bar_wait(q_full(st), q_phase, &gave_up);
+    const uint32_t ts = tm + st * 128, to = tm + 256 + st * D;
+    const uint32_t q_lo = desc_low(base + st * Sh::kQ, 16);
+    const uint32_t k_lo = desc_low(ring, 16), v_lo = desc_low(ring, PANEL);
+    int slot = 0;
+    uint32_t round = 0, p_phase = 0, q_phase = 0;
+    bool ok = true;
+    while (ok && next_work(a, tot, &x, x_end, &w)) {
+      const int lag = w.both ? 1 : 2;
+      if (!(ok = bar_wait(q_full(st), q_phase, &gave_up))) break;
       q_phase ^= 1;
-      if (!both && cnt == 1 && lane == 0) bar_arrive(o_full(1));  // stream 1 has no tile: nothing to wait for
-      for (int i = 0; i < cnt + lag && ok; ++i) {
-        const bool has_o = i >= lag, has_s = i < cnt;
-        const int s_lo = both ? 0 : (i & 1), s_hi = both ? 1 : (i & 1);
-        int v_slot = 0, k_slot = 0;
-        if (PV && has_o) {
-          v_slot = slot;
-          ok = bar_wait(full(slot), round & 1, &gave_up);
-          if (++slot == NS) {
-            slot = 0;
-            ++round;
-          }
-        }
-        if (has_s && ok) {
-          k_slot = slot;
-          ok = bar_wait(full(slot), round & 1, &gave_up);
-          if (++slot == NS) {
-            slot = 0;
-            ++round;
-          }
-        }
-        for (int st = s_lo; st <= s_hi && ok; ++st) {
-          const uint32_t ts = tm + st * 128, to = tm + 256 + st * D;
-          if (has_o) {
+      if (!w.both && w.cnt == 1 && st == 1 && lane == 0) bar_arrive(o_full(1));  // no tile for stream 1: nothing to wait for
+      bool fresh = true;  // the stream's first tile of the segment
+#pragma unroll 1
+      for (int i = 0; i < w.cnt + lag && ok; ++i) {
+        const bool mine = w.both || (i & 1) == st;
+        if (i >= lag && PV) {
+          if (!(ok = bar_wait(full(slot), round & 1, &gave_up))) break;
+          if (mine) {
             // the weights come in two halves of 64 keys: the products of the first run under the exponentials of the second
-            const uint32_t v = ring + v_slot * Sh::kTile;
-            const bool fresh = i == lag + (both ? 0 : (i & 1));  // the stream's first tile of the segment
+            const uint32_t v = v_lo + slot * (Sh::kTile >> 4);
 #pragma unroll
-            for (int half = 0; half < (PV ? 2 : 1); ++half) {
-              if (!(ok = bar_wait(p_full(st, half), p_phase[st], &gave_up))) break;
+            for (int half = 0; half < 2; ++half) {
+              if (!(ok = bar_wait(p_full(st, half), p_phase, &gave_up))) break;
               tc_fence_after();
-              if (PV && lane == 0) {
+              if (lane == 0) {
 #pragma unroll
                 for (int k = half * 4; k < half * 4 + 4; ++k)
 #pragma unroll
                   for (int part = 0; part < 2; ++part)
-                    mma_ts(to, ts + (k / 2) * 32 + part * 16 + (k & 1) * 8, mma_desc(v + k * 2048, kTcKeys * 128), id_o,
-                           !fresh || part || k);
+                    mma_ts(to, ts + (k / 2) * 32 + part * 16 + (k & 1) * 8, v + k * (2048 >> 4), id_o,
+                           k || part ? 1u : uint32_t(!fresh));
               }
+              __syncwarp();
             }
-            p_phase[st] ^= 1;
             if (!ok) break;
-            if (PV && lane == 0) {
-              if (st == s_hi) mma_commit(empty(v_slot));
-              if (i + (both ? 1 : 2) >= cnt + lag) mma_commit(o_full(st));
+            p_phase ^= 1;
+            fresh = false;
+            if (lane == 0) {
+              mma_commit(empty(slot));
+              if (i + lag >= w.cnt + lag) mma_commit(o_full(st));
             }
-          }
-          tc_fence_after();
-          if (lane == 0) {
-            if (has_s) {
-              const uint32_t k = ring + k_slot * Sh::kTile;
-#pragma unroll
-              for (int e = 0; e < D / 16; ++e) {
-                const uint32_t off = (e / 4) * (kTcKeys * 128) + (e % 4) * 32;
-                mma_ss(ts, mma_desc(q_sm[st] + off, 16), mma_desc(k + off, 16), id_s, e > 0);
-              }
-              if (st == s_hi) mma_commit(empty(k_slot));
-              mma_commit(s_full(st));
-            }
+          } else if (lane == 0) {
+            bar_arrive(empty(slot));
           }
           __syncwarp();
+          if (++slot == NS) {
+            slot = 0;
+            ++round;
+          }
+        } else if (i >= lag && mine) {  // without outputs: the logits have been read
+          if (!(ok = bar_wait(p_full(st, 0), p_phase, &gave_up))) break;
+          p_phase ^= 1;
+        }
+        if (i < w.cnt) {
+          if (!(ok = bar_wait(full(slot), round & 1, &gave_up))) break;
+          if (mine) {
+            tc_fence_after();
+            if (lane == 0) {
+              const uint32_t k = k_lo + slot * (Sh::kTile >> 4);
+#pragma unroll
+              for (int e = 0; e < D / 16; ++e) {
+                const uint32_t off = ((e / 4) * PANEL + (e % 4) * 32) >> 4;
+                mma_ss(ts, q_lo + off, k + off, id_s, e ? 1u : 0u);
+              }
+              mma_commit(s_full(st));
+              mma_commit(empty(slot));
+            }
+          } else if (lane == 0) {
+            bar_arrive(empty(slot));
+          }
+          __syncwarp();
+          if (++slot == NS) {
+            slot = 0;
+            ++round;
+          }
         }
       }
-      x = s.first + t1;
     }
     // nothing of the tensor pipe may be in flight when tensor memory is given back
-    int never = 0;
     if (lane == 0) mma_commit(done);
     __syncwarp();
+    int never = 0;
     bar_wait(done, 0, &never);
-  } else if (wid == 10) {
+  } else if (wid == 11) {
     if (blockIdx.x == 0) rows_publish(a, tot);
-  }
   } else {  // ---------------------------------------------------------------- the streams' rows
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowRegs));
     const int st = wid >> 2, row = tid & 127, wrow = (wid & 3) * 32;
     const uint32_t lane_base = uint32_t(wrow) << 16;
     const uint32_t ts = tm + lane_base + st * 128, to = tm + lane_base + 256 + st * D;
     const float c2 = a.scale * 1.4426950408889634f;  // weights as powers of two
-    uint32_t s_phase = 0, o_phase = 0;
+    const uint64_t cc = pair(c2, c2), minus = pair(-1.f, -1.f);
+    uint32_t s_phase = 0, o_phase = 0, x_phase = 0;
     bool ok = true;
-    while (x < x_end && ok) {
-      const RowsSeg s = rows_find(a, tot, x);
-      const int64_t t0 = x - s.first, t1 = min64(s.first + s.tiles, x_end) - s.first;
-      const int cnt = int(t1 - t0);
-      const int seg_rows = s.own ? a.m * a.group : a.rows;
-      const int blk = s.p * kTcRows;
-      const bool both = seg_rows - blk > 128;
-      const int r0 = blk + (both ? st * 128 : 0);  // the stream's first row
-      const int nrows = min(128, seg_rows - r0);
-      const int row_off = s.own ? s.b * a.m * a.group : 0;
-      constexpr int CH = D / 8, RP = 128 / CH;  // 16-byte pieces of a row, rows per pass of the stream's threads
+    while (ok && next_work(a, tot, &x, x_end, &w)) {
+      const int r0 = w.s.p * kTcRows + (w.both ? st * 128 : 0);  // the stream's first row
+      const int nrows = min(128, w.seg_rows - r0);
+      const int row_off = w.s.own ? w.s.b * a.m * a.group : 0;
       {
+        constexpr int CH = D / 8, RP = 128 / CH;  // 16-byte pieces of a row, rows per pass of the stream's threads
         const int c = row % CH, rq = row / CH;
         const __nv_bfloat16* Qp = static_cast<const __nv_bfloat16*>(a.Q) + c * 8;
-        const uint32_t dst = q_sm[st] + (c / 8) * (128 * 128);
-#pragma unroll
+        const uint32_t dst = base + st * Sh::kQ + (c / 8) * (128 * 128);
+#pragma unroll 1
         for (int g = 0; g < CH; g += 8) {  // eight loads in flight
           uint4 v[8];
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
             const int r = (g + q) * RP + rq;
-            v[q] = r < nrows ? *reinterpret_cast<const uint4*>(Qp + row_index(a, s.h, row_off + r0 + r) * D)
+            v[q] = r < nrows ? *reinterpret_cast<const uint4*>(Qp + row_index(a, w.s.h, row_off + r0 + r) * D)
                              : make_uint4(0, 0, 0, 0);
           }
 #pragma unroll
@@ -303,51 +321,58 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
       fence_async_smem();
       __syncwarp();
       if (lane == 0) bar_arrive(q_full(st));
-      const int64_t len = s.own ? own_tokens(a, s.b) : a.n;
-      const int64_t lim = row >= nrows ? 0 : (s.own ? own_limit(a, len, r0 + row) : prefix_limit(a, r0 + row));
+      const int lim = row >= nrows ? 0 : int(w.s.own ? own_limit(a, own_tokens(a, w.s.b), r0 + row) : prefix_limit(a, r0 + row));
       const bool active = wrow < nrows;  // a warp of padding rows leaves its weights alone: they reach no valid row
       float m_ref = -INFINITY, l_run = 0.f;
-      const int step = both ? 1 : 2, i0 = both ? 0 : st;
-      for (int i = i0; i < cnt; i += step) {
+      const int step = w.both ? 1 : 2, i0 = w.both ? 0 : st;
+#pragma unroll 1
+      for (int i = i0; i < w.cnt; i += step) {
         if (!(ok = bar_wait(s_full(st), s_phase, &gave_up))) break;
         s_phase ^= 1;
         tc_fence_after();
         if (active) {
-          float sv[kTcKeys];
+          const int left = lim - (w.t0 + i) * kTcKeys;  // keys of the tile that the row sees
+          const bool mask = __any_sync(0xffffffffu, left < kTcKeys);
+          float va[32], vb[32];
+          auto hide = [&](float* v, int c0) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) tmem_ld32(ts + 32 * j, sv + 32 * j);
-          tmem_wait_ld();
-          const int64_t left = lim - (t0 + i) * kTcKeys;
-          if (__any_sync(0xffffffffu, left < kTcKeys)) {
-            const int n_vis = left < 0 ? 0 : (left > kTcKeys ? kTcKeys : int(left));
+            for (int q = 0; q < 32; ++q)
+              if (c0 + q >= left) v[q] = -INFINITY;
+          };
+          auto largest = [&](const float* v, float m) {
 #pragma unroll
-            for (int j = 0; j < kTcKeys; ++j)
-              if (j >= n_vis) sv[j] = -INFINITY;
+            for (int q = 0; q < 32; q += 4) m = max3(max3(m, v[q], v[q + 1]), v[q + 2], v[q + 3]);
+            return m;
+          };
+          float mx = -INFINITY;
+          tmem_ld32(ts, va);
+          tmem_wait32(va);
+#pragma unroll 1
+          for (int j = 0; j < kTcKeys; j += 64) {  // one chunk is loaded while the other is looked at
+            tmem_ld32(ts + j + 32, vb);
+            if (mask) hide(va, j);
+            mx = largest(va, mx);
+            tmem_wait32(vb);
+            tmem_ld32(ts + ((j + 64) & (kTcKeys - 1)), va);  // last: the first chunk again, for the exponentials
+            if (mask) hide(vb, j + 32);
+            mx = largest(vb, mx);
+            tmem_wait32(va);
           }
-          float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
-#pragma unroll
-          for (int j = 4; j + 8 <= kTcKeys; j += 8)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], sv[j + q], sv[j + 4 + q]);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], sv[kTcKeys - 4 + q]);
-          const float m_new = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;
+          const float m_new = mx * c2;
           const bool grow = m_new > m_ref + kLazyMax || (m_ref == -INFINITY && m_new > -INFINITY);
           if (__any_sync(0xffffffffu, grow)) {
             const float up = grow ? m_new : m_ref;
             const float sc = m_ref == -INFINITY ? 0.f : ex2(m_ref - up);
             if (PV && i != i0) {
-              // l > 0 is not needed: a row without weights so far has O = 0 (or NaN from NaN)
-#pragma unroll
-              for (int j = 0; j < D / 32; ++j) {
-                float o[32];
-                tmem_ld32(to + 32 * j, o);
-                tmem_wait_ld();
+#pragma unroll 1
+              for (int j = 0; j < D; j += 32) {
+                tmem_ld32(to + j, vb);
+                tmem_wait32(vb);
                 if (grow) {
 #pragma unroll
-                  for (int q = 0; q < 32; ++q) o[q] = m_ref == -INFINITY ? 0.f : o[q] * sc;
+                  for (int q = 0; q < 32; ++q) vb[q] = m_ref == -INFINITY ? 0.f : vb[q] * sc;
                 }
-                tmem_st32(to + 32 * j, reinterpret_cast<const uint32_t*>(o));
+                tmem_st32(to + j, reinterpret_cast<const uint32_t*>(vb));
               }
             }
             if (grow) {
@@ -356,40 +381,45 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
             }
           }
           const float mb = m_ref == -INFINITY ? 0.f : m_ref;
-          const uint64_t cc = pair(c2, c2), mm = pair(-mb, -mb), minus = pair(-1.f, -1.f);
+          const uint64_t mm = pair(-mb, -mb);
           uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t w[32];  // 32 keys: their hi parts, then their lo parts
+          auto weigh = [&](const float* v, int c0) {  // 32 keys: their weights' hi parts, then their lo parts, over the logits
+            uint32_t o[32];
 #pragma unroll
             for (int q = 0; q < 16; ++q) {
               float e0, e1;
-              unpair(fma2(pair(sv[32 * j + 2 * q], sv[32 * j + 2 * q + 1]), cc, mm), &e0, &e1);
+              unpair(fma2(pair(v[2 * q], v[2 * q + 1]), cc, mm), &e0, &e1);
               const uint64_t p = pair(ex2(e0), ex2(e1));
               sum[q & 1] = add2(sum[q & 1], p);
               if (PV) {
                 float p0, p1;
                 unpair(p, &p0, &p1);
-                w[q] = pack_bf16(p0, p1);
-                unpair(fma2(pair(__uint_as_float(w[q] << 16), __uint_as_float(w[q] & 0xffff0000u)), minus, p), &p0, &p1);
-                w[16 + q] = pack_bf16(p0, p1);
+                o[q] = pack_bf16(p0, p1);
+                unpair(fma2(pair(__uint_as_float(o[q] << 16), __uint_as_float(o[q] & 0xffff0000u)), minus, p), &p0, &p1);
+                o[16 + q] = pack_bf16(p0, p1);
               }
             }
-            if (PV) {
-              tmem_st32(ts + 32 * j, w);
-              if (j & 1) {
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) bar_arrive(p_full(st, j >> 1));
-              }
-            }
+            if (PV) tmem_st32(ts + c0, o);
+          };
+#pragma unroll 1
+          for (int j = 0; j < kTcKeys; j += 64) {
+            tmem_ld32(ts + j + 32, vb);
+            if (mask) hide(va, j);
+            weigh(va, j);
+            tmem_wait32(vb);
+            if (j == 0) tmem_ld32(ts + 64, va);
+            if (mask) hide(vb, j + 32);
+            weigh(vb, j + 32);
+            if (j == 0) tmem_wait32(va);
+            if (PV) tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0 && (PV || j)) bar_arrive(p_full(st, PV ? j >> 6 : 0));
           }
           float s0, s1;
           unpair(add2(sum[0], sum[1]), &s0, &s1);
           l_run += s0 + s1;
-        }
-        if (!PV || !active) {
+        } else {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
@@ -399,52 +429,110 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
         }
       }
       if (!ok) break;
-      const bool any = i0 < cnt;  // a single tile leaves stream 1 without work
-      if (PV || !any) {  // also without work: the stream stays within one segment of the products' warp
+      if (PV || i0 >= w.cnt) {  // also without work: the stream stays within one segment of its products' warp
         if (!(ok = bar_wait(o_full(st), o_phase, &gave_up))) break;
         o_phase ^= 1;
         tc_fence_after();
       }
-      // the segment's share of this CTA: a partial per stream, or the result where this CTA's streams hold all tiles
-      const bool whole = !a.has_own && both && x == s.first && t1 == s.tiles;
-      if (active) {
-        const int64_t pr = part_row(a, blockIdx.x, s.own, s.id, first_of_cta) +
-                           (both ? st * 128 : st * ((s.own ? a.ro : a.rp) / 2)) + row;
-        const int64_t ri = row < nrows ? row_index(a, s.h, row_off + r0 + row) : 0;
-        float inv = 1.f;
+      // streams that shared the rows: stream 1 leaves its sums and rows where the queries lay, stream 0 joins them
+      const bool join = !w.both && w.cnt > 1;
+      const uint32_t xrow = base + row * (D * 4);  // the row's place, 16-byte pieces swizzled by the row
+      float other_l = 0.f, mine_s = 1.f, other_s = 0.f;
+      if (join) {
+        if (st == 1) {
+          if (!(ok = bar_wait(x_may, x_phase, &gave_up))) break;  // stream 0's products still read its queries
+          if (active) {
+            if (PV) {
+#pragma unroll 1
+              for (int j = 0; j < D; j += 32) {
+                float v[32];
+                tmem_ld32(to + j, v);
+                tmem_wait32(v);
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(xrow + ((((j >> 2) + q) ^ (row & 7)) << 4)),
+                               "f"(v[4 * q]), "f"(v[4 * q + 1]), "f"(v[4 * q + 2]), "f"(v[4 * q + 3])
+                               : "memory");
+              }
+            }
+            x_ml[row] = make_float2(m_ref, l_run);
+          }
+          __syncwarp();
+          if (lane == 0) bar_arrive(x_full);
+        } else {
+          __syncwarp();
+          if (lane == 0) bar_arrive(x_may);
+          if (!(ok = bar_wait(x_full, x_phase, &gave_up))) break;
+          if (active) {
+            const float2 ml = x_ml[row];
+            const bool none = ml.x == -INFINITY && ml.y == 0.f;
+            const float up = none ? m_ref : fmaxf(m_ref, ml.x);
+            mine_s = m_ref == -INFINITY ? (l_run == 0.f ? 0.f : 1.f) : ex2(m_ref - up);
+            other_s = none ? 0.f : ex2(ml.x - up);
+            other_l = ml.y;
+            l_run = l_run * mine_s + (none ? 0.f : other_l * other_s);
+            m_ref = up;
+          }
+        }
+      }
+      // the segment's share of this CTA: a partial, or the result where the share holds all its tiles
+      if (active && (w.both || st == 0)) {
+        const bool whole = !a.has_own && w.t0 == 0 && w.cnt == w.s.tiles;
+        const int64_t pr = part_row(a, blockIdx.x, w.s.own, w.s.id, x_begin < w.s.first) + (w.both ? st * 128 : 0) + row;
+        const int64_t ri = row < nrows ? row_index(a, w.s.h, row_off + r0 + row) : 0;
+        float inv = mine_s;
         if (row < nrows) {
           if (whole) {
-            inv = l_run == 0.f ? 0.f : 1.f / l_run;
+            const float n = l_run == 0.f ? 0.f : 1.f / l_run;
+            inv *= n;
+            other_s *= n;
             if (a.lse) a.lse[ri] = l_run > 0.f ? (m_ref + log2f(l_run)) * 0.6931471805599453f : (l_run == 0.f ? -INFINITY : l_run);
           } else {
             a.part_ml[pr] = make_float2(m_ref, l_run);
           }
         }
-        if (PV && any) {
+        if (PV) {
           float* dst = whole ? a.O + ri * D : a.part + pr * D;
-#pragma unroll
-          for (int j = 0; j < D / 32; ++j) {
-            float o[32];
-            tmem_ld32(to + 32 * j, o);
-            tmem_wait_ld();
+#pragma unroll 1
+          for (int j = 0; j < D; j += 32) {
+            float v[32];
+            tmem_ld32(to + j, v);
+            tmem_wait32(v);
             if (row < nrows) {
 #pragma unroll
-              for (int q = 0; q < 32; q += 4)
-                *reinterpret_cast<float4*>(dst + 32 * j + q) =
-                    make_float4(o[q] * inv, o[q + 1] * inv, o[q + 2] * inv, o[q + 3] * inv);
+              for (int q = 0; q < 8; ++q) {
+                float4 o = make_float4(v[4 * q] * inv, v[4 * q + 1] * inv, v[4 * q + 2] * inv, v[4 * q + 3] * inv);
+                if (join && other_s != 0.f) {
+                  float4 t;
+                  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                               : "=f"(t.x), "=f"(t.y), "=f"(t.z), "=f"(t.w)
+                               : "r"(xrow + ((((j >> 2) + q) ^ (row & 7)) << 4)));
+                  o.x = fmaf(t.x, other_s, o.x);
+                  o.y = fmaf(t.y, other_s, o.y);
+                  o.z = fmaf(t.z, other_s, o.z);
+                  o.w = fmaf(t.w, other_s, o.w);
+                }
+                *reinterpret_cast<float4*>(dst + j + 4 * q) = o;
+              }
             }
           }
         }
       }
+      if (join) {  // the next queries go where the rows lie
+        if (st == 0) {
+          __syncwarp();
+          if (lane == 0) bar_arrive(x_free);
+        }
+        if (!(ok = bar_wait(x_free, x_phase, &gave_up))) break;
+        x_phase ^= 1;
+      }
       tc_fence_before();
-      first_of_cta = false;
-      x = s.first + t1;
     }
   }
   tc_fence_before();
   __syncthreads();
   if (gave_up && tid == 0) raise_status(a.status, ZHA_ERR_TIMEOUT);
-  if (wid == 9) tmem_free(tm, 512);
+  if (wid == 11) tmem_free(tm, 512);
 }
 
 // ------------------------------------------------------------------ host side
@@ -509,17 +597,14 @@ cudaError_t launch_rows_tc(const RowsArgs& a, int d, cudaStream_t st) {
   return d == 128 ? run_tc<128, false>(a, maps, st) : run_tc<64, false>(a, maps, st);
 }
 
-// At most one CTA per SM, and none without a tile.  A row block of at most 128 rows has a partial per stream.
-void tc_plan(int hkv, int64_t B, int64_t rows, int64_t mg, int64_t n, int64_t ld_own, RowsPlan* p) {
-  p->kt = kTcKeys;
-  p->rb = kTcRows;
+void tc_plan(int64_t rows, int64_t mg, int64_t ld_own, RowsPlan* p) {
+  p->rb_log = 8;
+  p->kt_log = 7;
+  p->extra = 2;  // queries, first loads and the write-out of a segment take about as long as two tiles
   p->pp = int((rows + kTcRows - 1) / kTcRows);
   p->po = ld_own > 0 ? int((mg + kTcRows - 1) / kTcRows) : 0;
-  p->rp = rows > 128 ? kTcRows : int(2 * rows);
-  p->ro = mg > 128 ? kTcRows : int(2 * mg);
-  const double tiles = double(hkv) * p->pp * double((n + kTcKeys - 1) / kTcKeys) +
-                       double(B) * hkv * p->po * double((ld_own + kTcKeys - 1) / kTcKeys);
-  p->nc = tiles < 1 ? 1 : (tiles < 148 ? int(tiles) : 148);
+  p->rp = int(min64(rows, kTcRows));
+  p->ro = int(min64(mg, kTcRows));
 }
 
 }  // namespace zha

@@ -37,48 +37,47 @@ template <int D> struct WtShape {
 // Geometry of the flat list.  Up to 128 query heads of one KV head: a tile is `tok` whole tokens; more: 128 heads
 // of one token.
 struct WtPlan {
-  int tok, per_tok;    // tokens per tile, or tiles per token
-  int64_t tiles;       // row tiles of all m tokens
-  int64_t segs, full;  // segments per head; of these, the first `full` are seen by every row
-  int64_t head, all;   // list length of one head, of all
+  int tok, per_tok;  // tokens per tile, or tiles per token
+  int tiles;         // row tiles of all m tokens
+  int segs, full;    // segments per head; of these, the first `full` are seen by every row
+  int head;          // list length of one head
+  Shares sh;
 };
 
-__device__ __forceinline__ int64_t wt_first_tile(const WeightsArgs& a, const WtPlan& p, int64_t seg) {
+__device__ __forceinline__ int wt_first_tile(const WeightsArgs& a, const WtPlan& p, int seg) {
   if (!a.causal) return 0;
-  const int64_t tok = max64(0, seg * kWtKeys - (a.n - a.m));  // first token that sees the segment's first key
+  const int tok = int(max64(0, int64_t(seg) * kWtKeys - (a.n - a.m)));  // first token that sees the segment's first key
   return p.tok > 0 ? tok / p.tok : tok * p.per_tok;
 }
 
-__device__ __forceinline__ WtPlan wt_plan(const WeightsArgs& a) {
+__device__ __forceinline__ WtPlan wt_plan(const WeightsArgs& a, int nc) {
   WtPlan p;
   p.tok = a.group <= kWtCols ? kWtCols / a.group : 0;
   p.per_tok = a.group <= kWtCols ? 1 : (a.group + kWtCols - 1) / kWtCols;
-  p.tiles = p.tok > 0 ? (a.m + p.tok - 1) / p.tok : int64_t(a.m) * p.per_tok;
-  p.segs = (a.n + kWtKeys - 1) / kWtKeys;
-  p.full = a.causal ? min64(p.segs, (a.n - a.m) / kWtKeys + 1) : p.segs;
-  p.head = p.full * p.tiles +
-           warp_total(int(p.segs - p.full), [&](int i) { return p.tiles - wt_first_tile(a, p, p.full + i); });
-  p.all = p.head * a.hkv;
+  p.tiles = p.tok > 0 ? (a.m + p.tok - 1) / p.tok : a.m * p.per_tok;
+  p.segs = int((a.n + kWtKeys - 1) / kWtKeys);
+  p.full = a.causal ? min(p.segs, int((a.n - a.m) / kWtKeys) + 1) : p.segs;
+  p.head = p.full * p.tiles + warp_total(p.segs - p.full, [&](int i) { return p.tiles - wt_first_tile(a, p, p.full + i); });
+  p.sh.set(p.head * a.hkv, nc);
   return p;
 }
 
 struct WtSeg {
-  int h;
-  int64_t seg;
-  int64_t first, tiles;  // flat position and number of its tiles
-  int64_t t_first;       // its first row tile
+  int h, seg;
+  int first, tiles;  // place in the list and number of its tiles
+  int t_first;       // its first row tile
 };
 
-__device__ __forceinline__ WtSeg wt_find(const WeightsArgs& a, const WtPlan& p, int64_t x) {
+__device__ __forceinline__ WtSeg wt_find(const WeightsArgs& a, const WtPlan& p, int x) {
   WtSeg s;
-  s.h = int(x / p.head);
-  const int64_t r = x - s.h * p.head;
-  int64_t base;
+  s.h = x / p.head;
+  const int r = x - s.h * p.head;
+  int base;
   if (r < p.full * p.tiles) {
     s.seg = r / p.tiles;
     base = s.seg * p.tiles;
   } else {
-    const int i = warp_find(int(p.segs - p.full), [&](int q) { return p.tiles - wt_first_tile(a, p, p.full + q); },
+    const int i = warp_find(p.segs - p.full, [&](int q) { return p.tiles - wt_first_tile(a, p, p.full + q); },
                             r - p.full * p.tiles, &base);
     s.seg = p.full + i;
     base += p.full * p.tiles;
@@ -91,19 +90,18 @@ __device__ __forceinline__ WtSeg wt_find(const WeightsArgs& a, const WtPlan& p, 
 
 // Tokens, heads and number of rows of row tile t: column c is token tok0 + c / gw, head g0 + c % gw.
 struct WtTile {
-  int64_t tok0;
-  int g0, gw, cols;
+  int tok0, g0, gw, cols;
 };
-__device__ __forceinline__ WtTile wt_tile(const WeightsArgs& a, const WtPlan& p, int64_t t) {
+__device__ __forceinline__ WtTile wt_tile(const WeightsArgs& a, const WtPlan& p, int t) {
   WtTile w;
   if (p.tok > 0) {
     w.tok0 = t * p.tok;
     w.g0 = 0;
     w.gw = a.group;
-    w.cols = int(min64(p.tok, a.m - w.tok0)) * a.group;
+    w.cols = min(p.tok, a.m - w.tok0) * a.group;
   } else {
     w.tok0 = t / p.per_tok;
-    w.g0 = int(t - w.tok0 * p.per_tok) * kWtCols;
+    w.g0 = (t - w.tok0 * p.per_tok) * kWtCols;
     w.gw = kWtCols;
     w.cols = a.group - w.g0 < kWtCols ? a.group - w.g0 : kWtCols;
   }
@@ -166,9 +164,9 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
   const uint32_t tm = tmem_base;
   pdl_trigger();
   pdl_wait();
-  const WtPlan plan = wt_plan(a);
-  int64_t x = cta_first_tile(plan.all, gridDim.x, blockIdx.x);
-  const int64_t x_end = cta_first_tile(plan.all, gridDim.x, blockIdx.x + 1);
+  const WtPlan plan = wt_plan(a, gridDim.x);
+  const int x_begin = plan.sh.begin(blockIdx.x), x_end = plan.sh.begin(blockIdx.x + 1);
+  int x = x_begin;
 
   if (wid == 8) {  // ---------------------------------------------------------------- loads
     int slot = 0, ks = 0;
@@ -177,7 +175,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
     const uint32_t tile_bytes = uint32_t(wt_box_rows(a.group)) * D * 2;
     while (x < x_end && ok) {
       const WtSeg s = wt_find(a, plan, x);
-      const int64_t t1 = min64(s.first + s.tiles, x_end) - s.first;
+      const int t1 = min(s.first + s.tiles, x_end) - s.first;
       if (!(ok = bar_wait(k_empty(ks), (k_round & 1) ^ 1, &gave_up))) break;
       if (lane == 0) {
         bar_expect(k_full(ks), 2 * Sh::kHalf);
@@ -186,13 +184,13 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
 #pragma unroll
           for (int p = 0; p < PANELS; ++p)
             tma_load(k_sm + (2 * ks + st) * Sh::kHalf + p * 128 * 128, &maps.k, k_full(ks), p * 64,
-                     int(s.seg * kWtKeys + st * 128), s.h);
+                     s.seg * kWtKeys + st * 128, s.h);
       }
       if (++ks == 2) {
         ks = 0;
         ++k_round;
       }
-      for (int64_t t = x - s.first; t < t1; ++t) {
+      for (int t = x - s.first; t < t1; ++t) {
         const WtTile w = wt_tile(a, plan, s.t_first + t);
         if (!(ok = bar_wait(empty(slot), (round & 1) ^ 1, &gave_up))) break;
         if (lane == 0) {
@@ -200,10 +198,10 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
 #pragma unroll
           for (int p = 0; p < PANELS; ++p)
             tma_load(ring + slot * Sh::kHalf + p * 128 * 128, &maps.q, full(slot), p * 64,
-                     s.h * a.group + w.g0, int(w.tok0));
+                     s.h * a.group + w.g0, w.tok0);
         }
         for (int c = lane; c < kWtCols; c += 32)  // no row: every weight 2^-inf = 0
-          lse2[slot][c] = c < w.cols ? a.lse[(w.tok0 + c / w.gw) * a.hq + int64_t(s.h) * a.group + w.g0 + c % w.gw] *
+          lse2[slot][c] = c < w.cols ? a.lse[int64_t(w.tok0 + c / w.gw) * a.hq + s.h * a.group + w.g0 + c % w.gw] *
                                            1.4426950408889634f
                                      : INFINITY;
         __syncwarp();
@@ -228,9 +226,9 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
     bool ok = true;
     while (x < x_end && ok) {
       const WtSeg s = wt_find(a, plan, x);
-      const int64_t t1 = min64(s.first + s.tiles, x_end) - s.first;
+      const int t1 = min(s.first + s.tiles, x_end) - s.first;
       ok = bar_wait(k_full(ks), k_round & 1, &gave_up);
-      for (int64_t t = x - s.first; t < t1 && ok; ++t) {
+      for (int t = x - s.first; t < t1 && ok; ++t) {
         const WtTile w = wt_tile(a, plan, s.t_first + t);
         const uint32_t idesc = mma_idesc((w.cols + 15) / 16 * 16, false);
         ok = bar_wait(full(slot), round & 1, &gave_up);
@@ -238,11 +236,11 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
           if (!(ok = bar_wait(s_free(st, buf), (b_round & 1) ^ 1, &gave_up))) break;
           tc_fence_after();
           if (lane == 0) {
-            const uint32_t k = k_sm + (2 * ks + st) * Sh::kHalf, q = ring + slot * Sh::kHalf;
+            const uint32_t k = desc_low(k_sm + (2 * ks + st) * Sh::kHalf, 16), q = desc_low(ring + slot * Sh::kHalf, 16);
 #pragma unroll
             for (int e = 0; e < D / 16; ++e) {
               const uint32_t off = (e / 4) * (128 * 128) + (e % 4) * 32;
-              mma_ss(tm + st * 256 + buf * 128, mma_desc(k + off, 16), mma_desc(q + off, 16), idesc, e > 0);
+              mma_ss(tm + st * 256 + buf * 128, k + (off >> 4), q + (off >> 4), idesc, e > 0);
             }
             mma_commit(s_full(st, buf));
             if (st == 1) {
@@ -277,14 +275,14 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
     const float c2 = a.scale * 1.4426950408889634f;
     int slot = 0, buf = 0;
     uint32_t round = 0, b_round = 0;
-    bool ok = true, first_of_cta = true;
+    bool ok = true;
     while (x < x_end && ok) {
       const WtSeg s = wt_find(a, plan, x);
-      const int64_t t1 = min64(s.first + s.tiles, x_end) - s.first;
-      const int64_t k = s.seg * kWtKeys + st * 128 + key;
+      const int t1 = min(s.first + s.tiles, x_end) - s.first;
+      const int64_t k = int64_t(s.seg) * kWtKeys + st * 128 + key;
       const int64_t tok_min = a.causal ? k - (a.n - a.m) : 0;  // first token that sees this key
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int64_t t = x - s.first; t < t1; ++t) {
+      for (int t = x - s.first; t < t1; ++t) {
         const WtTile w = wt_tile(a, plan, s.t_first + t);
         // the log-sum-exps come with the tile's own barrier, the products with theirs
         if (!(ok = bar_wait(full(slot), round & 1, &gave_up))) break;
@@ -299,7 +297,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
         for (int j = 0; j < chunks; ++j) {
           float v[32];
           tmem_ld32(ts + 32 * j, v);
-          tmem_wait_ld();
+          tmem_wait32(v);
           const float4* l4 = reinterpret_cast<const float4*>(&lse2[slot][32 * j]);
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
@@ -340,9 +338,8 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
       if (x == s.first && t1 == s.tiles) {
         if (k < a.n) a.acc_out[s.h * a.ld_acc_out + k] = (a.acc_in ? a.acc_in[s.h * a.ld_acc_in + k] : 0.f) + total;
       } else {
-        a.sums[(int64_t(blockIdx.x) * 2 + (first_of_cta ? 0 : 1)) * kWtKeys + st * 128 + key] = total;
+        a.sums[(int64_t(blockIdx.x) * 2 + (x_begin < s.first ? 1 : 0)) * kWtKeys + st * 128 + key] = total;
       }
-      first_of_cta = false;
       x = s.first + t1;
     }
   }
@@ -355,18 +352,18 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
 // Segments cut by CTA borders: block c joins the one that begins in CTA c and ends in a later one.
 __global__ void __launch_bounds__(kWtKeys) weights_tc_join_kernel(WeightsArgs a) {
   pdl_wait();
-  const WtPlan plan = wt_plan(a);
   const int nc = gridDim.x, c = blockIdx.x;
-  const int64_t x0 = cta_first_tile(plan.all, nc, c), x1 = cta_first_tile(plan.all, nc, c + 1);
+  const WtPlan plan = wt_plan(a, nc);
+  const int x0 = plan.sh.begin(c), x1 = plan.sh.begin(c + 1);
   if (x0 >= x1) return;
   const WtSeg s = wt_find(a, plan, x1 - 1);
   if (s.first < x0 || s.first + s.tiles <= x1) return;
-  const int64_t k = s.seg * kWtKeys + threadIdx.x;
+  const int64_t k = int64_t(s.seg) * kWtKeys + threadIdx.x;
   if (k >= a.n) return;
-  const int last = tile_cta(plan.all, nc, s.first + s.tiles - 1);
+  const int last = plan.sh.owner(s.first + s.tiles - 1);
   float sum = 0.f;
-  for (int q = c; q <= last; ++q)  // it is every later CTA's first segment
-    if (!cta_empty(plan.all, nc, q)) sum += a.sums[(int64_t(q) * 2 + (q > c || s.first == x0 ? 0 : 1)) * kWtKeys + threadIdx.x];
+  for (int q = c; q <= last; ++q)  // it holds every later share's begin
+    sum += a.sums[(int64_t(q) * 2 + (q == c && x0 < s.first ? 1 : 0)) * kWtKeys + threadIdx.x];
   a.acc_out[s.h * a.ld_acc_out + k] = (a.acc_in ? a.acc_in[s.h * a.ld_acc_in + k] : 0.f) + sum;
 }
 
