@@ -11,16 +11,18 @@ namespace zha {
 
 // ------------------------------------------------------------------ selection
 // The keep - first - last largest sums among tokens [first, n - last), ties to
-// the lower token.  One cluster of 8 CTAs per KV head, each with a contiguous
-// eighth of the tokens.  The threshold is found most significant bits first, 11 +
-// 11 + 10 bits: shared-memory histograms, added over the cluster through distributed
-// shared memory (every CTA reads all eight, so no second exchange is needed).
-// Then each warp counts the tokens above and at the threshold in its own run of tokens, one scan over
-// warps and CTAs gives its output position, and it lists its kept tokens in order.
+// the lower token.  CTAS CTAs per KV head (one, or a cluster), each warp with a contiguous run of tokens.
+// The threshold is found most significant bits first, 11 + 11 + 10 bits: shared-memory histograms, added over the
+// cluster through distributed shared memory (every CTA reads all of them, so no second
+// exchange is needed).  Then each warp counts the tokens above and at the threshold in its run, one scan over warps
+// and CTAs gives its output position, and it lists its kept tokens in order.
+// The sums are read once: RK of them stay in each thread's registers as ordered keys (RK = 0: too many,
+// read again in each of the five passes, from L2).  What is left is latency: each pass ends in two
+// barriers and a scan.
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelCtas = 8;  // the portable cluster size
 constexpr int kSelBins = 2048;
+constexpr int kSelCluster = 8;  // the portable cluster size
 
 // Larger sum, larger key; NaN below everything; -0 equal to +0.
 __device__ __forceinline__ uint32_t evict_key(float x) {
@@ -28,29 +30,65 @@ __device__ __forceinline__ uint32_t evict_key(float x) {
   return float_to_ordered(x == 0.f ? 0.f : x);
 }
 
-__global__ void __cluster_dims__(kSelCtas, 1, 1) __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) {
-  cg::cluster_group cl = cg::this_cluster();
+template <int CTAS> __device__ __forceinline__ void sel_sync() {
+  if (CTAS > 1) cg::this_cluster().sync();
+  else __syncthreads();
+}
+
+// f(key, live) for each 32 tokens of a warp's run [t0, t1) in order; live: the lane has a token.
+template <int RK, typename F>
+__device__ __forceinline__ void sel_each(const uint32_t* regs, const float* mid, int t0, int t1, F f) {
+  const int lane = threadIdx.x & 31;
+  if (RK > 0) {
+#pragma unroll
+    for (int j = 0; j < RK; ++j) f(regs[j], t0 + 32 * j + lane < t1, t0 + 32 * j + lane);
+  } else {
+    for (int i0 = t0; i0 < t1; i0 += 256) {
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int i = i0 + 32 * j + lane;
+        v[j] = i < t1 ? __ldcg(mid + i) : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f(evict_key(v[j]), i0 + 32 * j + lane < t1, i0 + 32 * j + lane);
+    }
+  }
+}
+
+template <int CTAS, int RK> __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) {
   __shared__ uint32_t hist[kSelBins];
   __shared__ uint32_t wsum[kSelWarps];
-  __shared__ uint32_t found[2];                // bin of the threshold, tokens above it
+  __shared__ uint32_t found[2];  // bin of the threshold, tokens above it
   __shared__ uint32_t wgt[kSelWarps], weq[kSelWarps];
-  __shared__ uint32_t cta_cnt[2];              // tokens above / at the threshold of this CTA
-  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, rank = int(cl.block_rank());
-  const int h = blockIdx.x / kSelCtas;
-  const float* acc = a.acc + int64_t(h) * a.ld_acc;
+  __shared__ uint32_t cta_cnt[2];  // tokens above / at the threshold of this CTA
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int rank = CTAS > 1 ? int(cg::this_cluster().block_rank()) : 0;
+  const int h = blockIdx.x / CTAS;
   int32_t* out = a.idx + int64_t(h) * a.keep;
-  for (int64_t i = int64_t(rank) * kSelThreads + tid; i < a.first + a.last; i += int64_t(kSelCtas) * kSelThreads) {
+  pdl_trigger();
+  for (int64_t i = int64_t(rank) * kSelThreads + tid; i < a.first + a.last; i += int64_t(CTAS) * kSelThreads) {
     if (i < a.first) out[i] = int32_t(i);
     else out[a.keep - a.last + (i - a.first)] = int32_t(a.n - a.last + (i - a.first));
   }
-  const int64_t n_mid = a.n - a.first - a.last;
+  const int n_mid = int(a.n - a.first - a.last);
   uint32_t want = uint32_t(a.keep - a.first - a.last);  // tokens still to take at or below the current prefix
   if (want == 0) return;  // the same for every CTA of the cluster
   // a warp's run of tokens, a multiple of 32 so that its rows are whole warp iterations
-  const int64_t per = (n_mid + int64_t(kSelCtas) * kSelWarps * 32 - 1) / (int64_t(kSelCtas) * kSelWarps * 32) * 32;
-  const int64_t t0 = min64(n_mid, (int64_t(rank) * kSelWarps + wid) * per);
-  const int64_t t1 = min64(n_mid, t0 + per);
-  const float* mid = acc + a.first;
+  const int64_t per = (int64_t(n_mid) + CTAS * kSelWarps * 32 - 1) / (CTAS * kSelWarps * 32) * 32;
+  const int t0 = int(min64(n_mid, (int64_t(rank) * kSelWarps + wid) * per)), t1 = int(min64(n_mid, t0 + per));
+  const float* mid = a.acc + int64_t(h) * a.ld_acc + a.first;
+  uint32_t keys[RK > 0 ? RK : 1];
+  if (RK > 0) {
+    float v[RK > 0 ? RK : 1];
+#pragma unroll
+    for (int j = 0; j < RK; ++j) {
+      const int i = t0 + 32 * j + lane;
+      v[j] = i < t1 ? __ldcg(mid + i) : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < RK; ++j) keys[j] = evict_key(v[j]);
+  }
   uint32_t prefix = 0, mask = 0;
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
@@ -58,18 +96,18 @@ __global__ void __cluster_dims__(kSelCtas, 1, 1) __launch_bounds__(kSelThreads) 
     const uint32_t bins = pass == 2 ? 1024u : 2048u;
     for (int i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0u;
     __syncthreads();
-    for (int64_t i = t0 + lane; i < t1; i += 32) {
-      const uint32_t k = evict_key(__ldcg(mid + i));
-      if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1u);
-    }
-    cl.sync();
+    sel_each<RK>(keys, mid, t0, t1, [&](uint32_t k, bool live, int) {
+      if (live && (k & mask) == prefix) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1u);
+    });
+    sel_sync<CTAS>();
     // bins in descending order: thread t holds bins 2t and 2t + 1 from the top
     uint32_t v[2] = {0u, 0u};
 #pragma unroll
-    for (int q = 0; q < kSelCtas; ++q) {
-      const uint32_t* r = cl.map_shared_rank(hist, q);
-      v[0] += r[kSelBins - 1 - 2 * tid];
-      v[1] += r[kSelBins - 2 - 2 * tid];
+    for (int q = 0; q < CTAS; ++q) {
+      const uint32_t* r = CTAS > 1 ? cg::this_cluster().map_shared_rank(hist, q) : hist;
+      const uint2 two = *reinterpret_cast<const uint2*>(r + kSelBins - 2 - 2 * tid);
+      v[0] += two.y;
+      v[1] += two.x;
     }
     uint32_t inc = v[0] + v[1];
 #pragma unroll
@@ -79,18 +117,7 @@ __global__ void __cluster_dims__(kSelCtas, 1, 1) __launch_bounds__(kSelThreads) 
     }
     if (lane == 31) wsum[wid] = inc;
     __syncthreads();
-    uint32_t before = 0;
-    {
-      uint32_t w = wsum[lane];
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, w, off);
-        if (lane >= off) w += y;
-      }
-      const uint32_t up = __shfl_sync(0xffffffffu, w, (wid + 31) & 31);
-      before = wid == 0 ? 0u : up;
-    }
-    before += inc - v[0] - v[1];
+    uint32_t before = __reduce_add_sync(0xffffffffu, lane < wid ? wsum[lane] : 0u) + inc - v[0] - v[1];
     if (before < want && before + v[0] >= want) {
       found[0] = uint32_t(kSelBins - 1 - 2 * tid);
       found[1] = before;
@@ -98,64 +125,73 @@ __global__ void __cluster_dims__(kSelCtas, 1, 1) __launch_bounds__(kSelThreads) 
       found[0] = uint32_t(kSelBins - 2 - 2 * tid);
       found[1] = before + v[0];
     }
-    cl.sync();  // every CTA has read the histograms; `found` is visible to this CTA
+    sel_sync<CTAS>();  // every CTA has read the histograms; `found` is visible to this CTA
     prefix |= found[0] << shift;
     mask |= (bins - 1) << shift;
     want -= found[1];
-    __syncthreads();
   }
   // prefix is the threshold key; `want` of the tokens at it are kept, the lowest ones
   uint32_t gt = 0, eq = 0;
-  for (int64_t i = t0 + lane; i < t1; i += 32) {
-    const uint32_t k = evict_key(__ldcg(mid + i));
-    gt += k > prefix;
-    eq += k == prefix;
-  }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    gt += __shfl_xor_sync(0xffffffffu, gt, off);
-    eq += __shfl_xor_sync(0xffffffffu, eq, off);
-  }
+  sel_each<RK>(keys, mid, t0, t1, [&](uint32_t k, bool live, int) {
+    gt += live && k > prefix;
+    eq += live && k == prefix;
+  });
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
   if (lane == 0) {
     wgt[wid] = gt;
     weq[wid] = eq;
   }
   __syncthreads();
-  uint32_t g = wgt[lane], e = weq[lane], gsum = g, esum = e;
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    gsum += __shfl_xor_sync(0xffffffffu, gsum, off);
-    esum += __shfl_xor_sync(0xffffffffu, esum, off);
+  uint32_t gpre = __reduce_add_sync(0xffffffffu, lane < wid ? wgt[lane] : 0u);
+  uint32_t epre = __reduce_add_sync(0xffffffffu, lane < wid ? weq[lane] : 0u);
+  if (CTAS > 1) {
+    if (tid == kSelThreads - 1) {
+      cta_cnt[0] = gpre + gt;
+      cta_cnt[1] = epre + eq;
+    }
+    sel_sync<CTAS>();
+    for (int q = 0; q < rank; ++q) {
+      const uint32_t* r = cg::this_cluster().map_shared_rank(cta_cnt, q);
+      gpre += r[0];
+      epre += r[1];
+    }
   }
-  if (tid == 0) {
-    cta_cnt[0] = gsum;
-    cta_cnt[1] = esum;
-  }
-  uint32_t gpre = lane < wid ? g : 0u, epre = lane < wid ? e : 0u;
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    gpre += __shfl_xor_sync(0xffffffffu, gpre, off);
-    epre += __shfl_xor_sync(0xffffffffu, epre, off);
-  }
-  cl.sync();
-  for (int q = 0; q < rank; ++q) {
-    const uint32_t* r = cl.map_shared_rank(cta_cnt, q);
-    gpre += r[0];
-    epre += r[1];
-  }
-  for (int64_t i0 = t0; i0 < t1; i0 += 32) {
-    const int64_t i = i0 + lane;
-    const bool in = i < t1;
-    const uint32_t k = in ? evict_key(__ldcg(mid + i)) : 0u;
-    const bool is_gt = in && k > prefix, is_eq = in && k == prefix;
+  sel_each<RK>(keys, mid, t0, t1, [&](uint32_t k, bool live, int i) {
+    const bool is_gt = live && k > prefix, is_eq = live && k == prefix;
     const uint32_t bg = __ballot_sync(0xffffffffu, is_gt), be = __ballot_sync(0xffffffffu, is_eq);
     const uint32_t below = (1u << lane) - 1u;
     const uint32_t ge = gpre + __popc(bg & below), ee = epre + __popc(be & below);
     if (is_gt || (is_eq && ee < want)) out[a.first + ge + (ee < want ? ee : want)] = int32_t(a.first + i);
     gpre += __popc(bg);
     epre += __popc(be);
-  }
-  cl.sync();  // no CTA leaves while another reads its shared memory
+  });
+  if (CTAS > 1) sel_sync<CTAS>();  // no CTA leaves while another reads its shared memory
+}
+
+template <int CTAS, int RK> cudaError_t run_select(const EvictArgs& a, cudaStream_t st) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(unsigned(a.hkv) * CTAS);
+  c.blockDim = dim3(kSelThreads);
+  c.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = CTAS;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  c.attrs = at;
+  c.numAttrs = CTAS > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&c, evict_select_kernel<CTAS, RK>, a);
+}
+
+// One CTA where its registers hold all keys without waiting for a cluster; a cluster of eight above, its registers up to
+// 256K tokens.
+static cudaError_t launch_select(const EvictArgs& a, cudaStream_t st) {
+  const int64_t mid = a.n - a.first - a.last;
+  if (mid <= 4 * kSelThreads) return run_select<1, 4>(a, st);
+  if (mid <= 16 * kSelThreads) return run_select<1, 16>(a, st);
+  if (mid <= 8 * kSelThreads * kSelCluster) return run_select<kSelCluster, 8>(a, st);
+  if (mid <= 32 * kSelThreads * kSelCluster) return run_select<kSelCluster, 32>(a, st);
+  return run_select<kSelCluster, 0>(a, st);
 }
 
 // ------------------------------------------------------------------ moving the rows
@@ -167,6 +203,7 @@ constexpr int kMoveUnroll = 4;
 
 __global__ void __launch_bounds__(kMoveThreads) evict_gather_kernel(EvictArgs a) {
   const int h = blockIdx.y;
+  pdl_wait();
   const int cpr = a.row_bytes / 16;  // 16-byte pieces per row: 8, 16 or 32
   const int64_t pieces = a.keep * cpr;
   const int32_t* idx = a.idx + int64_t(h) * a.keep;
@@ -227,6 +264,7 @@ __global__ void __launch_bounds__(kSlideThreads) evict_slide_kernel(EvictArgs a)
   const int h = blockIdx.y, slices = a.row_bytes / 32;
   const int32_t* idx = a.idx + int64_t(h) * a.keep;
   const int x = blockIdx.x;
+  pdl_wait();
   if (x < 2 * slices) {
     const bool v = x >= slices;
     const int64_t off = int64_t(x - (v ? slices : 0)) * 32;
@@ -243,17 +281,13 @@ __global__ void __launch_bounds__(kSlideThreads) evict_slide_kernel(EvictArgs a)
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st) {
   count_launches(2);
-  evict_select_kernel<<<unsigned(a.hkv) * kSelCtas, kSelThreads, 0, st>>>(a);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_select(a, st);
   if (e != cudaSuccess) return e;
-  if (a.in_place) {
-    evict_slide_kernel<<<dim3(unsigned(a.row_bytes / 32 * 2 + 1), unsigned(a.hkv)), kSlideThreads, 0, st>>>(a);
-  } else {
-    const int64_t pieces = a.keep * (a.row_bytes / 16);
-    const unsigned gx = unsigned((pieces + kMoveThreads * kMoveUnroll - 1) / (kMoveThreads * kMoveUnroll));
-    evict_gather_kernel<<<dim3(gx, unsigned(a.hkv), 3), kMoveThreads, 0, st>>>(a);
-  }
-  return cudaGetLastError();
+  if (a.in_place)
+    return launch_after(evict_slide_kernel, dim3(unsigned(a.row_bytes / 32 * 2 + 1), unsigned(a.hkv)), kSlideThreads, 0, st, a);
+  const int64_t pieces = a.keep * (a.row_bytes / 16);
+  const unsigned gx = unsigned((pieces + kMoveThreads * kMoveUnroll - 1) / (kMoveThreads * kMoveUnroll));
+  return launch_after(evict_gather_kernel, dim3(gx, unsigned(a.hkv), 3), kMoveThreads, 0, st, a);
 }
 
 }  // namespace zha

@@ -27,6 +27,7 @@
 //
 // The code of a role runs a few times per launch when lengths are short, and its first run waits for its
 // instructions: loops over a row's 128 logits go in two rounds of 2 x 32 columns rather than unrolled.
+#include <climits>
 #include <cstring>
 
 #include "zha_rows.cuh"
@@ -37,6 +38,7 @@ namespace zha {
 constexpr int kTcKeys = 128;               // keys per tile
 constexpr int kTcThreads = 384;
 constexpr int kTcRows = 256;               // rows of a row block: two streams of 128
+constexpr int kTurnTiles = 4;              // segments of more tiles: the streams take turns
 constexpr float kLazyMax = 8.f;            // growth of the maximum (log2) that rescales O
 
 template <int D> struct TcShape {
@@ -79,7 +81,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
   using Sh = TcShape<D>;
   constexpr int NS = Sh::kSlots, PANELS = D / 64, PANEL = kTcKeys * 128;  // bytes of a 64-wide panel of a tile
   extern __shared__ uint8_t raw[];
-  __shared__ __align__(8) uint64_t bars[2 * NS + 15];
+  __shared__ __align__(8) uint64_t bars[2 * NS + 17];
   __shared__ float2 x_ml[128];  // stream 1's sums for the join
   __shared__ uint32_t tmem_base;
   __shared__ volatile int gave_up;
@@ -93,6 +95,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
   auto q_full = [&](int s) { return b0 + 8 * (2 * NS + 4 + s); };
   auto p_full = [&](int s, int half) { return b0 + 8 * (2 * NS + 6 + 2 * s + half); };
   const uint32_t fix = b0 + 8 * (2 * NS + 10), done = fix + 8, x_full = fix + 16, x_free = fix + 24, x_may = fix + 32;
+  auto turn = [&](int s) { return fix + 40 + 8 * s; };  // the other stream has weighed its tile
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
 
   if (wid == 11) {
@@ -113,6 +116,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
       bar_init(x_full, 4);
       bar_init(x_free, 4);
       bar_init(x_may, 4);
+      bar_init(turn(0), 4);
+      bar_init(turn(1), 4);
       gave_up = 0;
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -289,7 +294,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
     const uint32_t ts = tm + lane_base + st * 128, to = tm + lane_base + 256 + st * D;
     const float c2 = a.scale * 1.4426950408889634f;  // weights as powers of two
     const uint64_t cc = pair(c2, c2), minus = pair(-1.f, -1.f);
-    uint32_t s_phase = 0, o_phase = 0, x_phase = 0;
+    uint32_t s_phase = 0, o_phase = 0, x_phase = 0, t_phase = 0;
     bool ok = true;
     while (ok && next_work(a, tot, &x, x_end, &w)) {
       const int r0 = w.s.p * kTcRows + (w.both ? st * 128 : 0);  // the stream's first row
@@ -321,12 +326,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
       fence_async_smem();
       __syncwarp();
       if (lane == 0) bar_arrive(q_full(st));
-      const int lim = row >= nrows ? 0 : int(w.s.own ? own_limit(a, own_tokens(a, w.s.b), r0 + row) : prefix_limit(a, r0 + row));
+      // (padding rows: no limit, so that they never ask for the masked path)
+      const int lim = row >= nrows ? INT_MAX : int(w.s.own ? own_limit(a, own_tokens(a, w.s.b), r0 + row) : prefix_limit(a, r0 + row));
       const bool active = wrow < nrows;  // a warp of padding rows leaves its weights alone: they reach no valid row
       float m_ref = -INFINITY, l_run = 0.f;
       const int step = w.both ? 1 : 2, i0 = w.both ? 0 : st;
+      // Streams take turns: a tile may begin once the other stream has handed over half of its own.  Left alone they fall into
+      // step, and the tensor pipe idles while both weigh (256K tokens behind 64 sequences: 413 us, whole turns 400, half
+      // turns 380).
+      const bool turns = PV && w.cnt > kTurnTiles;
 #pragma unroll 1
       for (int i = i0; i < w.cnt; i += step) {
+        if (turns && (st || i != i0)) {
+          if (!(ok = bar_wait(turn(st), t_phase, &gave_up))) break;
+          t_phase ^= 1;
+        }
         if (!(ok = bar_wait(s_full(st), s_phase, &gave_up))) break;
         s_phase ^= 1;
         tc_fence_after();
@@ -345,19 +359,26 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
             return m;
           };
           float mx = -INFINITY;
-          tmem_ld32(ts, va);
-          tmem_wait32(va);
-#pragma unroll 1
-          for (int j = 0; j < kTcKeys; j += 64) {  // one chunk is loaded while the other is looked at
-            tmem_ld32(ts + j + 32, vb);
-            if (mask) hide(va, j);
-            mx = largest(va, mx);
-            tmem_wait32(vb);
-            tmem_ld32(ts + ((j + 64) & (kTcKeys - 1)), va);  // last: the first chunk again, for the exponentials
-            if (mask) hide(vb, j + 32);
-            mx = largest(vb, mx);
+          {
+            float vc[32], vd[32];
+            tmem_ld32(ts, va);
+            tmem_ld32(ts + 32, vb);
+            tmem_ld32(ts + 64, vc);
+            tmem_ld32(ts + 96, vd);
             tmem_wait32(va);
+            tmem_wait32(vb);
+            tmem_wait32(vc);
+            tmem_wait32(vd);
+            if (mask) {
+              hide(va, 0);
+              hide(vb, 32);
+              hide(vc, 64);
+              hide(vd, 96);
+            }
+            mx = largest(vd, largest(vc, mx));
+            mx = fmaxf(mx, largest(vb, largest(va, -INFINITY)));
           }
+          tmem_ld32(ts, va);  // again, chunk by chunk, for the exponentials
           const float m_new = mx * c2;
           const bool grow = m_new > m_ref + kLazyMax || (m_ref == -INFINITY && m_new > -INFINITY);
           if (__any_sync(0xffffffffu, grow)) {
@@ -403,6 +424,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
           };
 #pragma unroll 1
           for (int j = 0; j < kTcKeys; j += 64) {
+            tmem_wait32(va);
             tmem_ld32(ts + j + 32, vb);
             if (mask) hide(va, j);
             weigh(va, j);
@@ -410,11 +432,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
             if (j == 0) tmem_ld32(ts + 64, va);
             if (mask) hide(vb, j + 32);
             weigh(vb, j + 32);
-            if (j == 0) tmem_wait32(va);
             if (PV) tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0 && (PV || j)) bar_arrive(p_full(st, PV ? j >> 6 : 0));
+            if (lane == 0) {
+              if (PV || j) bar_arrive(p_full(st, PV ? j >> 6 : 0));
+              if (turns && j == 0) bar_arrive(turn(st ^ 1));
+            }
           }
           float s0, s1;
           unpair(add2(sum[0], sum[1]), &s0, &s1);
@@ -425,8 +449,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
           if (lane == 0) {
             bar_arrive(p_full(st, 0));
             if (PV) bar_arrive(p_full(st, 1));
+            if (turns) bar_arrive(turn(st ^ 1));
           }
         }
+      }
+      // turns of the other stream that this one has no tile to wait for: the last one of stream 1, for stream 0 and of
+      // stream 0 for a stream 1 with one tile less
+      if (ok && turns && (st == 0 ? w.both || !(w.cnt & 1) : !w.both && (w.cnt & 1))) {
+        if (!(ok = bar_wait(turn(st), t_phase, &gave_up))) break;
+        t_phase ^= 1;
       }
       if (!ok) break;
       if (PV || i0 >= w.cnt) {  // also without work: the stream stays within one segment of its products' warp
