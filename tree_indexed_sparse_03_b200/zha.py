@@ -262,11 +262,13 @@ class ZhaTree:
         see cache_evict) and rebuild the tree over them.  Returns the kept tokens' positions [Hkv, keep] int32."""
         c = self.cfg
         n = self.size
-        ld_acc = _check_sums("acc", acc, c, n)
-        _check_device(("acc", acc), ("K", self.K))
         if not 1 <= keep <= n:
             raise ValueError(f"keep must be in [1, {n}]")
-        idx = _empty((c.n_kv_heads, keep), torch.int32, acc.device, stream)
+        ld_acc = _sums_ld("acc", acc, c.n_kv_heads, n)
+        dev = torch.cuda.current_device()
+        if acc.get_device() != dev or self.K.get_device() != dev:
+            _refuse_device("the cache and acc")
+        idx = _empty(acc, (c.n_kv_heads, keep), torch.int32, stream)
         _check(lib().zha_tree_evict(self._h, acc.data_ptr(), ld_acc, keep, first, last, idx.data_ptr(),
                                     _stream(stream)))
         return idx
@@ -348,50 +350,64 @@ def dense_decode(cfg: ZhaConfig, K: torch.Tensor, V: torch.Tensor, n: int, Q: to
 
 # ---------------------------------------------------------------- shared prefix, weights, eviction
 # These entry points take tensors as they lie (row strides included) and never copy them; every tensor must be on
-# the current CUDA device.  Outputs they allocate belong to the stream the call runs on.
+# the current CUDA device.  Outputs they allocate belong to the stream the call runs on.  A short call takes the GPU
+# about ten microseconds, so the checks read each tensor's attributes once.
 
-def _empty(shape, dtype, device, stream) -> torch.Tensor:
+_F32 = torch.float32
+
+
+def _raw_stream(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _empty(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _check_device(*named) -> None:
-    dev = torch.cuda.current_device()
-    for name, t in named:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{name} must be on the current CUDA device (cuda:{dev})")
+def _refuse_device(name: str):
+    raise ValueError(f"{name} must be on the current CUDA device (cuda:{torch.cuda.current_device()})")
 
 
-def _check_cache(name: str, t: torch.Tensor, cfg: ZhaConfig, lead: Tuple[int, ...]) -> int:
-    """Row stride in tokens of a cache tensor [*lead, tokens, d] whose heads may be slices of longer ones."""
-    d, dt = cfg.d, TORCH_DTYPE[cfg.dtype]
-    if t.dtype != dt or not t.is_cuda or t.dim() != len(lead) + 2 or t.shape[:-2] != lead or t.shape[-1] != d:
-        raise ValueError(f"{name} must be a CUDA {dt} tensor {[*lead, 'tokens', d]}")
+def _cache_ld(name: str, t: torch.Tensor, hkv: int, d: int, dt, tokens: int) -> int:
+    """Row stride in tokens of a cache tensor [hkv, >= tokens, d] whose heads may be slices of longer ones."""
+    if t.dtype is not dt or t.dim() != 3 or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA {dt} tensor [{hkv}, >= {tokens}, {d}]")
+    h, have, dd = t.shape
+    if h != hkv or dd != d or have < tokens:
+        raise ValueError(f"{name} must be a CUDA {dt} tensor [{hkv}, >= {tokens}, {d}]")
     if t.is_contiguous():
-        return t.shape[-2]
-    st = t.stride()
-    ld = st[-3] // d if lead[-1] > 1 else (st[0] // (lead[-1] * d) if len(lead) > 1 and lead[0] > 1 else t.shape[-2])
-    if (st[-1] != 1 or st[-2] != d or ld < t.shape[-2] or (lead[-1] > 1 and st[-3] != ld * d)
-            or (len(lead) > 1 and lead[0] > 1 and st[0] != lead[-1] * ld * d)):
+        return have
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or s1 != d or (h > 1 and (s0 % d or s0 < have * d)):
         raise ValueError(f"{name} must have contiguous rows, one after another, and heads a whole number of rows apart")
-    return ld
+    return s0 // d if h > 1 else have
 
 
-def _check_sums(name: str, t: torch.Tensor, cfg: ZhaConfig, n: int) -> int:
-    """Row stride of per-token sums [Hkv, >= n] fp32."""
-    if t.dtype != torch.float32 or not t.is_cuda or t.dim() != 2 or t.shape[0] != cfg.n_kv_heads or t.shape[1] < n:
-        raise ValueError(f"{name} must be a CUDA float32 tensor [{cfg.n_kv_heads}, >= {n}]")
+def _same_layout(a: str, x: torch.Tensor, b: str, y: torch.Tensor, ld: int, hkv: int, d: int, dt, tokens: int) -> None:
+    if _cache_ld(b, y, hkv, d, dt, tokens) != ld or x.shape[1] != y.shape[1]:
+        raise ValueError(f"{a} and {b} must have the same shape and strides")
+
+
+def _sums_ld(name: str, t: torch.Tensor, hkv: int, n: int) -> int:
+    """Row stride of per-token sums [hkv, >= n] fp32."""
+    if t.dtype is not _F32 or t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA float32 tensor [{hkv}, >= {n}]")
+    h, have = t.shape
+    if h != hkv or have < n:
+        raise ValueError(f"{name} must be a CUDA float32 tensor [{hkv}, >= {n}]")
     if t.is_contiguous():
-        return t.shape[1]
-    if t.stride(1) != 1 or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        return have
+    s0, s1 = t.stride()
+    if s1 != 1 or (h > 1 and s0 < have):
         raise ValueError(f"{name} must have contiguous rows")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return s0 if h > 1 else have
 
 
 def _check_out(name: str, t: torch.Tensor, shape) -> None:
-    if t.shape != shape or t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous():
+    if t.shape != shape or t.dtype is not _F32 or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA float32 tensor {list(shape)}")
 
 
@@ -403,7 +419,31 @@ def _new_scratch(nbytes: int, device) -> torch.Tensor:
     return scratch
 
 
-class PrefixDecoder:
+class _Attend:
+    """What PrefixDecoder and DenseWeights share: the configuration's fields, a workspace, its status."""
+
+    def __init__(self, cfg: ZhaConfig, nbytes: int, device):
+        self.cfg = cfg
+        self._cfg = ctypes.byref(cfg)
+        self._shape = (cfg.n_kv_heads, cfg.d, TORCH_DTYPE[cfg.dtype])
+        self.scratch = _new_scratch(nbytes, device)
+        self._device = self.scratch.get_device()
+        self._scratch = (self.scratch.data_ptr(), self.scratch.numel())
+
+    def _check_q(self, Q: torch.Tensor, dims, lead: str):
+        c = self.cfg
+        dt = TORCH_DTYPE[c.dtype]
+        shape = Q.shape
+        if (Q.dtype is not dt or not Q.is_cuda or not Q.is_contiguous() or len(shape) not in dims or shape[-1] != c.d
+                or shape[-2] != c.n_q_heads):
+            raise ValueError(f"Q must be a contiguous CUDA {dt} tensor {lead.format(c.n_q_heads, c.d)}")
+        return shape
+
+    def status(self, stream=None) -> None:
+        _check(lib().zha_scratch_status(self.scratch.data_ptr(), _stream(stream)))
+
+
+class PrefixDecoder(_Attend):
     """Attention of up to B sequences x m query tokens over a shared prefix of up to n_max tokens and own caches of up
     to own_max tokens (zha_prefix_decode), with a workspace of its own.
 
@@ -412,9 +452,7 @@ class PrefixDecoder:
     """
 
     def __init__(self, cfg: ZhaConfig, B: int, n_max: int, own_max: int = 0, m: int = 1, device="cuda"):
-        self.cfg = cfg
-        self._cfg = ctypes.byref(cfg)
-        self.scratch = _new_scratch(int(lib().zha_prefix_scratch_bytes(self._cfg, B, m, n_max, own_max)), device)
+        super().__init__(cfg, int(lib().zha_prefix_scratch_bytes(ctypes.byref(cfg), B, m, n_max, own_max)), device)
         self.B, self.m, self.n_max, self.own_max = B, m, n_max, own_max
 
     def __call__(self, K: Optional[torch.Tensor], V: Optional[torch.Tensor], n: int, Q: torch.Tensor,
@@ -422,54 +460,59 @@ class PrefixDecoder:
                  own_len: Optional[torch.Tensor] = None, *, out=None, want_lse: bool = False, stream=None):
         """Q [B, m, Hq, d] (or [B, Hq, d]); K, V [Hkv, >= n, d] (None for n = 0); K_own, V_own [B, Hkv, >= own_len, d]
         with own_len [B] int32, or all three None.  Returns O fp32 of Q's shape, or (O, lse of Q's shape but d)."""
-        c = self.cfg
-        shape = Q.shape
-        if (Q.dtype != TORCH_DTYPE[c.dtype] or not Q.is_cuda or not Q.is_contiguous() or Q.dim() not in (3, 4)
-                or shape[-1] != c.d or shape[-2] != c.n_q_heads):
-            raise ValueError(f"Q must be a contiguous CUDA {TORCH_DTYPE[c.dtype]} tensor [B, m, {c.n_q_heads}, {c.d}] "
-                             f"or [B, {c.n_q_heads}, {c.d}]")
+        shape = self._check_q(Q, (3, 4), "[B, m, {0}, {1}] or [B, {0}, {1}]")
+        hkv, d, dt = self._shape
+        dev = self._device
+        if torch.cuda.current_device() != dev:
+            _refuse_device("the workspace")
+        if Q.get_device() != dev:
+            _refuse_device("Q")
         B, m = shape[0], shape[1] if len(shape) == 4 else 1
         ld = ld_own = 0
+        k = v = ko = vo = ln = None
         if n:
             if K is None or V is None:
                 raise ValueError("n > 0 needs K and V")
-            ld = _check_cache("K", K, c, (c.n_kv_heads,))
-            if _check_cache("V", V, c, (c.n_kv_heads,)) != ld or K.shape != V.shape:
-                raise ValueError("K and V must have the same shape and strides")
-            if not 0 <= n <= K.shape[1]:
-                raise ValueError(f"n must be in [0, {K.shape[1]}]")
-        if K_own is not None and K_own.shape[-2] > 0:
+            if n < 0:
+                raise ValueError("n must be >= 0")
+            ld = _cache_ld("K", K, hkv, d, dt, n)
+            _same_layout("K", K, "V", V, ld, hkv, d, dt, n)
+            if K.get_device() != dev or V.get_device() != dev:
+                _refuse_device("K and V")
+            k, v = K.data_ptr(), V.data_ptr()
+        if K_own is not None:
             if V_own is None or own_len is None:
                 raise ValueError("K_own, V_own and own_len go together")
-            ld_own = _check_cache("K_own", K_own, c, (B, c.n_kv_heads))
-            if _check_cache("V_own", V_own, c, (B, c.n_kv_heads)) != ld_own or K_own.shape != V_own.shape:
-                raise ValueError("K_own and V_own must have the same shape and strides")
-            if ld_own != K_own.shape[-2]:
-                raise ValueError("K_own and V_own must be contiguous: own_len bounds them")
-            if own_len.shape != (B,) or own_len.dtype != torch.int32 or not own_len.is_cuda or not own_len.is_contiguous():
+            own_shape = K_own.shape
+            if (len(own_shape) != 4 or own_shape[0] != B or own_shape[1] != hkv or own_shape[3] != d
+                    or V_own.shape != own_shape or K_own.dtype is not dt or V_own.dtype is not dt
+                    or not K_own.is_contiguous() or not V_own.is_contiguous()):
+                raise ValueError(f"K_own and V_own must be contiguous CUDA {dt} tensors [{B}, {hkv}, tokens, {d}]")
+            if own_len.dtype is not torch.int32 or own_len.shape != (B,) or not own_len.is_contiguous():
                 raise ValueError(f"own_len must be a contiguous CUDA int32 tensor [{B}]")
-        elif (K_own is None) != (V_own is None) or (K_own is None) != (own_len is None):
+            if K_own.get_device() != dev or V_own.get_device() != dev or own_len.get_device() != dev:
+                _refuse_device("K_own, V_own and own_len")
+            ld_own = own_shape[2]
+            if ld_own:
+                ko, vo, ln = K_own.data_ptr(), V_own.data_ptr(), own_len.data_ptr()
+        elif V_own is not None or own_len is not None:
             raise ValueError("K_own, V_own and own_len go together")
         if B > self.B or m > self.m or n > self.n_max or ld_own > self.own_max:
             raise ValueError(f"the decoder was made for B <= {self.B}, m <= {self.m}, n <= {self.n_max} and own caches "
                              f"of at most {self.own_max} tokens")
-        if out is not None:
+        if out is None:
+            out = _empty(Q, shape, _F32, stream)
+        else:
             _check_out("out", out, shape)
-        _check_device(("Q", Q), ("K", K), ("V", V), ("K_own", K_own), ("V_own", V_own), ("own_len", own_len),
-                      ("out", out), ("the workspace", self.scratch))
-        O = out if out is not None else _empty(shape, torch.float32, Q.device, stream)
-        lse = _empty(shape[:-1], torch.float32, Q.device, stream) if want_lse else None
-        if Q.numel() == 0:
-            return (O, lse) if want_lse else O
-        own = ld_own > 0
-        _check(lib().zha_prefix_decode(self._cfg, K.data_ptr() if n else None, V.data_ptr() if n else None, ld, n,
-                                       K_own.data_ptr() if own else None, V_own.data_ptr() if own else None, ld_own,
-                                       own_len.data_ptr() if own else None, Q.data_ptr(), O.data_ptr(), _ptr(lse), B, m,
-                                       self.scratch.data_ptr(), self.scratch.numel(), _stream(stream)))
-        return (O, lse) if want_lse else O
-
-    def status(self, stream=None) -> None:
-        _check(lib().zha_scratch_status(self.scratch.data_ptr(), _stream(stream)))
+            if out.get_device() != dev:
+                _refuse_device("out")
+        lse = _empty(Q, shape[:-1], _F32, stream) if want_lse else None
+        if B and m:
+            rc = lib().zha_prefix_decode(self._cfg, k, v, ld, n, ko, vo, ld_own, ln, Q.data_ptr(), out.data_ptr(),
+                                         _ptr(lse), B, m, *self._scratch, _raw_stream(stream, dev))
+            if rc:
+                _check(rc)
+        return (out, lse) if want_lse else out
 
 
 def prefix_decode(cfg: ZhaConfig, K, V, n: int, Q: torch.Tensor, K_own=None, V_own=None, own_len=None, *,
@@ -483,54 +526,61 @@ def prefix_decode(cfg: ZhaConfig, K, V, n: int, Q: torch.Tensor, K_own=None, V_o
     return res
 
 
-class DenseWeights:
+class DenseWeights(_Attend):
     """Dense attention of up to m query tokens over up to n_max tokens that adds up every token's attention weight
     (zha_dense_weights), with a workspace of its own (as for PrefixDecoder)."""
 
     def __init__(self, cfg: ZhaConfig, m: int, n_max: int, device="cuda"):
-        self.cfg = cfg
-        self._cfg = ctypes.byref(cfg)
+        super().__init__(cfg, int(lib().zha_weights_scratch_bytes(ctypes.byref(cfg), m, n_max)), device)
         self.m, self.n_max = m, n_max
-        self.scratch = _new_scratch(int(lib().zha_weights_scratch_bytes(self._cfg, m, n_max)), device)
 
     def __call__(self, K: torch.Tensor, V: Optional[torch.Tensor], n: int, Q: torch.Tensor,
                  acc: Optional[torch.Tensor] = None, *, causal: bool = False, acc_out: Optional[torch.Tensor] = None,
                  out=None, stream=None):
         """Q [m, Hq, d]; K, V [Hkv, >= n, d]; acc [Hkv, >= n] fp32 the sums so far (None: zeros).  Returns (O fp32 of
         Q's shape, acc_out [Hkv, n] = acc + the weights); V None leaves O out (None).  acc_out may be acc."""
-        c = self.cfg
-        if (Q.dtype != TORCH_DTYPE[c.dtype] or not Q.is_cuda or not Q.is_contiguous() or Q.dim() != 3
-                or Q.shape[-1] != c.d or Q.shape[-2] != c.n_q_heads):
-            raise ValueError(f"Q must be a contiguous CUDA {TORCH_DTYPE[c.dtype]} tensor [m, {c.n_q_heads}, {c.d}]")
-        m = Q.shape[0]
-        ld = _check_cache("K", K, c, (c.n_kv_heads,))
-        if V is not None and (_check_cache("V", V, c, (c.n_kv_heads,)) != ld or K.shape != V.shape):
-            raise ValueError("K and V must have the same shape and strides")
-        if not 1 <= n <= K.shape[1]:
-            raise ValueError(f"n must be in [1, {K.shape[1]}]")
+        shape = self._check_q(Q, (3,), "[m, {0}, {1}]")
+        hkv, d, dt = self._shape
+        dev = self._device
+        if torch.cuda.current_device() != dev:
+            _refuse_device("the workspace")
+        m = shape[0]
+        if n < 1:
+            raise ValueError("n must be >= 1")
+        ld = _cache_ld("K", K, hkv, d, dt, n)
+        if Q.get_device() != dev or K.get_device() != dev:
+            _refuse_device("Q and K")
         if not 1 <= m <= self.m or n > self.n_max:
             raise ValueError(f"the workspace was made for 1 <= m <= {self.m} and n <= {self.n_max}")
-        ld_in = _check_sums("acc", acc, c, n) if acc is not None else 0
-        if acc_out is None:
-            acc_out = _empty((c.n_kv_heads, n), torch.float32, Q.device, stream)
-        ld_out = _check_sums("acc_out", acc_out, c, n)
-        if V is None:
-            if out is not None:
-                raise ValueError("out needs V")
+        v = o = None
+        if V is not None:
+            _same_layout("K", K, "V", V, ld, hkv, d, dt, n)
+            if out is None:
+                out = _empty(Q, shape, _F32, stream)
+            else:
+                _check_out("out", out, shape)
+            if V.get_device() != dev or out.get_device() != dev:
+                _refuse_device("V and out")
+            v, o = V.data_ptr(), out.data_ptr()
         elif out is not None:
-            _check_out("out", out, Q.shape)
-        _check_device(("Q", Q), ("K", K), ("V", V), ("acc", acc), ("acc_out", acc_out), ("out", out),
-                      ("the workspace", self.scratch))
-        O = out
-        if V is not None and out is None:
-            O = _empty(Q.shape, torch.float32, Q.device, stream)
-        _check(lib().zha_dense_weights(self._cfg, K.data_ptr(), _ptr(V), ld, n, Q.data_ptr(), _ptr(O), m,
-                                       1 if causal else 0, _ptr(acc), ld_in, acc_out.data_ptr(), ld_out,
-                                       self.scratch.data_ptr(), self.scratch.numel(), _stream(stream)))
-        return O, acc_out
-
-    def status(self, stream=None) -> None:
-        _check(lib().zha_scratch_status(self.scratch.data_ptr(), _stream(stream)))
+            raise ValueError("out needs V")
+        a, ld_in = None, 0
+        if acc is not None:
+            ld_in = _sums_ld("acc", acc, hkv, n)
+            if acc.get_device() != dev:
+                _refuse_device("acc")
+            a = acc.data_ptr()
+        if acc_out is None:
+            acc_out, ld_out = _empty(Q, (hkv, n), _F32, stream), n
+        else:
+            ld_out = _sums_ld("acc_out", acc_out, hkv, n)
+            if acc_out.get_device() != dev:
+                _refuse_device("acc_out")
+        rc = lib().zha_dense_weights(self._cfg, K.data_ptr(), v, ld, n, Q.data_ptr(), o, m, 1 if causal else 0, a, ld_in,
+                                     acc_out.data_ptr(), ld_out, *self._scratch, _raw_stream(stream, dev))
+        if rc:
+            _check(rc)
+        return out, acc_out
 
 
 def cache_evict(cfg: ZhaConfig, K: torch.Tensor, V: torch.Tensor, n: int, acc: torch.Tensor, keep: int, *,
@@ -539,32 +589,40 @@ def cache_evict(cfg: ZhaConfig, K: torch.Tensor, V: torch.Tensor, n: int, acc: t
     """Shorten a cache K, V [Hkv, >= n, d] to `keep` tokens per head: the first `first`, the last `last` and those with
     the largest sums acc [Hkv, >= n] between (zha_cache_evict).  K_out and V_out [Hkv, >= keep, d] both None: in
     place, the sums too unless acc_out is given.  Returns (kept positions [Hkv, keep] int32, acc_out)."""
-    ld = _check_cache("K", K, cfg, (cfg.n_kv_heads,))
-    if _check_cache("V", V, cfg, (cfg.n_kv_heads,)) != ld or K.shape != V.shape:
-        raise ValueError("K and V must have the same shape and strides")
-    if not 1 <= n <= K.shape[1]:
-        raise ValueError(f"n must be in [1, {K.shape[1]}]")
+    hkv, d, dt = cfg.n_kv_heads, cfg.d, TORCH_DTYPE[cfg.dtype]
+    if n < 1:
+        raise ValueError("n must be >= 1")
     if not 1 <= keep <= n:
         raise ValueError(f"keep must be in [1, {n}]")
-    ld_acc = _check_sums("acc", acc, cfg, n)
-    if (K_out is None) != (V_out is None):
-        raise ValueError("K_out and V_out go together")
+    ld = _cache_ld("K", K, hkv, d, dt, n)
+    _same_layout("K", K, "V", V, ld, hkv, d, dt, n)
+    ld_acc = _sums_ld("acc", acc, hkv, n)
+    dev = torch.cuda.current_device()
+    if K.get_device() != dev or V.get_device() != dev or acc.get_device() != dev:
+        _refuse_device("K, V and acc")
     if K_out is None:
+        if V_out is not None:
+            raise ValueError("K_out and V_out go together")
         K_out, V_out, ld_out = K, V, ld
         if acc_out is None:
             acc_out = acc
     else:
-        ld_out = _check_cache("K_out", K_out, cfg, (cfg.n_kv_heads,))
-        if _check_cache("V_out", V_out, cfg, (cfg.n_kv_heads,)) != ld_out or K_out.shape != V_out.shape:
-            raise ValueError("K_out and V_out must have the same shape and strides")
-        if K_out.shape[1] < keep:
-            raise ValueError(f"K_out and V_out must hold {keep} tokens per head")
-        if acc_out is None:
-            acc_out = _empty((cfg.n_kv_heads, keep), torch.float32, acc.device, stream)
-    ld_acc_out = _check_sums("acc_out", acc_out, cfg, keep)
-    _check_device(("K", K), ("V", V), ("acc", acc), ("K_out", K_out), ("V_out", V_out), ("acc_out", acc_out))
-    idx = _empty((cfg.n_kv_heads, keep), torch.int32, acc.device, stream)
-    _check(lib().zha_cache_evict(ctypes.byref(cfg), K.data_ptr(), V.data_ptr(), ld, n, acc.data_ptr(), ld_acc, keep,
-                                 first, last, K_out.data_ptr(), V_out.data_ptr(), ld_out, acc_out.data_ptr(),
-                                 ld_acc_out, idx.data_ptr(), _stream(stream)))
+        if V_out is None:
+            raise ValueError("K_out and V_out go together")
+        ld_out = _cache_ld("K_out", K_out, hkv, d, dt, keep)
+        _same_layout("K_out", K_out, "V_out", V_out, ld_out, hkv, d, dt, keep)
+        if K_out.get_device() != dev or V_out.get_device() != dev:
+            _refuse_device("K_out and V_out")
+    if acc_out is None:
+        acc_out, ld_acc_out = _empty(acc, (hkv, keep), _F32, stream), keep
+    else:
+        ld_acc_out = _sums_ld("acc_out", acc_out, hkv, keep)
+        if acc_out.get_device() != dev:
+            _refuse_device("acc_out")
+    idx = _empty(acc, (hkv, keep), torch.int32, stream)
+    rc = lib().zha_cache_evict(ctypes.byref(cfg), K.data_ptr(), V.data_ptr(), ld, n, acc.data_ptr(), ld_acc, keep, first,
+                               last, K_out.data_ptr(), V_out.data_ptr(), ld_out, acc_out.data_ptr(), ld_acc_out,
+                               idx.data_ptr(), _raw_stream(stream, dev))
+    if rc:
+        _check(rc)
     return idx, acc_out
