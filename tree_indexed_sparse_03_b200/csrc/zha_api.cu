@@ -665,6 +665,9 @@ int zha_prefix_decode(const zha_config* cfg, const void* K, const void* V, int64
 }
 
 // Scratch of zha_dense_weights: status, partials, the rows' log-sum-exp, the row splits' column sums.
+// (or the kept logits).
+static int64_t logits_ld(int64_t n) { return (n + 3) & ~int64_t(3); }
+
 static int weights_layout(const zha_config* cfg, int32_t m, int64_t n, RowsPlan* rp, WeightsPlan* wp, uint64_t* lse_off,
                           uint64_t* sums_off, uint64_t* bytes) {
   int rc = prefix_plan(cfg, 1, m, n, 0, rp);
@@ -675,6 +678,7 @@ static int weights_layout(const zha_config* cfg, int32_t m, int64_t n, RowsPlan*
   if (wp->places >= double(1 << 30)) return fail(ZHA_ERR_UNSUPPORTED, "too many (query, key) pairs for one call");
   *lse_off = kScratchHead + rows_part_bytes(cfg, 1, m, *rp);
   *sums_off = align256(*lse_off + uint64_t(m) * cfg->n_q_heads * 4);
+  if (rows <= kLogitRows) wp->sum_floats = uint64_t(cfg->n_kv_heads) * rows * logits_ld(n);
   *bytes = align256(*sums_off + wp->sum_floats * 4);
   return ZHA_OK;
 }
@@ -684,8 +688,12 @@ size_t zha_weights_scratch_bytes(const zha_config* cfg, int32_t m, int64_t n) {
   WeightsPlan wp;
   uint64_t lse_off, sums_off, bytes;
   if (weights_layout(cfg, m, n, &rp, &wp, &lse_off, &sums_off, &bytes)) return 0;
+  // the calls of fewest query tokens are those that keep their logits
+  const int64_t group = cfg->n_q_heads / cfg->n_kv_heads, few = min64(m, kLogitRows / group) * group;
+  const uint64_t sums = weights_sums_bound(cfg->dtype, cfg->n_kv_heads, n);
+  const uint64_t logits = uint64_t(cfg->n_kv_heads) * few * logits_ld(n);
   return size_t(kScratchHead + rows_bound_bytes(cfg, 1, m, n, 0) + align256(uint64_t(m) * cfg->n_q_heads * 4) +
-                align256(weights_sums_bound(cfg->dtype, cfg->n_kv_heads, n) * 4));
+                align256((sums > logits ? sums : logits) * 4));
 }
 
 int zha_dense_weights(const zha_config* cfg, const void* K, const void* V, int64_t ld, int64_t n, const void* Q,
@@ -722,8 +730,14 @@ int zha_dense_weights(const zha_config* cfg, const void* K, const void* V, int64
   a.n = n;
   a.rows = m * a.group;
   a.causal = causal;
+  if (a.rows <= kLogitRows) {
+    a.logits = reinterpret_cast<float*>(static_cast<char*>(scratch) + sums_off);
+    a.ld_logits = logits_ld(n);
+  }
   WeightsArgs w;
   std::memset(&w, 0, sizeof(w));
+  w.logits = a.logits;
+  w.ld_logits = a.ld_logits;
   w.K = K;
   w.Q = Q;
   w.lse = a.lse;

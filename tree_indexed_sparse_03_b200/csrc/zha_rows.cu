@@ -119,6 +119,12 @@ __global__ void __launch_bounds__(kRowsThreads) rows_scalar_kernel(RowsArgs a) {
           acc[i][j] = k0 + l16 + 16 * j < lim[i] ? acc[i][j] * c2 : -INFINITY;
           mx = fmaxf(mx, acc[i][j]);
         }
+        if (a.logits && r0 + half * RT + i < seg_rows) {
+          float* lg = a.logits + (int64_t(s.h) * a.rows + r0 + half * RT + i) * a.ld_logits + k0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (k0 + l16 + 16 * j < a.n) __stcg(lg + l16 + 16 * j, acc[i][j]);
+        }
 #pragma unroll
         for (int off = 8; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
         const float base = mx == -INFINITY ? 0.f : mx;  // a row that sees nothing yet: every weight 2^-inf = 0
@@ -421,6 +427,34 @@ __global__ void __launch_bounds__(256) weights_join_kernel(WeightsArgs a) {
   a.acc_out[h * a.ld_acc_out + k] = (a.acc_in ? a.acc_in[h * a.ld_acc_in + k] : 0.f) + s;
 }
 
+// acc_out = acc_in + the weights of the kept logits: four keys per thread, all rows' logits in flight.  Bound by the
+// logits' way through L2.
+__global__ void __launch_bounds__(256) weights_logits_kernel(WeightsArgs a) {
+  __shared__ float lse2[kLogitRows];
+  const int h = blockIdx.y;
+  const int64_t k = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4;
+  pdl_wait();
+  if (threadIdx.x < a.rows) {
+    const int t = threadIdx.x / a.group;
+    lse2[threadIdx.x] = a.lse[int64_t(t) * a.hq + h * a.group + (threadIdx.x - t * a.group)] * 1.4426950408889634f;
+  }
+  __syncthreads();
+  if (k >= a.n) return;
+  const float* lg = a.logits + int64_t(h) * a.rows * a.ld_logits + k;
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+  for (int r = 0; r < a.rows; ++r) {
+    const float4 t = __ldcg(reinterpret_cast<const float4*>(lg + r * a.ld_logits));
+    s[0] += exp2f(t.x - lse2[r]);
+    s[1] += exp2f(t.y - lse2[r]);
+    s[2] += exp2f(t.z - lse2[r]);
+    s[3] += exp2f(t.w - lse2[r]);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (k + e < a.n) a.acc_out[h * a.ld_acc_out + k + e] = (a.acc_in ? a.acc_in[h * a.ld_acc_in + k + e] : 0.f) + s[e];
+}
+
 // ------------------------------------------------------------------ host side
 namespace {
 
@@ -570,6 +604,10 @@ uint64_t weights_sums_bound(int dtype, int hkv, int64_t n) {
 }
 
 cudaError_t launch_weights(const WeightsArgs& a, int dtype, int d, cudaStream_t st) {
+  if (a.logits) {
+    count_launches(1);
+    return launch_after(weights_logits_kernel, dim3(unsigned((a.n + 1023) / 1024), unsigned(a.hkv)), 256, 0, st, a);
+  }
   if (dtype == ZHA_BF16) return launch_weights_tc(a, d, st);
   count_launches(a.rsplit > 1 ? 2 : 1);
   const cudaError_t e = d == 128 ? run_weights_rt<float, 128>(a, st) : run_weights_rt<float, 64>(a, st);

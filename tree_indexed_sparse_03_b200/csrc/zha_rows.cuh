@@ -33,7 +33,9 @@ struct RowsArgs {
   float* lse;               // [B][m][hq] natural log, may be NULL
   float* part;              // partials: numerators, d floats per row
   float2* part_ml;          // and (running max in powers of two, running sum) per row
-  float* logits;            // NULL, or [hkv][rows][n] raw dot products of the prefix to leave for the weights pass
+  float* logits;            // NULL, or [hkv][rows][ld_logits]: the prefix logits in powers of two (-inf where masked), kept
+                            // for the weights pass
+  int64_t ld_logits;
   int* status;
   int* plan;                // the flat list as the attention kernel's first CTA found it, for the join (rows_publish)
   int64_t ld, n, ld_own;
@@ -278,7 +280,8 @@ struct WeightsArgs {
   const float* acc_in;   // NULL: zeros
   float* acc_out;        // [hkv][ld_acc_out]
   float* sums;           // partial column sums: [rsplit][hkv][n] (rsplit > 1), tensor cores: [CTA][2][256]
-  const float* logits;   // [hkv][rows][n] raw dot products (NULL: computed again)
+  const float* logits;   // [hkv][rows][ld_logits] as the attention left them (NULL: computed again)
+  int64_t ld_logits;
   int* status;
   int64_t ld, n, ld_acc_in, ld_acc_out;
   int rows;              // m * group
@@ -310,6 +313,10 @@ uint64_t weights_sums_bound(int dtype, int hkv, int64_t n);
 uint64_t weights_tc_floats();
 cudaError_t launch_weights_tc(const WeightsArgs& a, int d, cudaStream_t st);
 cudaError_t launch_weights(const WeightsArgs& a, int dtype, int d, cudaStream_t st);
+
+// Calls of up to this many rows per KV head keep their logits (4 bytes per row and key, mostly in L2) rather than read
+// K again (2 d bytes per key) and run its products again.
+constexpr int kLogitRows = 16;
 
 struct EvictArgs {
   const void* K;

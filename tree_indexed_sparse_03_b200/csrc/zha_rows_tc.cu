@@ -52,6 +52,31 @@ struct TcMaps {
   CUtensorMap k, v, ko, vo;
 };
 
+// 32 logits of a row from column c0 on, of which the row sees the tile's first `left`.
+__device__ __forceinline__ void hide32(float* v, int c0, int left) {
+#pragma unroll
+  for (int q = 0; q < 32; ++q)
+    if (c0 + q >= left) v[q] = -INFINITY;
+}
+__device__ __forceinline__ float largest32(const float* v) {
+  float m[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+  for (int q = 4; q < 28; q += 8)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m[e] = max3(m[e], v[q + e], v[q + 4 + e]);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], v[28 + e]);
+  return fmaxf(max3(m[0], m[1], m[2]), m[3]);
+}
+// Kept logits: lg is the row's run of the tile that begins at key k0.  Columns past the last key of a 16-byte piece lie in the
+// row's padding.
+__device__ __forceinline__ void keep_logits(const RowsArgs& a, float* lg, const float* v, int k0, int c0, float c2) {
+#pragma unroll
+  for (int q = 0; q < 32; q += 4)
+    if (k0 + c0 + q < a.n)
+      __stcg(reinterpret_cast<float4*>(lg + c0 + q), make_float4(v[q] * c2, v[q + 1] * c2, v[q + 2] * c2, v[q + 3] * c2));
+}
+
 // One share of a segment as every role sees it.
 struct TcWork {
   RowsSeg s;
@@ -76,12 +101,12 @@ __device__ __forceinline__ bool next_work(const RowsArgs& a, const RowsTotals& t
   return false;
 }
 
-template <int D, bool PV>
+template <int D, bool PV, bool LG>
 __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, const __grid_constant__ TcMaps maps) {
   using Sh = TcShape<D>;
   constexpr int NS = Sh::kSlots, PANELS = D / 64, PANEL = kTcKeys * 128;  // bytes of a 64-wide panel of a tile
   extern __shared__ uint8_t raw[];
-  __shared__ __align__(8) uint64_t bars[2 * NS + 17];
+  __shared__ __align__(8) uint64_t bars[2 * NS + 19];
   __shared__ float2 x_ml[128];  // stream 1's sums for the join
   __shared__ uint32_t tmem_base;
   __shared__ volatile int gave_up;
@@ -90,7 +115,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
   const uint32_t b0 = smem_u32(bars);
   auto full = [&](int s) { return b0 + 8 * s; };
   auto empty = [&](int s) { return b0 + 8 * (NS + s); };
-  auto s_full = [&](int s) { return b0 + 8 * (2 * NS + s); };
+  // logits ready; without outputs a stream has two buffers for them, the second in place of O
+  auto s_full = [&](int s, int buf = 0) { return b0 + 8 * (2 * NS + (buf ? 17 : 0) + s); };
   auto o_full = [&](int s) { return b0 + 8 * (2 * NS + 2 + s); };
   auto q_full = [&](int s) { return b0 + 8 * (2 * NS + 4 + s); };
   auto p_full = [&](int s, int half) { return b0 + 8 * (2 * NS + 6 + 2 * s + half); };
@@ -106,6 +132,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
       }
       for (int s = 0; s < 2; ++s) {
         bar_init(s_full(s), 1);
+        bar_init(s_full(s, 1), 1);
         bar_init(o_full(s), 1);
         bar_init(q_full(s), 4);
         bar_init(p_full(s, 0), 4);
@@ -207,7 +234,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
     const uint32_t q_lo = desc_low(base + st * Sh::kQ, 16);
     const uint32_t k_lo = desc_low(ring, 16), v_lo = desc_low(ring, PANEL);
     int slot = 0;
-    uint32_t round = 0, p_phase = 0, q_phase = 0;
+    uint32_t round = 0, p_phase = 0, q_phase = 0, b_round = 0;
+    int buf = 0;
     bool ok = true;
     while (ok && next_work(a, tot, &x, x_end, &w)) {
       const int lag = w.both ? 1 : 2;
@@ -252,23 +280,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
             slot = 0;
             ++round;
           }
-        } else if (i >= lag && mine) {  // without outputs: the logits have been read
-          if (!(ok = bar_wait(p_full(st, 0), p_phase, &gave_up))) break;
-          p_phase ^= 1;
         }
         if (i < w.cnt) {
           if (!(ok = bar_wait(full(slot), round & 1, &gave_up))) break;
           if (mine) {
+            if (!PV && !(ok = bar_wait(p_full(st, buf), (b_round & 1) ^ 1, &gave_up))) break;  // the buffer has been read
             tc_fence_after();
             if (lane == 0) {
               const uint32_t k = k_lo + slot * (Sh::kTile >> 4);
 #pragma unroll
               for (int e = 0; e < D / 16; ++e) {
                 const uint32_t off = ((e / 4) * PANEL + (e % 4) * 32) >> 4;
-                mma_ss(ts, q_lo + off, k + off, id_s, e ? 1u : 0u);
+                mma_ss(ts + (PV ? 0 : buf * 256), q_lo + off, k + off, id_s, e ? 1u : 0u);
               }
-              mma_commit(s_full(st));
+              mma_commit(s_full(st, PV ? 0 : buf));
               mma_commit(empty(slot));
+            }
+            if (!PV && ++buf == 2) {
+              buf = 0;
+              ++b_round;
             }
           } else if (lane == 0) {
             bar_arrive(empty(slot));
@@ -295,6 +325,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
     const float c2 = a.scale * 1.4426950408889634f;  // weights as powers of two
     const uint64_t cc = pair(c2, c2), minus = pair(-1.f, -1.f);
     uint32_t s_phase = 0, o_phase = 0, x_phase = 0, t_phase = 0;
+    int buf = 0;
     bool ok = true;
     while (ok && next_work(a, tot, &x, x_end, &w)) {
       const int r0 = w.s.p * kTcRows + (w.both ? st * 128 : 0);  // the stream's first row
@@ -331,10 +362,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
       const bool active = wrow < nrows;  // a warp of padding rows leaves its weights alone: they reach no valid row
       float m_ref = -INFINITY, l_run = 0.f;
       const int step = w.both ? 1 : 2, i0 = w.both ? 0 : st;
+      if constexpr (PV) {
       // Streams take turns: a tile may begin once the other stream has handed over half of its own.  Left alone they fall into
       // step, and the tensor pipe idles while both weigh (256K tokens behind 64 sequences: 413 us, whole turns 400, half
       // turns 380).
-      const bool turns = PV && w.cnt > kTurnTiles;
+      const bool turns = w.cnt > kTurnTiles;
 #pragma unroll 1
       for (int i = i0; i < w.cnt; i += step) {
         if (turns && (st || i != i0)) {
@@ -348,17 +380,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
           const int left = lim - (w.t0 + i) * kTcKeys;  // keys of the tile that the row sees
           const bool mask = __any_sync(0xffffffffu, left < kTcKeys);
           float va[32], vb[32];
-          auto hide = [&](float* v, int c0) {
-#pragma unroll
-            for (int q = 0; q < 32; ++q)
-              if (c0 + q >= left) v[q] = -INFINITY;
-          };
-          auto largest = [&](const float* v, float m) {
-#pragma unroll
-            for (int q = 0; q < 32; q += 4) m = max3(max3(m, v[q], v[q + 1]), v[q + 2], v[q + 3]);
-            return m;
-          };
-          float mx = -INFINITY;
+          float mx;
           {
             float vc[32], vd[32];
             tmem_ld32(ts, va);
@@ -370,13 +392,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
             tmem_wait32(vc);
             tmem_wait32(vd);
             if (mask) {
-              hide(va, 0);
-              hide(vb, 32);
-              hide(vc, 64);
-              hide(vd, 96);
+              hide32(va, 0, left);
+              hide32(vb, 32, left);
+              hide32(vc, 64, left);
+              hide32(vd, 96, left);
             }
-            mx = largest(vd, largest(vc, mx));
-            mx = fmaxf(mx, largest(vb, largest(va, -INFINITY)));
+            mx = fmaxf(fmaxf(largest32(va), largest32(vb)), fmaxf(largest32(vc), largest32(vd)));
           }
           tmem_ld32(ts, va);  // again, chunk by chunk, for the exponentials
           const float m_new = mx * c2;
@@ -384,7 +405,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
           if (__any_sync(0xffffffffu, grow)) {
             const float up = grow ? m_new : m_ref;
             const float sc = m_ref == -INFINITY ? 0.f : ex2(m_ref - up);
-            if (PV && i != i0) {
+            if (i != i0) {
 #pragma unroll 1
               for (int j = 0; j < D; j += 32) {
                 tmem_ld32(to + j, vb);
@@ -404,39 +425,41 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
           const float mb = m_ref == -INFINITY ? 0.f : m_ref;
           const uint64_t mm = pair(-mb, -mb);
           uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+          // kept logits: the row's own run of the tile (columns past the last key lie in the padding of the row)
+          float* lg = LG && row < nrows
+                          ? a.logits + (int64_t(w.s.h) * a.rows + r0 + row) * a.ld_logits + int64_t(w.t0 + i) * kTcKeys
+                          : nullptr;
           auto weigh = [&](const float* v, int c0) {  // 32 keys: their weights' hi parts, then their lo parts, over the logits
             uint32_t o[32];
 #pragma unroll
             for (int q = 0; q < 16; ++q) {
-              float e0, e1;
-              unpair(fma2(pair(v[2 * q], v[2 * q + 1]), cc, mm), &e0, &e1);
-              const uint64_t p = pair(ex2(e0), ex2(e1));
+              const uint64_t e = fma2(pair(v[2 * q], v[2 * q + 1]), cc, mm);
+              const uint64_t p = ex2_pair(e);
               sum[q & 1] = add2(sum[q & 1], p);
-              if (PV) {
-                float p0, p1;
-                unpair(p, &p0, &p1);
-                o[q] = pack_bf16(p0, p1);
-                unpair(fma2(pair(__uint_as_float(o[q] << 16), __uint_as_float(o[q] & 0xffff0000u)), minus, p), &p0, &p1);
-                o[16 + q] = pack_bf16(p0, p1);
-              }
+              float p0, p1;
+              unpair(p, &p0, &p1);
+              o[q] = pack_bf16(p0, p1);
+              unpair(fma2(pair(__uint_as_float(o[q] << 16), __uint_as_float(o[q] & 0xffff0000u)), minus, p), &p0, &p1);
+              o[16 + q] = pack_bf16(p0, p1);
             }
-            if (PV) tmem_st32(ts + c0, o);
+            tmem_st32(ts + c0, o);
+            if (LG && lg) keep_logits(a, lg, v, (w.t0 + i) * kTcKeys, c0, c2);
           };
 #pragma unroll 1
           for (int j = 0; j < kTcKeys; j += 64) {
             tmem_wait32(va);
             tmem_ld32(ts + j + 32, vb);
-            if (mask) hide(va, j);
+            if (mask) hide32(va, j, left);
             weigh(va, j);
             tmem_wait32(vb);
             if (j == 0) tmem_ld32(ts + 64, va);
-            if (mask) hide(vb, j + 32);
+            if (mask) hide32(vb, j + 32, left);
             weigh(vb, j + 32);
-            if (PV) tmem_wait_st();
+            tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-              if (PV || j) bar_arrive(p_full(st, PV ? j >> 6 : 0));
+              bar_arrive(p_full(st, j >> 6));
               if (turns && j == 0) bar_arrive(turn(st ^ 1));
             }
           }
@@ -448,7 +471,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
           __syncwarp();
           if (lane == 0) {
             bar_arrive(p_full(st, 0));
-            if (PV) bar_arrive(p_full(st, 1));
+            bar_arrive(p_full(st, 1));
             if (turns) bar_arrive(turn(st ^ 1));
           }
         }
@@ -458,6 +481,59 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
       if (ok && turns && (st == 0 ? w.both || !(w.cnt & 1) : !w.both && (w.cnt & 1))) {
         if (!(ok = bar_wait(turn(st), t_phase, &gave_up))) break;
         t_phase ^= 1;
+      }
+      } else {
+#pragma unroll 1
+      for (int i = i0; i < w.cnt; i += step) {  // only the sums
+        if (!(ok = bar_wait(s_full(st, buf), s_phase, &gave_up))) break;
+        tc_fence_after();
+        if (active) {
+          const int left = lim - (w.t0 + i) * kTcKeys;  // keys of the tile that the row sees
+          const bool mask = __any_sync(0xffffffffu, left < kTcKeys);
+          const uint32_t tb = ts + buf * 256;
+          float* lg = LG && row < nrows
+                          ? a.logits + (int64_t(w.s.h) * a.rows + r0 + row) * a.ld_logits + int64_t(w.t0 + i) * kTcKeys
+                          : nullptr;
+          float v[kTcKeys];
+#pragma unroll
+          for (int j = 0; j < kTcKeys; j += 32) tmem_ld32(tb + j, v + j);
+#pragma unroll
+          for (int j = 0; j < kTcKeys; j += 32) tmem_wait32(v + j);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(p_full(st, buf));  // the buffer has been read
+          if (mask) {
+#pragma unroll
+            for (int j = 0; j < kTcKeys; j += 32) hide32(v + j, j, left);
+          }
+          const float m_new = fmaxf(fmaxf(largest32(v), largest32(v + 32)), fmaxf(largest32(v + 64), largest32(v + 96))) * c2;
+          if (m_new > m_ref + kLazyMax || (m_ref == -INFINITY && m_new > -INFINITY)) {
+            l_run *= m_ref == -INFINITY ? 0.f : ex2(m_ref - m_new);
+            m_ref = m_new;
+          }
+          const float mb = m_ref == -INFINITY ? 0.f : m_ref;
+          const uint64_t mm = pair(-mb, -mb);
+          uint64_t sum[4] = {pair(0.f, 0.f), pair(0.f, 0.f), pair(0.f, 0.f), pair(0.f, 0.f)};
+#pragma unroll
+          for (int q = 0; q < kTcKeys / 2; ++q)
+            sum[q & 3] = add2(sum[q & 3], ex2_pair(fma2(pair(v[2 * q], v[2 * q + 1]), cc, mm)));
+          float s0, s1;
+          unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), &s0, &s1);
+          l_run += s0 + s1;
+          if (LG && lg) {
+#pragma unroll
+            for (int j = 0; j < kTcKeys; j += 32) keep_logits(a, lg, v + j, (w.t0 + i) * kTcKeys, j, c2);
+          }
+        } else {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(p_full(st, buf));
+        }
+        if (++buf == 2) {
+          buf = 0;
+          s_phase ^= 1;
+        }
+      }
       }
       if (!ok) break;
       if (PV || i0 >= w.cnt) {  // also without work: the stream stays within one segment of its products' warp
@@ -602,11 +678,16 @@ cudaError_t make_rows_map(CUtensorMap* map, const void* base, int d, int64_t row
 
 namespace {
 
-template <int D, bool PV> cudaError_t run_tc(const RowsArgs& a, const TcMaps& maps, cudaStream_t st) {
-  const cudaError_t e = allow_smem(rows_tc_kernel<D, PV>, TcShape<D>::kSmem);
+template <int D, bool PV, bool LG> cudaError_t run_tc_as(const RowsArgs& a, const TcMaps& maps, cudaStream_t st) {
+  const cudaError_t e = allow_smem(rows_tc_kernel<D, PV, LG>, TcShape<D>::kSmem);
   if (e != cudaSuccess) return e;
-  rows_tc_kernel<D, PV><<<a.nc, kTcThreads, TcShape<D>::kSmem, st>>>(a, maps);
+  rows_tc_kernel<D, PV, LG><<<a.nc, kTcThreads, TcShape<D>::kSmem, st>>>(a, maps);
   return cudaGetLastError();
+}
+
+template <int D> cudaError_t run_tc(const RowsArgs& a, const TcMaps& maps, cudaStream_t st) {
+  if (a.logits) return a.O ? run_tc_as<D, true, true>(a, maps, st) : run_tc_as<D, false, true>(a, maps, st);
+  return a.O ? run_tc_as<D, true, false>(a, maps, st) : run_tc_as<D, false, false>(a, maps, st);
 }
 
 }  // namespace
@@ -624,8 +705,7 @@ cudaError_t launch_rows_tc(const RowsArgs& a, int d, cudaStream_t st) {
     if (e == cudaSuccess) e = make_rows_map(&maps.vo, a.Vo, d, a.ld_own, a.ld_own, int64_t(a.B) * a.hkv, kTcKeys, 1);
   }
   if (e != cudaSuccess) return e;
-  if (a.O) return d == 128 ? run_tc<128, true>(a, maps, st) : run_tc<64, true>(a, maps, st);
-  return d == 128 ? run_tc<128, false>(a, maps, st) : run_tc<64, false>(a, maps, st);
+  return d == 128 ? run_tc<128>(a, maps, st) : run_tc<64>(a, maps, st);
 }
 
 void tc_plan(int64_t rows, int64_t mg, int64_t ld_own, RowsPlan* p) {

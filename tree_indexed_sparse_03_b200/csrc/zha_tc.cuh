@@ -114,6 +114,20 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+// Eight columns, with the wait.
+__device__ __forceinline__ void tmem_ld8(uint32_t addr, float* f) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n tcgen05.wait::ld.sync.aligned;"
+      : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 // ---------------------------------------------------------------- matrix products
 // Shared-memory operand of 128-byte swizzled rows: start address, leading-dimension and stride byte
 // offsets in 16-byte units; bits 46-48 hold the constant 1, bits 61-63 the swizzle mode 2 (128 bytes).
@@ -179,6 +193,12 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+__device__ __forceinline__ uint64_t ex2_pair(uint64_t x) {
+  float x0, x1;
+  unpair(x, &x0, &x1);
+  return pair(ex2(x0), ex2(x1));
 }
 
 // Host: 3-d tensor map of bf16 rows [planes][rows][d], planes `plane_rows` rows apart, tiles of 64 elements x

@@ -14,8 +14,8 @@
 // the CTAs.  A segment inside one CTA is written out directly, one cut by
 // a CTA border leaves partial sums that weights_tc_join_kernel adds in CTA order.
 //
-// Roles: warps 0-3 and 4-7 the two streams' keys, warp 8 the loads (K pairs, row tiles with their
-// log-sum-exps), warp 9 the products.
+// Roles: warps 0-3 and 4-7 the two streams' keys, warp 8 the loads (K pairs, row tiles), warp 9 the products, warp 10
+// the row tiles' log-sum-exps.
 #include <cstring>
 
 #include "zha_rows.cuh"
@@ -23,7 +23,7 @@
 
 namespace zha {
 
-constexpr int kWtThreads = 320;
+constexpr int kWtThreads = 352;
 constexpr int kWtKeys = 256;   // keys per segment
 constexpr int kWtCols = 128;   // query rows per tile (columns of the product)
 constexpr int kWtSlots = 3;    // row tiles in flight
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
   constexpr int NS = kWtSlots, PANELS = D / 64;
   extern __shared__ uint8_t raw[];
   __shared__ __align__(8) uint64_t bars[2 * NS + 13];
-  __shared__ __align__(16) float lse2[NS][kWtCols];
+  __shared__ __align__(16) float minus_lse[NS][kWtCols];  // in powers of two; -inf where a tile has no row
   __shared__ uint32_t tmem_base;
   __shared__ volatile int gave_up;
   const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
@@ -200,12 +200,6 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
             tma_load(ring + slot * Sh::kHalf + p * 128 * 128, &maps.q, full(slot), p * 64,
                      s.h * a.group + w.g0, w.tok0);
         }
-        for (int c = lane; c < kWtCols; c += 32)  // no row: every weight 2^-inf = 0
-          lse2[slot][c] = c < w.cols ? a.lse[int64_t(w.tok0 + c / w.gw) * a.hq + s.h * a.group + w.g0 + c % w.gw] *
-                                           1.4426950408889634f
-                                     : INFINITY;
-        __syncwarp();
-        if (lane == 0) bar_arrive(full(slot));
         if (++slot == NS) {
           slot = 0;
           ++round;
@@ -219,6 +213,33 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
         if (q < slot || round > 0) bar_wait(full(q), (q < slot ? round : round - 1) & 1, &never);
       for (int q = 0; q < 2; ++q)
         if (q < ks || k_round > 0) bar_wait(k_full(q), (q < ks ? k_round : k_round - 1) & 1, &never);
+    }
+  } else if (wid == 10) {  // ---------------------------------------------------------------- log-sum-exps
+    int slot = 0;
+    uint32_t round = 0;
+    bool ok = true;
+    while (x < x_end && ok) {
+      const WtSeg s = wt_find(a, plan, x);
+      const int t1 = min(s.first + s.tiles, x_end) - s.first;
+      for (int t = x - s.first; t < t1; ++t) {
+        const WtTile w = wt_tile(a, plan, s.t_first + t);
+        float v[kWtCols / 32];  // on their way while the slot is still in use
+#pragma unroll
+        for (int q = 0; q < kWtCols / 32; ++q) {
+          const int c = lane + 32 * q, i = c / w.gw;
+          v[q] = c < w.cols ? a.lse[int64_t(w.tok0 + i) * a.hq + s.h * a.group + w.g0 + (c - i * w.gw)] : INFINITY;
+        }
+        if (!(ok = bar_wait(empty(slot), (round & 1) ^ 1, &gave_up))) break;
+#pragma unroll
+        for (int q = 0; q < kWtCols / 32; ++q) minus_lse[slot][lane + 32 * q] = v[q] * -1.4426950408889634f;
+        __syncwarp();
+        if (lane == 0) bar_arrive(full(slot));
+        if (++slot == NS) {
+          slot = 0;
+          ++round;
+        }
+      }
+      x = s.first + t1;
     }
   } else if (wid == 9) {  // ---------------------------------------------------------------- products
     int slot = 0, ks = 0, buf = 0;
@@ -273,6 +294,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
     const int st = wid >> 2, key = tid & 127;
     const uint32_t lane_base = uint32_t((wid & 3) * 32) << 16;
     const float c2 = a.scale * 1.4426950408889634f;
+    const uint64_t cc = pair(c2, c2);
     int slot = 0, buf = 0;
     uint32_t round = 0, b_round = 0;
     bool ok = true;
@@ -281,7 +303,8 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
       const int t1 = min(s.first + s.tiles, x_end) - s.first;
       const int64_t k = int64_t(s.seg) * kWtKeys + st * 128 + key;
       const int64_t tok_min = a.causal ? k - (a.n - a.m) : 0;  // first token that sees this key
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      const float before = a.acc_in && k < a.n ? a.acc_in[s.h * a.ld_acc_in + k] : 0.f;
+      uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
       for (int t = x - s.first; t < t1; ++t) {
         const WtTile w = wt_tile(a, plan, s.t_first + t);
         // the log-sum-exps come with the tile's own barrier, the products with theirs
@@ -290,40 +313,37 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
         tc_fence_after();
         const int64_t hid = (tok_min - w.tok0) * w.gw;  // columns before this one do not see the key
         const int c_min = hid < 0 ? 0 : (hid > kWtCols ? kWtCols : int(hid));
-        const bool mask = __any_sync(0xffffffffu, c_min > 0);
+        const bool mask = __any_sync(0xffffffffu, c_min > 0) || w.cols < kWtCols;
         const uint32_t ts = tm + lane_base + st * 256 + buf * 128;
-        const int chunks = (w.cols + 31) / 32;
-#pragma unroll 1
-        for (int j = 0; j < chunks; ++j) {
-          float v[32];
-          tmem_ld32(ts + 32 * j, v);
-          tmem_wait32(v);
-          const float4* l4 = reinterpret_cast<const float4*>(&lse2[slot][32 * j]);
+        float v[kWtCols];
+        const bool wide = w.cols > 64;  // up to 64 columns: the others are neither loaded nor added
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const float4 l = l4[q];
-            float p[4] = {ex2(fmaf(v[4 * q], c2, -l.x)), ex2(fmaf(v[4 * q + 1], c2, -l.y)),
-                          ex2(fmaf(v[4 * q + 2], c2, -l.z)), ex2(fmaf(v[4 * q + 3], c2, -l.w))};
-            if (mask) {
+        for (int j = 0; j < kWtCols; j += 32)
+          if (j < 64 || wide) tmem_ld32(ts + j, v + j);
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (32 * j + 4 * q + e < c_min) p[e] = 0.f;
-            }
-            if (32 * j + 4 * q + 3 >= w.cols) {  // columns that no product wrote
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (32 * j + 4 * q + e >= w.cols) p[e] = 0.f;
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sum[e] += p[e];
-          }
-        }
+        for (int j = 0; j < kWtCols; j += 32)
+          if (j < 64 || wide) tmem_wait32(v + j);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          bar_arrive(s_free(st, buf));
-          bar_arrive(empty(slot));
+        if (lane == 0) bar_arrive(s_free(st, buf));  // all of the tile is in registers
+        if (mask) {  // also the columns that no product wrote
+#pragma unroll
+          for (int q = 0; q < kWtCols; ++q)
+            if (q < c_min || q >= w.cols) v[q] = -INFINITY;
         }
+        const ulonglong2* l = reinterpret_cast<const ulonglong2*>(minus_lse[slot]);
+        auto add = [&](int q0) {
+#pragma unroll
+          for (int q = q0; q < q0 + 64; q += 4) {
+            const ulonglong2 l4 = l[q / 4];
+            sum[0] = add2(sum[0], ex2_pair(fma2(pair(v[q], v[q + 1]), cc, l4.x)));
+            sum[1] = add2(sum[1], ex2_pair(fma2(pair(v[q + 2], v[q + 3]), cc, l4.y)));
+          }
+        };
+        add(0);
+        if (wide) add(64);
+        __syncwarp();
+        if (lane == 0) bar_arrive(empty(slot));
         if (++slot == NS) {
           slot = 0;
           ++round;
@@ -334,9 +354,11 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
         }
       }
       if (!ok) break;
-      const float total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      float s0, s1;
+      unpair(add2(sum[0], sum[1]), &s0, &s1);
+      const float total = s0 + s1;
       if (x == s.first && t1 == s.tiles) {
-        if (k < a.n) a.acc_out[s.h * a.ld_acc_out + k] = (a.acc_in ? a.acc_in[s.h * a.ld_acc_in + k] : 0.f) + total;
+        if (k < a.n) a.acc_out[s.h * a.ld_acc_out + k] = before + total;
       } else {
         a.sums[(int64_t(blockIdx.x) * 2 + (x_begin < s.first ? 1 : 0)) * kWtKeys + st * 128 + key] = total;
       }
