@@ -4,8 +4,9 @@
 // The products are computed again with keys as the rows: S^T = K Q^T, 128 keys x 128 query rows per
 // product, so that a column sum is one thread's sum over its own accumulator row
 // and no exchange between threads is needed.  Two streams of 128 keys share every
-// tile of query rows; each has two accumulators in tensor memory, so that one tile's product runs under the other's
-// exponentials.  Per tile and stream 512 cycles of products (d = 128) against 1024 of
+// tile of query rows; each has two accumulators in tensor memory and a warpgroup for each of them, which take every other
+// tile: with one warpgroup per stream all eight warps waited for their next tile at about the same time and the
+// exponential unit stood still for a quarter of it.  The two warpgroups of a stream add up at a segment's end.  Per tile and stream 512 cycles of products (d = 128) against 1024 of
 // exponentials (16 per cycle and SM): the exponentials bound it for many rows, the second read
 // of K for few.
 //
@@ -14,8 +15,8 @@
 // the CTAs.  A segment inside one CTA is written out directly, one cut by
 // a CTA border leaves partial sums that weights_tc_join_kernel adds in CTA order.
 //
-// Roles: warps 0-3 and 4-7 the two streams' keys, warp 8 the loads (K pairs, row tiles), warp 9 the products, warp 10
-// the row tiles' log-sum-exps.
+// Roles: warps 0-15 the keys (warpgroup g: stream g & 1, accumulator g >> 1), warp 16 the loads (K pairs, row tiles),
+// warp 17 the products, warp 18 the row tiles' log-sum-exps.
 #include <cstring>
 
 #include "zha_rows.cuh"
@@ -23,10 +24,11 @@
 
 namespace zha {
 
-constexpr int kWtThreads = 352;
+constexpr int kWtThreads = 608;
 constexpr int kWtKeys = 256;   // keys per segment
 constexpr int kWtCols = 128;   // query rows per tile (columns of the product)
-constexpr int kWtSlots = 3;    // row tiles in flight
+constexpr int kWtSlots = 2;    // row tiles in flight
+constexpr int kWtLse = 4;      // tiles whose log-sum-exps are in shared memory (they stay until the tile has been added)
 constexpr int kWtFloats = 148 * 2 * kWtKeys;  // partial sums: two slots per CTA
 
 template <int D> struct WtShape {
@@ -118,10 +120,11 @@ struct WtMaps {
 template <int D>
 __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a, const __grid_constant__ WtMaps maps) {
   using Sh = WtShape<D>;
-  constexpr int NS = kWtSlots, PANELS = D / 64;
+  constexpr int NS = kWtSlots, NL = kWtLse, PANELS = D / 64;
   extern __shared__ uint8_t raw[];
-  __shared__ __align__(8) uint64_t bars[2 * NS + 13];
-  __shared__ __align__(16) float minus_lse[NS][kWtCols];  // in powers of two; -inf where a tile has no row
+  __shared__ __align__(8) uint64_t bars[2 * NS + 21 + 2 * NL];
+  __shared__ float other[2][2][128];  // [segment parity][stream]: sums of the stream's second warpgroup
+  __shared__ __align__(16) float minus_lse[NL][kWtCols];  // in powers of two; -inf where a tile has no row
   __shared__ uint32_t tmem_base;
   __shared__ volatile int gave_up;
   const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
@@ -134,12 +137,20 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
   auto s_full = [&](int st, int b) { return b0 + 8 * (2 * NS + 4 + 2 * st + b); };
   auto s_free = [&](int st, int b) { return b0 + 8 * (2 * NS + 8 + 2 * st + b); };
   const uint32_t done = b0 + 8 * (2 * NS + 12);
+  auto x_full = [&](int par, int st) { return done + 8 + 8 * (2 * par + st); };
+  auto l_full = [&](int s) { return done + 72 + 8 * s; };
+  auto l_empty = [&](int s) { return done + 72 + 8 * (NL + s); };
+  auto x_free = [&](int par, int st) { return done + 40 + 8 * (2 * par + st); };
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
 
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
-      bar_init(full(s), 2);    // the copy's bytes, the log-sum-exps
-      bar_init(empty(s), 9);   // the products of both streams, and the eight warps that read the log-sum-exps
+      bar_init(full(s), 1);
+      bar_init(empty(s), 1);
+    }
+    for (int s = 0; s < NL; ++s) {
+      bar_init(l_full(s), 1);
+      bar_init(l_empty(s), 8);  // a warpgroup of each stream
     }
     for (int s = 0; s < 2; ++s) {
       bar_init(k_full(s), 1);
@@ -147,6 +158,8 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
       for (int b = 0; b < 2; ++b) {
         bar_init(s_full(s, b), 1);
         bar_init(s_free(s, b), 4);
+        bar_init(x_full(b, s), 4);
+        bar_init(x_free(b, s), 4);
       }
     }
     bar_init(done, 1);
@@ -157,7 +170,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
   for (int i = tid; i < NS * Sh::kHalf / 16; i += kWtThreads)
     asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(ring + i * 16), "r"(0) : "memory");
   fence_async_smem();
-  if (wid == 9) tmem_alloc(smem_u32(&tmem_base), 512);
+  if (wid == 17) tmem_alloc(smem_u32(&tmem_base), 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -168,7 +181,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
   const int x_begin = plan.sh.begin(blockIdx.x), x_end = plan.sh.begin(blockIdx.x + 1);
   int x = x_begin;
 
-  if (wid == 8) {  // ---------------------------------------------------------------- loads
+  if (wid == 16) {  // ---------------------------------------------------------------- loads
     int slot = 0, ks = 0;
     uint32_t round = 0, k_round = 0;
     bool ok = true;
@@ -214,7 +227,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
       for (int q = 0; q < 2; ++q)
         if (q < ks || k_round > 0) bar_wait(k_full(q), (q < ks ? k_round : k_round - 1) & 1, &never);
     }
-  } else if (wid == 10) {  // ---------------------------------------------------------------- log-sum-exps
+  } else if (wid == 18) {  // ---------------------------------------------------------------- log-sum-exps
     int slot = 0;
     uint32_t round = 0;
     bool ok = true;
@@ -229,19 +242,19 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
           const int c = lane + 32 * q, i = c / w.gw;
           v[q] = c < w.cols ? a.lse[int64_t(w.tok0 + i) * a.hq + s.h * a.group + w.g0 + (c - i * w.gw)] : INFINITY;
         }
-        if (!(ok = bar_wait(empty(slot), (round & 1) ^ 1, &gave_up))) break;
+        if (!(ok = bar_wait(l_empty(slot), (round & 1) ^ 1, &gave_up))) break;
 #pragma unroll
         for (int q = 0; q < kWtCols / 32; ++q) minus_lse[slot][lane + 32 * q] = v[q] * -1.4426950408889634f;
         __syncwarp();
-        if (lane == 0) bar_arrive(full(slot));
-        if (++slot == NS) {
+        if (lane == 0) bar_arrive(l_full(slot));
+        if (++slot == NL) {
           slot = 0;
           ++round;
         }
       }
       x = s.first + t1;
     }
-  } else if (wid == 9) {  // ---------------------------------------------------------------- products
+  } else if (wid == 17) {  // ---------------------------------------------------------------- products
     int slot = 0, ks = 0, buf = 0;
     uint32_t round = 0, k_round = 0, b_round = 0;
     bool ok = true;
@@ -291,11 +304,11 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
     __syncwarp();
     bar_wait(done, 0, &never);
   } else {  // ---------------------------------------------------------------- the streams' keys
-    const int st = wid >> 2, key = tid & 127;
+    const int st = (wid >> 2) & 1, mine = wid >> 3, key = tid & 127;
     const uint32_t lane_base = uint32_t((wid & 3) * 32) << 16;
     const float c2 = a.scale * 1.4426950408889634f;
     const uint64_t cc = pair(c2, c2);
-    int slot = 0, buf = 0;
+    int slot = 0, buf = 0, seg_no = 0;
     uint32_t round = 0, b_round = 0;
     bool ok = true;
     while (x < x_end && ok) {
@@ -303,48 +316,44 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
       const int t1 = min(s.first + s.tiles, x_end) - s.first;
       const int64_t k = int64_t(s.seg) * kWtKeys + st * 128 + key;
       const int64_t tok_min = a.causal ? k - (a.n - a.m) : 0;  // first token that sees this key
-      const float before = a.acc_in && k < a.n ? a.acc_in[s.h * a.ld_acc_in + k] : 0.f;
+      const float before = mine == 0 && a.acc_in && k < a.n ? a.acc_in[s.h * a.ld_acc_in + k] : 0.f;
       uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
       for (int t = x - s.first; t < t1; ++t) {
-        const WtTile w = wt_tile(a, plan, s.t_first + t);
-        // the log-sum-exps come with the tile's own barrier, the products with theirs
-        if (!(ok = bar_wait(full(slot), round & 1, &gave_up))) break;
-        if (!(ok = bar_wait(s_full(st, buf), b_round & 1, &gave_up))) break;
-        tc_fence_after();
-        const int64_t hid = (tok_min - w.tok0) * w.gw;  // columns before this one do not see the key
-        const int c_min = hid < 0 ? 0 : (hid > kWtCols ? kWtCols : int(hid));
-        const bool mask = __any_sync(0xffffffffu, c_min > 0) || w.cols < kWtCols;
-        const uint32_t ts = tm + lane_base + st * 256 + buf * 128;
-        float v[kWtCols];
-        const bool wide = w.cols > 64;  // up to 64 columns: the others are neither loaded nor added
+        if (buf == mine) {
+          const WtTile w = wt_tile(a, plan, s.t_first + t);
+          if (!(ok = bar_wait(l_full(slot), round & 1, &gave_up))) break;
+          if (!(ok = bar_wait(s_full(st, buf), b_round & 1, &gave_up))) break;
+          tc_fence_after();
+          const int64_t hid = (tok_min - w.tok0) * w.gw;  // columns before this one do not see the key
+          const int c_min = hid < 0 ? 0 : (hid > kWtCols ? kWtCols : int(hid));
+          const bool mask = __any_sync(0xffffffffu, c_min > 0) || w.cols < kWtCols;
+          const uint32_t ts = tm + lane_base + st * 256 + buf * 128;
+#pragma unroll 1
+          for (int j = 0; j < w.cols; j += 32) {
+            float v[32];
+            tmem_ld32(ts + j, v);
+            tmem_wait32(v);
+            if (mask) {  // also the columns that no product wrote
 #pragma unroll
-        for (int j = 0; j < kWtCols; j += 32)
-          if (j < 64 || wide) tmem_ld32(ts + j, v + j);
+              for (int q = 0; q < 32; ++q)
+                if (j + q < c_min || j + q >= w.cols) v[q] = -INFINITY;
+            }
+            const ulonglong2* l = reinterpret_cast<const ulonglong2*>(&minus_lse[slot][j]);
 #pragma unroll
-        for (int j = 0; j < kWtCols; j += 32)
-          if (j < 64 || wide) tmem_wait32(v + j);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) bar_arrive(s_free(st, buf));  // all of the tile is in registers
-        if (mask) {  // also the columns that no product wrote
-#pragma unroll
-          for (int q = 0; q < kWtCols; ++q)
-            if (q < c_min || q >= w.cols) v[q] = -INFINITY;
-        }
-        const ulonglong2* l = reinterpret_cast<const ulonglong2*>(minus_lse[slot]);
-        auto add = [&](int q0) {
-#pragma unroll
-          for (int q = q0; q < q0 + 64; q += 4) {
-            const ulonglong2 l4 = l[q / 4];
-            sum[0] = add2(sum[0], ex2_pair(fma2(pair(v[q], v[q + 1]), cc, l4.x)));
-            sum[1] = add2(sum[1], ex2_pair(fma2(pair(v[q + 2], v[q + 3]), cc, l4.y)));
+            for (int q = 0; q < 8; ++q) {
+              const ulonglong2 l4 = l[q];
+              sum[0] = add2(sum[0], ex2_pair(fma2(pair(v[4 * q], v[4 * q + 1]), cc, l4.x)));
+              sum[1] = add2(sum[1], ex2_pair(fma2(pair(v[4 * q + 2], v[4 * q + 3]), cc, l4.y)));
+            }
           }
-        };
-        add(0);
-        if (wide) add(64);
-        __syncwarp();
-        if (lane == 0) bar_arrive(empty(slot));
-        if (++slot == NS) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            bar_arrive(s_free(st, buf));
+            bar_arrive(l_empty(slot));
+          }
+        }
+        if (++slot == NL) {
           slot = 0;
           ++round;
         }
@@ -356,11 +365,25 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
       if (!ok) break;
       float s0, s1;
       unpair(add2(sum[0], sum[1]), &s0, &s1);
-      const float total = s0 + s1;
-      if (x == s.first && t1 == s.tiles) {
-        if (k < a.n) a.acc_out[s.h * a.ld_acc_out + k] = before + total;
+      float total = s0 + s1;
+      const int par = seg_no & 1;
+      const uint32_t use = uint32_t(seg_no >> 1) & 1;  // the parity's pair of barriers serves every other segment
+      ++seg_no;
+      if (mine == 1) {
+        if (!(ok = bar_wait(x_free(par, st), use ^ 1, &gave_up))) break;
+        other[par][st][key] = total;
+        __syncwarp();
+        if (lane == 0) bar_arrive(x_full(par, st));
       } else {
-        a.sums[(int64_t(blockIdx.x) * 2 + (x_begin < s.first ? 1 : 0)) * kWtKeys + st * 128 + key] = total;
+        if (!(ok = bar_wait(x_full(par, st), use, &gave_up))) break;
+        total += other[par][st][key];
+        __syncwarp();
+        if (lane == 0) bar_arrive(x_free(par, st));
+        if (x == s.first && t1 == s.tiles) {
+          if (k < a.n) a.acc_out[s.h * a.ld_acc_out + k] = before + total;
+        } else {
+          a.sums[(int64_t(blockIdx.x) * 2 + (x_begin < s.first ? 1 : 0)) * kWtKeys + st * 128 + key] = total;
+        }
       }
       x = s.first + t1;
     }
@@ -368,7 +391,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
   tc_fence_before();
   __syncthreads();
   if (gave_up && tid == 0) raise_status(a.status, ZHA_ERR_TIMEOUT);
-  if (wid == 9) tmem_free(tm, 512);
+  if (wid == 17) tmem_free(tm, 512);
 }
 
 // Segments cut by CTA borders: block c joins the one that begins in CTA c and ends in a later one.
