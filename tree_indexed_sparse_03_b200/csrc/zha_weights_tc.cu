@@ -4,9 +4,10 @@
 // The products are computed again with keys as the rows: S^T = K Q^T, 128 keys x 128 query rows per
 // product, so that a column sum is one thread's sum over its own accumulator row
 // and no exchange between threads is needed.  Two streams of 128 keys share every
-// tile of query rows; each has two accumulators in tensor memory and a warpgroup for each of them, which take every other
-// tile: with one warpgroup per stream all eight warps waited for their next tile at about the same time and the
-// exponential unit stood still for a quarter of it.  The two warpgroups of a stream add up at a segment's end.  Per tile and stream 512 cycles of products (d = 128) against 1024 of
+// tile of query rows; each has two accumulators in tensor memory, so that one tile's product runs under the other's
+// exponentials, and two warpgroups, each for half of a tile's columns: with one warpgroup the exponential unit stood
+// still between tiles for a quarter of the time, with two on alternate tiles both accumulators came free at the same
+// time and the products had nothing to run under.  The two warpgroups of a stream add up at a segment's end.  Per tile and stream 512 cycles of products (d = 128) against 1024 of
 // exponentials (16 per cycle and SM): the exponentials bound it for many rows, the second read
 // of K for few.
 //
@@ -15,7 +16,7 @@
 // the CTAs.  A segment inside one CTA is written out directly, one cut by
 // a CTA border leaves partial sums that weights_tc_join_kernel adds in CTA order.
 //
-// Roles: warps 0-15 the keys (warpgroup g: stream g & 1, accumulator g >> 1), warp 16 the loads (K pairs, row tiles),
+// Roles: warps 0-15 the keys (warpgroup g: stream g & 1, columns 64 (g >> 1) on), warp 16 the loads (K pairs, row tiles),
 // warp 17 the products, warp 18 the row tiles' log-sum-exps.
 #include <cstring>
 
@@ -150,14 +151,14 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
     }
     for (int s = 0; s < NL; ++s) {
       bar_init(l_full(s), 1);
-      bar_init(l_empty(s), 8);  // a warpgroup of each stream
+      bar_init(l_empty(s), 16);
     }
     for (int s = 0; s < 2; ++s) {
       bar_init(k_full(s), 1);
       bar_init(k_empty(s), 1);
       for (int b = 0; b < 2; ++b) {
         bar_init(s_full(s, b), 1);
-        bar_init(s_free(s, b), 4);
+        bar_init(s_free(s, b), 8);
         bar_init(x_full(b, s), 4);
         bar_init(x_free(b, s), 4);
       }
@@ -319,39 +320,37 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
       const float before = mine == 0 && a.acc_in && k < a.n ? a.acc_in[s.h * a.ld_acc_in + k] : 0.f;
       uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
       for (int t = x - s.first; t < t1; ++t) {
-        if (buf == mine) {
-          const WtTile w = wt_tile(a, plan, s.t_first + t);
-          if (!(ok = bar_wait(l_full(slot), round & 1, &gave_up))) break;
-          if (!(ok = bar_wait(s_full(st, buf), b_round & 1, &gave_up))) break;
-          tc_fence_after();
-          const int64_t hid = (tok_min - w.tok0) * w.gw;  // columns before this one do not see the key
-          const int c_min = hid < 0 ? 0 : (hid > kWtCols ? kWtCols : int(hid));
-          const bool mask = __any_sync(0xffffffffu, c_min > 0) || w.cols < kWtCols;
-          const uint32_t ts = tm + lane_base + st * 256 + buf * 128;
+        const WtTile w = wt_tile(a, plan, s.t_first + t);
+        if (!(ok = bar_wait(l_full(slot), round & 1, &gave_up))) break;
+        if (!(ok = bar_wait(s_full(st, buf), b_round & 1, &gave_up))) break;
+        tc_fence_after();
+        const int64_t hid = (tok_min - w.tok0) * w.gw;  // columns before this one do not see the key
+        const int c_min = hid < 0 ? 0 : (hid > kWtCols ? kWtCols : int(hid));
+        const bool mask = __any_sync(0xffffffffu, c_min > 0) || w.cols < kWtCols;
+        const uint32_t ts = tm + lane_base + st * 256 + buf * 128;
 #pragma unroll 1
-          for (int j = 0; j < w.cols; j += 32) {
-            float v[32];
-            tmem_ld32(ts + j, v);
-            tmem_wait32(v);
-            if (mask) {  // also the columns that no product wrote
+        for (int j = 64 * mine; j < min(64 * mine + 64, w.cols); j += 32) {
+          float v[32];
+          tmem_ld32(ts + j, v);
+          tmem_wait32(v);
+          if (mask) {  // also the columns that no product wrote
 #pragma unroll
-              for (int q = 0; q < 32; ++q)
-                if (j + q < c_min || j + q >= w.cols) v[q] = -INFINITY;
-            }
-            const ulonglong2* l = reinterpret_cast<const ulonglong2*>(&minus_lse[slot][j]);
+            for (int q = 0; q < 32; ++q)
+              if (j + q < c_min || j + q >= w.cols) v[q] = -INFINITY;
+          }
+          const ulonglong2* l = reinterpret_cast<const ulonglong2*>(&minus_lse[slot][j]);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const ulonglong2 l4 = l[q];
-              sum[0] = add2(sum[0], ex2_pair(fma2(pair(v[4 * q], v[4 * q + 1]), cc, l4.x)));
-              sum[1] = add2(sum[1], ex2_pair(fma2(pair(v[4 * q + 2], v[4 * q + 3]), cc, l4.y)));
-            }
+          for (int q = 0; q < 8; ++q) {
+            const ulonglong2 l4 = l[q];
+            sum[0] = add2(sum[0], ex2_pair(fma2(pair(v[4 * q], v[4 * q + 1]), cc, l4.x)));
+            sum[1] = add2(sum[1], ex2_pair(fma2(pair(v[4 * q + 2], v[4 * q + 3]), cc, l4.y)));
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            bar_arrive(s_free(st, buf));
-            bar_arrive(l_empty(slot));
-          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          bar_arrive(s_free(st, buf));
+          bar_arrive(l_empty(slot));
         }
         if (++slot == NL) {
           slot = 0;
