@@ -339,19 +339,26 @@ ZHA_API int zha_dense_weights(const zha_config* cfg, const void* K, const void* 
  *              its entries [keep, n) are set to zero: the places of tokens to come.
  *   idx      - [Hkv][keep] int32: the kept tokens of each head, ascending.
  * 0 <= first, 0 <= last, 1 <= keep, first + last <= keep <= n.
- * Needs no scratch.  Asynchronous on `stream`; can be captured into a graph.
+ *   scratch  - scratch_bytes bytes, 256-byte aligned, at least
+ *              zha_evict_scratch_bytes(cfg, n) (which grows with n; 0 up to 16K tokens, and for an
+ *              invalid request; NULL will do where it is 0; ZHA_ERR_CAPACITY when it
+ *              is smaller).  Needs no initialisation; shared as that of zha_prefix_decode.
+ * Asynchronous on `stream`; can be captured into a graph.
  */
+ZHA_API size_t zha_evict_scratch_bytes(const zha_config* cfg, int64_t n);
 ZHA_API int zha_cache_evict(const zha_config* cfg, const void* K, const void* V, int64_t ld, int64_t n, const float* acc,
                     int64_t ld_acc, int64_t keep, int64_t first, int64_t last, void* K_out, void* V_out, int64_t ld_out,
-                    float* acc_out, int64_t ld_acc_out, int32_t* idx, void* stream);
+                    float* acc_out, int64_t ld_acc_out, int32_t* idx, void* scratch, size_t scratch_bytes,
+                    void* stream);
 
 /*
  * zha_tree_evict: zha_cache_evict in place on a tree's own cache, then the tree
  * over the kept tokens (as zha_tree_build(keep)).  acc - [Hkv][ld_acc], shortened
- * in place.  `keep` is at most zha_tree_size.
+ * in place.  `keep` is at most zha_tree_size.  Scratch as for zha_cache_evict over
+ * zha_tree_size tokens.
  */
 ZHA_API int zha_tree_evict(zha_tree* tree, float* acc, int64_t ld_acc, int64_t keep, int64_t first, int64_t last,
-                   int32_t* idx, void* stream);
+                   int32_t* idx, void* scratch, size_t scratch_bytes, void* stream);
 
 /* Synchronise `stream` and return the status word at the start of a scratch of
  * zha_prefix_decode or zha_dense_weights (ZHA_OK, or ZHA_ERR_TIMEOUT when a bounded wait

@@ -350,7 +350,8 @@ def sums_case(kind, hkv, n, seed):
     ("plain", 1, 1, 0, 0), ("plain", 5, 5, 2, 3), ("plain", 4097, 1, 0, 0), ("plain", 4097, 1000, 4, 64),
     ("ties", 3001, 1500, 1, 0), ("ties", 9000, 123, 0, 100), ("equal", 2500, 700, 3, 9), ("special", 5003, 2600, 0, 1),
     ("special", 5003, 4990, 7, 0), ("small", 2049, 600, 0, 0), ("plain", 300001, 70007, 4, 1024),
-    ("plain", 3000, 100, 60, 40), ("plain", 66000, 65999, 1, 1),
+    ("plain", 3000, 100, 60, 40), ("plain", 66000, 65999, 1, 1), ("ties", 16384, 9000, 0, 0), ("special", 16385, 9001, 0, 0),
+    ("equal", 70001, 30000, 5, 7), ("special", 50007, 49000, 3, 40000), ("plain", 40000, 300, 200, 100),
 ])
 def test_evict(dtype, d, hkv, kind, n, keep, first, last):
     if n > 100000 and (dtype, d) != ("bf16", 128):

@@ -93,12 +93,12 @@ def test_weights_refusals(L, kw, code):
 def evict(L, c=None, **kw):
     MB = 1 << 20
     a = dict(K=P, V=P + 16 * MB, ld=1000, n=900, acc=P + 32 * MB, ld_acc=900, keep=100, first=4, last=8,
-             K_out=P + 48 * MB, V_out=P + 64 * MB, ld_out=100, acc_out=P + 80 * MB, ld_acc_out=100, idx=P + 96 * MB)
+             K_out=P + 48 * MB, V_out=P + 64 * MB, ld_out=100, acc_out=P + 80 * MB, ld_acc_out=100, idx=P + 96 * MB, scratch=P + 112 * MB, nbytes=BIG)
     a.update(kw)
     c = c or cfg()
     return L.zha_cache_evict(ctypes.byref(c), a["K"], a["V"], a["ld"], a["n"], a["acc"], a["ld_acc"], a["keep"],
                              a["first"], a["last"], a["K_out"], a["V_out"], a["ld_out"], a["acc_out"],
-                             a["ld_acc_out"], a["idx"], None)
+                             a["ld_acc_out"], a["idx"], a["scratch"], a["nbytes"], None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -114,6 +114,10 @@ def evict(L, c=None, **kw):
     (dict(V_out=P + (48 << 20)), zb.ZHA_ERR_INVALID),       # two outputs in one place
     (dict(idx=P + (32 << 20)), zb.ZHA_ERR_INVALID),         # the list over the sums
     (dict(K=P + 8), zb.ZHA_ERR_INVALID), (dict(acc_out=P + (80 << 20) + 2), zb.ZHA_ERR_INVALID),
+    (dict(n=50000, ld=50000, ld_acc=50000, scratch=None, acc=P + (1 << 30), K_out=P + (2 << 30), V=P + (3 << 30),
+          V_out=P + (4 << 30)), zb.ZHA_ERR_INVALID),        # a long cache needs its workspace
+    (dict(n=50000, ld=50000, ld_acc=50000, nbytes=1024, acc=P + (1 << 30), K_out=P + (2 << 30), V=P + (3 << 30),
+          V_out=P + (4 << 30)), zb.ZHA_ERR_CAPACITY),
 ])
 def test_evict_refusals(L, kw, code):
     before = L.zha_launch_count()
@@ -121,8 +125,15 @@ def test_evict_refusals(L, kw, code):
     assert L.zha_last_error() and L.zha_launch_count() == before
 
 
+def test_evict_workspace_grows_with_the_cache(L):
+    ref = ctypes.byref(cfg())
+    sizes = [L.zha_evict_scratch_bytes(ref, n) for n in (1, 16384, 16385, 40961, 300000, 1 << 20, (1 << 31) - 1)]
+    assert sizes[0] == sizes[1] == 0 and sizes[2] > 4 * 3 * 2048 * 4 and sizes == sorted(sizes)
+    assert L.zha_evict_scratch_bytes(ref, 0) == 0 and L.zha_evict_scratch_bytes(ref, 1 << 31) == 0
+
+
 def test_tree_evict_and_status_refuse_null(L):
-    assert L.zha_tree_evict(None, P, 10, 5, 0, 0, P, None) == zb.ZHA_ERR_INVALID
+    assert L.zha_tree_evict(None, P, 10, 5, 0, 0, P, None, 0, None) == zb.ZHA_ERR_INVALID
     assert L.zha_scratch_status(None, None) == zb.ZHA_ERR_INVALID
 
 

@@ -766,9 +766,14 @@ int zha_dense_weights(const zha_config* cfg, const void* K, const void* V, int64
   return ZHA_OK;
 }
 
+size_t zha_evict_scratch_bytes(const zha_config* cfg, int64_t n) {
+  if (validate(cfg) || n < 1 || n >= kMaxTokens) return 0;
+  return size_t(align256(evict_scratch_bytes(cfg->n_kv_heads, n)));
+}
+
 int zha_cache_evict(const zha_config* cfg, const void* K, const void* V, int64_t ld, int64_t n, const float* acc,
                     int64_t ld_acc, int64_t keep, int64_t first, int64_t last, void* K_out, void* V_out, int64_t ld_out,
-                    float* acc_out, int64_t ld_acc_out, int32_t* idx, void* stream) {
+                    float* acc_out, int64_t ld_acc_out, int32_t* idx, void* scratch, size_t scratch_bytes, void* stream) {
   int rc = validate(cfg);
   if (rc) return rc;
   if (!K || !V || !acc || !K_out || !V_out || !acc_out || !idx) return fail(ZHA_ERR_INVALID, "a pointer is NULL");
@@ -782,8 +787,13 @@ int zha_cache_evict(const zha_config* cfg, const void* K, const void* V, int64_t
   if (!aligned(K, 16) || !aligned(V, 16) || !aligned(K_out, 16) || !aligned(V_out, 16) || !aligned(acc, 4) ||
       !aligned(acc_out, 4) || !aligned(idx, 4))
     return fail(ZHA_ERR_INVALID, "K, V and their outputs must be 16-byte aligned, acc, acc_out and idx 4-byte");
+  const uint64_t need = evict_scratch_bytes(cfg->n_kv_heads, n);
+  if (need > 0 && (!scratch || !aligned(scratch, 256)))
+    return fail(ZHA_ERR_INVALID, "scratch must be given, 256-byte aligned");
+  if (scratch_bytes < need) return fail(ZHA_ERR_CAPACITY, "scratch is smaller than zha_evict_scratch_bytes");
   EvictArgs a;
   std::memset(&a, 0, sizeof(a));
+  a.scratch = scratch;
   a.row_bytes = cfg->d * elem_size(cfg->dtype);
   const uint64_t hk = uint64_t(cfg->n_kv_heads) - 1, rb = uint64_t(a.row_bytes);
   // inputs and outputs with the bytes they span; an output may be its own input (rows of a head then move
@@ -825,10 +835,10 @@ int zha_cache_evict(const zha_config* cfg, const void* K, const void* V, int64_t
 }
 
 int zha_tree_evict(zha_tree* t, float* acc, int64_t ld_acc, int64_t keep, int64_t first, int64_t last, int32_t* idx,
-                   void* stream) {
+                   void* scratch, size_t scratch_bytes, void* stream) {
   if (!t) return fail(ZHA_ERR_INVALID, "tree is NULL");
   int rc = zha_cache_evict(&t->cfg, t->dev.K, t->dev.V, t->cfg.capacity, t->n, acc, ld_acc, keep, first, last, t->dev.K,
-                           t->dev.V, t->cfg.capacity, acc, ld_acc, idx, stream);
+                           t->dev.V, t->cfg.capacity, acc, ld_acc, idx, scratch, scratch_bytes, stream);
   if (rc) return rc;
   return zha_tree_build(t, keep, stream);
 }

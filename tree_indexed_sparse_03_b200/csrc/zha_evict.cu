@@ -1,28 +1,20 @@
 // Eviction from a KV cache by accumulated attention weight (zha_cache_evict):
 // per KV head the tokens to keep, then the kept rows of K, V and the sums
 // moved to the front in token order.
-#include <cooperative_groups.h>
-
 #include "zha_rows.cuh"
-
-namespace cg = cooperative_groups;
 
 namespace zha {
 
 // ------------------------------------------------------------------ selection
 // The keep - first - last largest sums among tokens [first, n - last), ties to
-// the lower token.  CTAS CTAs per KV head (one, or a cluster), each warp with a contiguous run of tokens.
-// The threshold is found most significant bits first, 11 + 11 + 10 bits: shared-memory histograms, added over the
-// cluster through distributed shared memory (every CTA reads all of them, so no second
-// exchange is needed).  Then each warp counts the tokens above and at the threshold in its run, one scan over warps
-// and CTAs gives its output position, and it lists its kept tokens in order.
-// The sums are read once: RK of them stay in each thread's registers as ordered keys (RK = 0: too many,
-// read again in each of the five passes, from L2).  What is left is latency: each pass ends in two
-// barriers and a scan.
+// the lower token.  The threshold is found most significant bits first, 11 + 11 + 10 bits, from histograms of the
+// ordered keys; then each warp counts the tokens above and at the threshold in its run of tokens, a scan gives its
+// output position, and it lists its kept tokens in order.  What bounds it is latency: up to 32K tokens one CTA per head
+// keeps all keys in registers (4K tokens 5 us; read again from L2 in each pass 25 us), above that the passes are
+// kernels over the whole GPU.
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelBins = 2048;
-constexpr int kSelCluster = 8;  // the portable cluster size
 
 // Larger sum, larger key; NaN below everything; -0 equal to +0.
 __device__ __forceinline__ uint32_t evict_key(float x) {
@@ -30,175 +22,264 @@ __device__ __forceinline__ uint32_t evict_key(float x) {
   return float_to_ordered(x == 0.f ? 0.f : x);
 }
 
-template <int CTAS> __device__ __forceinline__ void sel_sync() {
-  if (CTAS > 1) cg::this_cluster().sync();
-  else __syncthreads();
-}
-
-// f(key, live) for each 32 tokens of a warp's run [t0, t1) in order; live: the lane has a token.
-template <int RK, typename F>
-__device__ __forceinline__ void sel_each(const uint32_t* regs, const float* mid, int t0, int t1, F f) {
-  const int lane = threadIdx.x & 31;
-  if (RK > 0) {
+// The bin that holds the want-th largest key and the keys above that bin, from a histogram of kSelBins bins (thread t holds
+// bins 2t and 2t + 1 from the top); the result is in found[] after the next barrier.
+__device__ __forceinline__ void sel_find(const uint32_t* hist, uint32_t want, uint32_t* wsum, uint32_t* found) {
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const uint2 two = *reinterpret_cast<const uint2*>(hist + kSelBins - 2 - 2 * tid);
+  const uint32_t v[2] = {two.y, two.x};
+  uint32_t inc = v[0] + v[1];
 #pragma unroll
-    for (int j = 0; j < RK; ++j) f(regs[j], t0 + 32 * j + lane < t1, t0 + 32 * j + lane);
-  } else {
-    for (int i0 = t0; i0 < t1; i0 += 256) {
-      float v[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int i = i0 + 32 * j + lane;
-        v[j] = i < t1 ? __ldcg(mid + i) : 0.f;
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f(evict_key(v[j]), i0 + 32 * j + lane < t1, i0 + 32 * j + lane);
-    }
+  for (int off = 1; off < 32; off <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, inc, off);
+    if (lane >= off) inc += y;
+  }
+  if (lane == 31) wsum[wid] = inc;
+  __syncthreads();
+  const uint32_t before = __reduce_add_sync(0xffffffffu, lane < wid ? wsum[lane] : 0u) + inc - v[0] - v[1];
+  if (before < want && before + v[0] >= want) {
+    found[0] = uint32_t(kSelBins - 1 - 2 * tid);
+    found[1] = before;
+  } else if (before + v[0] < want && before + v[0] + v[1] >= want) {
+    found[0] = uint32_t(kSelBins - 2 - 2 * tid);
+    found[1] = before + v[0];
   }
 }
 
-template <int CTAS, int RK> __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) {
-  __shared__ uint32_t hist[kSelBins];
-  __shared__ uint32_t wsum[kSelWarps];
-  __shared__ uint32_t found[2];  // bin of the threshold, tokens above it
-  __shared__ uint32_t wgt[kSelWarps], weq[kSelWarps];
-  __shared__ uint32_t cta_cnt[2];  // tokens above / at the threshold of this CTA
-  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  const int rank = CTAS > 1 ? int(cg::this_cluster().block_rank()) : 0;
-  const int h = blockIdx.x / CTAS;
-  int32_t* out = a.idx + int64_t(h) * a.keep;
-  pdl_trigger();
-  for (int64_t i = int64_t(rank) * kSelThreads + tid; i < a.first + a.last; i += int64_t(CTAS) * kSelThreads) {
+__device__ __forceinline__ int sel_shift(int pass) { return pass == 0 ? 21 : (pass == 1 ? 10 : 0); }
+__device__ __forceinline__ uint32_t sel_mask(int pass) { return pass == 2 ? 1023u : 2047u; }
+
+// A thread's keys: RK rounds of 32 tokens of its warp's run [t0, t1).
+template <int RK>
+__device__ __forceinline__ void sel_load(const float* mid, int t0, int t1, uint32_t* keys) {
+  const int lane = threadIdx.x & 31;
+  float v[RK];
+#pragma unroll
+  for (int j = 0; j < RK; ++j) {
+    const int i = t0 + 32 * j + lane;
+    v[j] = i < t1 ? __ldcg(mid + i) : 0.f;
+  }
+#pragma unroll
+  for (int j = 0; j < RK; ++j) keys[j] = evict_key(v[j]);
+}
+
+template <int RK>
+__device__ __forceinline__ void sel_count(const uint32_t* keys, int t0, int t1, uint32_t prefix, uint32_t* gt, uint32_t* eq) {
+  const int lane = threadIdx.x & 31;
+  uint32_t g = 0, e = 0;
+#pragma unroll
+  for (int j = 0; j < RK; ++j) {
+    const bool live = t0 + 32 * j + lane < t1;
+    g += live && keys[j] > prefix;
+    e += live && keys[j] == prefix;
+  }
+  *gt = __reduce_add_sync(0xffffffffu, g);
+  *eq = __reduce_add_sync(0xffffffffu, e);
+}
+
+// A warp lists its kept tokens: gpre keys above the threshold and epre at it come before its run.
+template <int RK>
+__device__ __forceinline__ void sel_list(const uint32_t* keys, int t0, int t1, uint32_t prefix, uint32_t want, uint32_t gpre,
+                                         uint32_t epre, int first, int32_t* out) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t below = (1u << lane) - 1u;
+#pragma unroll
+  for (int j = 0; j < RK; ++j) {
+    const int i = t0 + 32 * j + lane;
+    const bool live = i < t1, is_gt = live && keys[j] > prefix, is_eq = live && keys[j] == prefix;
+    const uint32_t bg = __ballot_sync(0xffffffffu, is_gt), be = __ballot_sync(0xffffffffu, is_eq);
+    const uint32_t ge = gpre + __popc(bg & below), ee = epre + __popc(be & below);
+    if (is_gt || (is_eq && ee < want)) out[first + ge + (ee < want ? ee : want)] = first + i;
+    gpre += __popc(bg);
+    epre += __popc(be);
+  }
+}
+
+// The tokens kept whatever their sums, by `threads` threads.
+__device__ __forceinline__ void sel_ends(const EvictArgs& a, int32_t* out, int64_t thread, int64_t threads) {
+  for (int64_t i = thread; i < a.first + a.last; i += threads) {
     if (i < a.first) out[i] = int32_t(i);
     else out[a.keep - a.last + (i - a.first)] = int32_t(a.n - a.last + (i - a.first));
   }
+}
+
+// Short caches: one CTA per head, all keys in its registers.
+template <int RK> __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) {
+  __shared__ __align__(8) uint32_t hist[kSelBins];
+  __shared__ uint32_t wsum[kSelWarps], found[2], wgt[kSelWarps], weq[kSelWarps];
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, h = blockIdx.x;
+  int32_t* out = a.idx + int64_t(h) * a.keep;
+  pdl_trigger();
+  sel_ends(a, out, tid, kSelThreads);
   const int n_mid = int(a.n - a.first - a.last);
   uint32_t want = uint32_t(a.keep - a.first - a.last);  // tokens still to take at or below the current prefix
-  if (want == 0) return;  // the same for every CTA of the cluster
-  // a warp's run of tokens, a multiple of 32 so that its rows are whole warp iterations
-  const int64_t per = (int64_t(n_mid) + CTAS * kSelWarps * 32 - 1) / (CTAS * kSelWarps * 32) * 32;
-  const int t0 = int(min64(n_mid, (int64_t(rank) * kSelWarps + wid) * per)), t1 = int(min64(n_mid, t0 + per));
-  const float* mid = a.acc + int64_t(h) * a.ld_acc + a.first;
-  uint32_t keys[RK > 0 ? RK : 1];
-  if (RK > 0) {
-    float v[RK > 0 ? RK : 1];
-#pragma unroll
-    for (int j = 0; j < RK; ++j) {
-      const int i = t0 + 32 * j + lane;
-      v[j] = i < t1 ? __ldcg(mid + i) : 0.f;
-    }
-#pragma unroll
-    for (int j = 0; j < RK; ++j) keys[j] = evict_key(v[j]);
-  }
+  if (want == 0) return;
+  // a warp's run of tokens, a multiple of 32 so that its rounds are whole
+  const int per = (n_mid + kSelWarps * 32 - 1) / (kSelWarps * 32) * 32;
+  const int t0 = min(n_mid, wid * per), t1 = min(n_mid, t0 + per);
+  uint32_t keys[RK];
+  sel_load<RK>(a.acc + int64_t(h) * a.ld_acc + a.first, t0, t1, keys);
   uint32_t prefix = 0, mask = 0;
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
-    const uint32_t bins = pass == 2 ? 1024u : 2048u;
+    const int shift = sel_shift(pass);
     for (int i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0u;
     __syncthreads();
-    sel_each<RK>(keys, mid, t0, t1, [&](uint32_t k, bool live, int) {
-      if (live && (k & mask) == prefix) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1u);
-    });
-    sel_sync<CTAS>();
-    // bins in descending order: thread t holds bins 2t and 2t + 1 from the top
-    uint32_t v[2] = {0u, 0u};
 #pragma unroll
-    for (int q = 0; q < CTAS; ++q) {
-      const uint32_t* r = CTAS > 1 ? cg::this_cluster().map_shared_rank(hist, q) : hist;
-      const uint2 two = *reinterpret_cast<const uint2*>(r + kSelBins - 2 - 2 * tid);
-      v[0] += two.y;
-      v[1] += two.x;
-    }
-    uint32_t inc = v[0] + v[1];
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, inc, off);
-      if (lane >= off) inc += y;
-    }
-    if (lane == 31) wsum[wid] = inc;
+    for (int j = 0; j < RK; ++j)
+      if (t0 + 32 * j + lane < t1 && (keys[j] & mask) == prefix) atomicAdd(&hist[(keys[j] >> shift) & sel_mask(pass)], 1u);
     __syncthreads();
-    uint32_t before = __reduce_add_sync(0xffffffffu, lane < wid ? wsum[lane] : 0u) + inc - v[0] - v[1];
-    if (before < want && before + v[0] >= want) {
-      found[0] = uint32_t(kSelBins - 1 - 2 * tid);
-      found[1] = before;
-    } else if (before + v[0] < want && before + v[0] + v[1] >= want) {
-      found[0] = uint32_t(kSelBins - 2 - 2 * tid);
-      found[1] = before + v[0];
-    }
-    sel_sync<CTAS>();  // every CTA has read the histograms; `found` is visible to this CTA
+    sel_find(hist, want, wsum, found);
+    __syncthreads();
     prefix |= found[0] << shift;
-    mask |= (bins - 1) << shift;
+    mask |= sel_mask(pass) << shift;
     want -= found[1];
   }
   // prefix is the threshold key; `want` of the tokens at it are kept, the lowest ones
-  uint32_t gt = 0, eq = 0;
-  sel_each<RK>(keys, mid, t0, t1, [&](uint32_t k, bool live, int) {
-    gt += live && k > prefix;
-    eq += live && k == prefix;
-  });
-  gt = __reduce_add_sync(0xffffffffu, gt);
-  eq = __reduce_add_sync(0xffffffffu, eq);
+  uint32_t gt, eq;
+  sel_count<RK>(keys, t0, t1, prefix, &gt, &eq);
   if (lane == 0) {
     wgt[wid] = gt;
     weq[wid] = eq;
   }
   __syncthreads();
-  uint32_t gpre = __reduce_add_sync(0xffffffffu, lane < wid ? wgt[lane] : 0u);
-  uint32_t epre = __reduce_add_sync(0xffffffffu, lane < wid ? weq[lane] : 0u);
-  if (CTAS > 1) {
-    if (tid == kSelThreads - 1) {
-      cta_cnt[0] = gpre + gt;
-      cta_cnt[1] = epre + eq;
-    }
-    sel_sync<CTAS>();
-    for (int q = 0; q < rank; ++q) {
-      const uint32_t* r = cg::this_cluster().map_shared_rank(cta_cnt, q);
-      gpre += r[0];
-      epre += r[1];
-    }
+  sel_list<RK>(keys, t0, t1, prefix, want, __reduce_add_sync(0xffffffffu, lane < wid ? wgt[lane] : 0u),
+               __reduce_add_sync(0xffffffffu, lane < wid ? weq[lane] : 0u), int(a.first), out);
+}
+
+// Long caches: chunks of 8192 tokens over the whole GPU, one kernel per pass; the histograms are added in global memory (an
+// integer sum, the same in any order).  Kernel `pass` = 0, 1, 2 adds the pass's histogram, 3 counts each chunk's keys above and at
+// the threshold, 4 lists.  Every kernel finds the bin of the pass before it from that histogram (all CTAs the
+// same one; the first leaves it for the kernels after the next).
+constexpr int kWideKeys = 8;
+constexpr int kWideChunk = kSelThreads * kWideKeys;
+
+struct WideState {       // of one head
+  uint32_t hist[3][kSelBins];
+  uint32_t prefix[4], want[4];  // after pass 0, 1, 2 (entries 1..3)
+};
+
+__global__ void __launch_bounds__(kSelThreads) evict_wide_kernel(EvictArgs a, int pass, int chunks) {
+  __shared__ __align__(8) uint32_t hist[kSelBins];
+  __shared__ uint32_t wsum[kSelWarps], found[2], wgt[kSelWarps], weq[kSelWarps];
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, h = blockIdx.y;
+  WideState* s = reinterpret_cast<WideState*>(a.scratch) + h;
+  uint32_t* counts = reinterpret_cast<uint32_t*>(reinterpret_cast<WideState*>(a.scratch) + a.hkv) + int64_t(h) * chunks * 2;
+  const int n_mid = int(a.n - a.first - a.last);
+  const float* mid = a.acc + int64_t(h) * a.ld_acc + a.first;
+  int32_t* out = a.idx + int64_t(h) * a.keep;
+  // the histogram passes take every gridDim.x-th chunk, the others have one CTA per chunk
+  int chunk = blockIdx.x;
+  int t0 = min(n_mid, chunk * kWideChunk + wid * kWideKeys * 32), t1 = min(n_mid, t0 + kWideKeys * 32);
+  uint32_t keys[kWideKeys];
+  sel_load<kWideKeys>(mid, t0, t1, keys);
+  pdl_trigger();
+  if (pass == 0) sel_ends(a, out, int64_t(blockIdx.x) * kSelThreads + tid, int64_t(gridDim.x) * kSelThreads);
+  else pdl_wait();
+  uint32_t prefix = 0, mask = 0, want = uint32_t(a.keep - a.first - a.last);
+  if (pass > 1) {
+    prefix = __ldcg(&s->prefix[pass - 1]);
+    want = __ldcg(&s->want[pass - 1]);
   }
-  sel_each<RK>(keys, mid, t0, t1, [&](uint32_t k, bool live, int i) {
-    const bool is_gt = live && k > prefix, is_eq = live && k == prefix;
-    const uint32_t bg = __ballot_sync(0xffffffffu, is_gt), be = __ballot_sync(0xffffffffu, is_eq);
-    const uint32_t below = (1u << lane) - 1u;
-    const uint32_t ge = gpre + __popc(bg & below), ee = epre + __popc(be & below);
-    if (is_gt || (is_eq && ee < want)) out[a.first + ge + (ee < want ? ee : want)] = int32_t(a.first + i);
-    gpre += __popc(bg);
-    epre += __popc(be);
-  });
-  if (CTAS > 1) sel_sync<CTAS>();  // no CTA leaves while another reads its shared memory
+  if (pass > 0 && pass < 4) {
+    const int done = pass - 1;  // the pass whose histogram is complete
+    for (int i = tid; i < kSelBins; i += kSelThreads) hist[i] = __ldcg(&s->hist[done][i]);
+    __syncthreads();
+    sel_find(hist, want, wsum, found);
+    __syncthreads();
+    prefix |= found[0] << sel_shift(done);
+    want -= found[1];
+    if (blockIdx.x == 0 && tid == 0) {
+      s->prefix[pass] = prefix;
+      s->want[pass] = want;
+    }
+    mask = ~((1u << sel_shift(done)) - 1u);
+  }
+  if (pass < 3) {
+    for (int i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0u;
+    __syncthreads();
+    while (true) {
+#pragma unroll
+      for (int j = 0; j < kWideKeys; ++j)
+        if (t0 + 32 * j + lane < t1 && (keys[j] & mask) == prefix)
+          atomicAdd(&hist[(keys[j] >> sel_shift(pass)) & sel_mask(pass)], 1u);
+      chunk += gridDim.x;
+      if (chunk >= chunks) break;
+      t0 = min(n_mid, chunk * kWideChunk + wid * kWideKeys * 32);
+      t1 = min(n_mid, t0 + kWideKeys * 32);
+      sel_load<kWideKeys>(mid, t0, t1, keys);
+    }
+    __syncthreads();
+    for (int i = tid; i < kSelBins; i += kSelThreads)
+      if (hist[i]) atomicAdd(&s->hist[pass][i], hist[i]);
+    return;
+  }
+  uint32_t gt, eq;
+  sel_count<kWideKeys>(keys, t0, t1, prefix, &gt, &eq);
+  if (lane == 0) {
+    wgt[wid] = gt;
+    weq[wid] = eq;
+  }
+  __syncthreads();
+  if (pass == 3) {
+    if (wid == 0) {
+      gt = __reduce_add_sync(0xffffffffu, wgt[lane]);
+      eq = __reduce_add_sync(0xffffffffu, weq[lane]);
+      if (lane == 0) {
+        counts[2 * chunk] = gt;
+        counts[2 * chunk + 1] = eq;
+      }
+    }
+    return;
+  }
+  uint32_t gpre = lane < wid ? wgt[lane] : 0u, epre = lane < wid ? weq[lane] : 0u;
+  for (int q = lane; q < chunk; q += 32) {
+    gpre += __ldcg(counts + 2 * q);
+    epre += __ldcg(counts + 2 * q + 1);
+  }
+  sel_list<kWideKeys>(keys, t0, t1, prefix, want, __reduce_add_sync(0xffffffffu, gpre), __reduce_add_sync(0xffffffffu, epre),
+                      int(a.first), out);
 }
 
-template <int CTAS, int RK> cudaError_t run_select(const EvictArgs& a, cudaStream_t st) {
-  cudaLaunchConfig_t c = {};
-  c.gridDim = dim3(unsigned(a.hkv) * CTAS);
-  c.blockDim = dim3(kSelThreads);
-  c.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = CTAS;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  c.attrs = at;
-  c.numAttrs = CTAS > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&c, evict_select_kernel<CTAS, RK>, a);
+constexpr int kShortMost = 16 * kSelThreads;  // up to here one CTA holds all keys (30K tokens: 22 us with 32 a thread, 16 us over
+                                              // the whole GPU)
+
+static int64_t wide_chunks(int64_t mid) { return (mid + kWideChunk - 1) / kWideChunk; }
+
+// Scratch of the long caches' selection over n tokens (whatever first and last are).
+uint64_t evict_scratch_bytes(int hkv, int64_t n) {
+  return n <= kShortMost ? 0 : uint64_t(hkv) * (sizeof(WideState) + uint64_t(wide_chunks(n)) * 8);
 }
 
-// One CTA where its registers hold all keys without waiting for a cluster; a cluster of eight above, its registers up to
-// 256K tokens.
+template <int RK> static cudaError_t run_select(const EvictArgs& a, cudaStream_t st) {
+  count_launches(1);
+  evict_select_kernel<RK><<<unsigned(a.hkv), kSelThreads, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
 static cudaError_t launch_select(const EvictArgs& a, cudaStream_t st) {
   const int64_t mid = a.n - a.first - a.last;
-  if (mid <= 4 * kSelThreads) return run_select<1, 4>(a, st);
-  if (mid <= 16 * kSelThreads) return run_select<1, 16>(a, st);
-  if (mid <= 8 * kSelThreads * kSelCluster) return run_select<kSelCluster, 8>(a, st);
-  if (mid <= 32 * kSelThreads * kSelCluster) return run_select<kSelCluster, 32>(a, st);
-  return run_select<kSelCluster, 0>(a, st);
+  if (mid <= 4 * kSelThreads || a.keep == a.first + a.last) return run_select<4>(a, st);
+  if (mid <= kShortMost) return run_select<16>(a, st);
+  count_launches(5);
+  cudaError_t e = cudaMemsetAsync(a.scratch, 0, size_t(a.hkv) * sizeof(WideState), st);
+  if (e != cudaSuccess) return e;
+  const int chunks = int(wide_chunks(mid));
+  const int few = int(min64(chunks, (2 * 148 + a.hkv - 1) / a.hkv));  // two CTAs per SM: one merge into the global histogram each
+  evict_wide_kernel<<<dim3(unsigned(few), unsigned(a.hkv)), kSelThreads, 0, st>>>(a, 0, chunks);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  for (int pass = 1; pass < 5; ++pass) {
+    const dim3 grid(unsigned(pass < 3 ? few : chunks), unsigned(a.hkv));
+    if ((e = launch_after(evict_wide_kernel, grid, kSelThreads, 0, st, a, pass, chunks)) != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 // ------------------------------------------------------------------ moving the rows
-// Separate outputs: a plain gather.  Each thread moves four 16-byte pieces, kMoveRows kept
-// rows apart, so that four loads are in flight; bound by HBM (each kept row read and
-// written once).
-constexpr int kMoveThreads = 256;
+// Separate outputs: a plain gather.  Each thread has four 16-byte pieces in flight; bound by HBM
+// (each kept row read and written once).  1M -> 512K tokens, 4 heads of 128 bf16: 128 threads and streaming stores 435 us with the
+// selection, 256 and plain stores 465, eight pieces 507, two 489.
+constexpr int kMoveThreads = 128;
 constexpr int kMoveUnroll = 4;
 
 __global__ void __launch_bounds__(kMoveThreads) evict_gather_kernel(EvictArgs a) {
@@ -227,7 +308,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_gather_kernel(EvictArgs a)
 #pragma unroll
   for (int u = 0; u < kMoveUnroll; ++u) {
     const int64_t i = i0 + u * kMoveThreads;
-    if (i < pieces) *reinterpret_cast<uint4*>(dst + i * 16) = v[u];
+    if (i < pieces) __stcs(reinterpret_cast<uint4*>(dst + i * 16), v[u]);  // not read again soon
   }
 }
 
@@ -280,7 +361,7 @@ __global__ void __launch_bounds__(kSlideThreads) evict_slide_kernel(EvictArgs a)
 }
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st) {
-  count_launches(2);
+  count_launches(1);
   const cudaError_t e = launch_select(a, st);
   if (e != cudaSuccess) return e;
   if (a.in_place)

@@ -326,10 +326,12 @@ struct EvictArgs {
   void* V_out;
   float* acc_out;
   int32_t* idx;           // [hkv][keep]
+  void* scratch;          // evict_scratch_bytes (long caches)
   int64_t ld, ld_acc, ld_out, ld_acc_out, n, keep, first, last;
   int hkv, row_bytes;     // bytes of one token's row of K or V
   int in_place;           // some output is its own input: rows move in order
 };
+uint64_t evict_scratch_bytes(int hkv, int64_t n);
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st);
 
 }  // namespace zha

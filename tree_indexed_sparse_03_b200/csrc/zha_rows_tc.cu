@@ -599,29 +599,52 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
           }
         }
         if (PV) {
-          float* dst = whole ? a.O + ri * D : a.part + pr * D;
+          // through shared memory, half a row at a time, so that it leaves in whole runs (one thread's row
+          // straight from its registers took 4 us a segment): over the other stream's rows when joining, else over the
+          // stream's own queries, which no product reads any more
+          constexpr int HC = D / 2, LN = HC / 4;  // columns of a half, lanes for one
+          const int stride = join ? D * 4 : HC * 4;
+          const uint32_t mine = join ? xrow : base + st * Sh::kQ + row * stride;
 #pragma unroll 1
-          for (int j = 0; j < D; j += 32) {
-            float v[32];
-            tmem_ld32(to + j, v);
-            tmem_wait32(v);
-            if (row < nrows) {
+          for (int c0 = 0; c0 < D; c0 += HC) {
+            const uint32_t at = mine + (join ? c0 * 4 : 0);
+#pragma unroll 1
+            for (int j = 0; j < HC; j += 32) {
+              float v[32];
+              tmem_ld32(to + c0 + j, v);
+              tmem_wait32(v);
 #pragma unroll
               for (int q = 0; q < 8; ++q) {
+                const uint32_t cell = at + ((((j >> 2) + q) ^ (row & 7)) << 4);
                 float4 o = make_float4(v[4 * q] * inv, v[4 * q + 1] * inv, v[4 * q + 2] * inv, v[4 * q + 3] * inv);
                 if (join && other_s != 0.f) {
                   float4 t;
                   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
                                : "=f"(t.x), "=f"(t.y), "=f"(t.z), "=f"(t.w)
-                               : "r"(xrow + ((((j >> 2) + q) ^ (row & 7)) << 4)));
+                               : "r"(cell));
                   o.x = fmaf(t.x, other_s, o.x);
                   o.y = fmaf(t.y, other_s, o.y);
                   o.z = fmaf(t.z, other_s, o.z);
                   o.w = fmaf(t.w, other_s, o.w);
                 }
-                *reinterpret_cast<float4*>(dst + j + 4 * q) = o;
+                asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(cell), "f"(o.x), "f"(o.y), "f"(o.z), "f"(o.w)
+                             : "memory");
               }
             }
+            __syncwarp();
+            const uint32_t warp_at = at - lane * stride;
+            const int ln = lane % LN;
+#pragma unroll 4
+            for (int r = lane / LN; r < min(32, nrows - wrow); r += 32 / LN) {
+              const int rr = wrow + r;
+              float4 o;
+              asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                           : "=f"(o.x), "=f"(o.y), "=f"(o.z), "=f"(o.w)
+                           : "r"(warp_at + r * stride + ((ln ^ (rr & 7)) << 4)));
+              float* dst = whole ? a.O + row_index(a, w.s.h, row_off + r0 + rr) * D : a.part + (pr - row + rr) * D;
+              *reinterpret_cast<float4*>(dst + c0 + ln * 4) = o;
+            }
+            __syncwarp();
           }
         }
       }

@@ -58,9 +58,11 @@ _SIGS = {
                                      _c.c_int64, _c.c_void_p, _c.c_size_t, _c.c_void_p]),
     "zha_cache_evict": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int64, _c.c_int64, _c.c_void_p,
                                    _c.c_int64, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_void_p, _c.c_void_p,
-                                   _c.c_int64, _c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_void_p]),
+                                   _c.c_int64, _c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_void_p, _c.c_size_t,
+                                   _c.c_void_p]),
+    "zha_evict_scratch_bytes": (_c.c_size_t, [_c.c_void_p, _c.c_int64]),
     "zha_tree_evict": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_int64,
-                                  _c.c_void_p, _c.c_void_p]),
+                                  _c.c_void_p, _c.c_void_p, _c.c_size_t, _c.c_void_p]),
     "zha_scratch_status": (_c.c_int, [_c.c_void_p, _c.c_void_p]),
     "zha_tree_status": (_c.c_int, [_c.c_void_p, _c.c_void_p]),
     "zha_tree_set_step_p": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_int32]),
@@ -269,7 +271,8 @@ class ZhaTree:
         if acc.get_device() != dev or self.K.get_device() != dev:
             _refuse_device("the cache and acc")
         idx = _empty(acc, (c.n_kv_heads, keep), torch.int32, stream)
-        _check(lib().zha_tree_evict(self._h, acc.data_ptr(), ld_acc, keep, first, last, idx.data_ptr(),
+        work, nbytes = _evict_scratch(c, acc, n, stream)
+        _check(lib().zha_tree_evict(self._h, acc.data_ptr(), ld_acc, keep, first, last, idx.data_ptr(), _ptr(work), nbytes,
                                     _stream(stream)))
         return idx
 
@@ -583,6 +586,11 @@ class DenseWeights(_Attend):
         return out, acc_out
 
 
+def _evict_scratch(cfg: ZhaConfig, acc: torch.Tensor, n: int, stream):
+    nbytes = lib().zha_evict_scratch_bytes(ctypes.byref(cfg), n)
+    return (_empty(acc, (nbytes,), torch.uint8, stream) if nbytes else None), nbytes
+
+
 def cache_evict(cfg: ZhaConfig, K: torch.Tensor, V: torch.Tensor, n: int, acc: torch.Tensor, keep: int, *,
                 first: int = 0, last: int = 0, K_out: Optional[torch.Tensor] = None,
                 V_out: Optional[torch.Tensor] = None, acc_out: Optional[torch.Tensor] = None, stream=None):
@@ -620,9 +628,10 @@ def cache_evict(cfg: ZhaConfig, K: torch.Tensor, V: torch.Tensor, n: int, acc: t
         if acc_out.get_device() != dev:
             _refuse_device("acc_out")
     idx = _empty(acc, (hkv, keep), torch.int32, stream)
+    work, nbytes = _evict_scratch(cfg, acc, n, stream)
     rc = lib().zha_cache_evict(ctypes.byref(cfg), K.data_ptr(), V.data_ptr(), ld, n, acc.data_ptr(), ld_acc, keep, first,
                                last, K_out.data_ptr(), V_out.data_ptr(), ld_out, acc_out.data_ptr(), ld_acc_out,
-                               idx.data_ptr(), _raw_stream(stream, dev))
+                               idx.data_ptr(), _ptr(work), nbytes, _raw_stream(stream, dev))
     if rc:
         _check(rc)
     return idx, acc_out
