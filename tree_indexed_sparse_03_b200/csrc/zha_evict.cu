@@ -110,6 +110,7 @@ template <int RK> __global__ void __launch_bounds__(kSelThreads) evict_select_ke
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, h = blockIdx.x;
   int32_t* out = a.idx + int64_t(h) * a.keep;
   pdl_trigger();
+  pdl_wait();
   sel_ends(a, out, tid, kSelThreads);
   const int n_mid = int(a.n - a.first - a.last);
   uint32_t want = uint32_t(a.keep - a.first - a.last);  // tokens still to take at or below the current prefix
@@ -253,8 +254,7 @@ uint64_t evict_scratch_bytes(int hkv, int64_t n) {
 
 template <int RK> static cudaError_t run_select(const EvictArgs& a, cudaStream_t st) {
   count_launches(1);
-  evict_select_kernel<RK><<<unsigned(a.hkv), kSelThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_after(evict_select_kernel<RK>, dim3(unsigned(a.hkv)), kSelThreads, 0, st, a);
 }
 
 static cudaError_t launch_select(const EvictArgs& a, cudaStream_t st) {

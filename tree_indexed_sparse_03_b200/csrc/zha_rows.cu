@@ -31,6 +31,7 @@ __global__ void __launch_bounds__(kRowsThreads) rows_scalar_kernel(RowsArgs a) {
   const int half = wid * 2 + (lane >> 4), l16 = lane & 15;
   const float c2 = a.scale * 1.4426950408889634f;  // weights as powers of two
   pdl_trigger();
+  pdl_wait();
   const RowsTotals tot = rows_totals(a);
   if (blockIdx.x == 0 && wid == 0) rows_publish(a, tot);
   const int x_begin = tot.sh.begin(blockIdx.x), x_end = tot.sh.begin(blockIdx.x + 1);
@@ -470,8 +471,7 @@ template <typename T, int D, int RT> cudaError_t run_rows(const RowsArgs& a, cud
   const size_t sm = rows_smem(D, RT);
   cudaError_t e = allow_smem(rows_scalar_kernel<T, D, RT>, sm);
   if (e != cudaSuccess) return e;
-  rows_scalar_kernel<T, D, RT><<<a.nc, kRowsThreads, sm, st>>>(a);
-  return cudaGetLastError();
+  return launch_after(rows_scalar_kernel<T, D, RT>, dim3(a.nc), kRowsThreads, sm, st, a);
 }
 
 template <typename T, int D> cudaError_t run_rows_rt(const RowsArgs& a, cudaStream_t st) {

@@ -152,6 +152,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
     tmem_alloc(smem_u32(&tmem_base), 512);
   }
   pdl_trigger();
+  pdl_wait();  // everything above runs under the end of the kernel before
   const RowsTotals tot = rows_totals(a);
   const int x_begin = tot.sh.begin(blockIdx.x), x_end = tot.sh.begin(blockIdx.x + 1);
   int x = x_begin;
@@ -165,6 +166,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
     int slot = 0;
     uint32_t round = 0, fix_phase = 0;
     bool ok = true;
+    const uint64_t once = l2_evict_first(), many = l2_evict_normal();
     int pend_slot = -1, pend_row = 0;  // a V tile whose rows from pend_row on are still to be cleared
     auto clear_pending = [&]() {
       if (pend_slot < 0) return true;
@@ -185,6 +187,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
     };
     while (ok && next_work(a, tot, &x, x_end, &w)) {
       const int lag = w.both ? 1 : 2;
+      // tiles that no other row block reads go first when L2 needs room (kept logits stay)
+      const uint64_t policy = w.s.own || a.pp == 1 ? once : many;
       const CUtensorMap* mk = w.s.own ? &maps.ko : &maps.k;
       const CUtensorMap* mv = w.s.own ? &maps.vo : &maps.v;
       const int plane = w.s.own ? w.s.b * a.hkv + w.s.h : w.s.h;
@@ -206,7 +210,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
         if (lane == 0) {
           bar_expect(bar, Sh::kTile);
 #pragma unroll
-          for (int p = 0; p < PANELS; ++p) tma_load(dst + p * PANEL, kv ? mv : mk, bar, p * 64, k0, plane);
+          for (int p = 0; p < PANELS; ++p) tma_load(dst + p * PANEL, kv ? mv : mk, bar, p * 64, k0, plane, policy);
         }
         if (clear) {
           pend_slot = slot;
@@ -704,8 +708,7 @@ namespace {
 template <int D, bool PV, bool LG> cudaError_t run_tc_as(const RowsArgs& a, const TcMaps& maps, cudaStream_t st) {
   const cudaError_t e = allow_smem(rows_tc_kernel<D, PV, LG>, TcShape<D>::kSmem);
   if (e != cudaSuccess) return e;
-  rows_tc_kernel<D, PV, LG><<<a.nc, kTcThreads, TcShape<D>::kSmem, st>>>(a, maps);
-  return cudaGetLastError();
+  return launch_after(rows_tc_kernel<D, PV, LG>, dim3(a.nc), kTcThreads, TcShape<D>::kSmem, st, a, maps);
 }
 
 template <int D> cudaError_t run_tc(const RowsArgs& a, const TcMaps& maps, cudaStream_t st) {

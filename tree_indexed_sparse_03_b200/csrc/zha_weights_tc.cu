@@ -186,6 +186,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
     int slot = 0, ks = 0;
     uint32_t round = 0, k_round = 0;
     bool ok = true;
+    const uint64_t many = l2_evict_normal();
     const uint32_t tile_bytes = uint32_t(wt_box_rows(a.group)) * D * 2;
     while (x < x_end && ok) {
       const WtSeg s = wt_find(a, plan, x);
@@ -198,7 +199,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
 #pragma unroll
           for (int p = 0; p < PANELS; ++p)
             tma_load(k_sm + (2 * ks + st) * Sh::kHalf + p * 128 * 128, &maps.k, k_full(ks), p * 64,
-                     s.seg * kWtKeys + st * 128, s.h);
+                     s.seg * kWtKeys + st * 128, s.h, many);
       }
       if (++ks == 2) {
         ks = 0;
@@ -212,7 +213,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
 #pragma unroll
           for (int p = 0; p < PANELS; ++p)
             tma_load(ring + slot * Sh::kHalf + p * 128 * 128, &maps.q, full(slot), p * 64,
-                     s.h * a.group + w.g0, w.tok0);
+                     s.h * a.group + w.g0, w.tok0, many);
         }
         if (++slot == NS) {
           slot = 0;
