@@ -106,6 +106,7 @@ def check_prefix(dtype, d, hkv, group, B, m, n, own, lens, seed=1, ld=None):
     (2, 8, 19, 1, 1025, 129, [(b * 37) % 130 for b in range(19)]),
     (1, 8, 70, 4, 515, 20, [(b * 7) % 21 for b in range(70)]),
     (4, 8, 3, 1, 5003, 260, [260, 0, 131]),
+    (4, 3, 120, 1, 100, 300, [(b * 61) % 301 for b in range(120)]),  # several short segments per CTA
 ])
 def test_prefix(dtype, d, hkv, group, B, m, n, own, lens):
     check_prefix(dtype, d, hkv, group, B, m, n, own, lens, ld=n + 5 if n % 2 else n)
@@ -211,6 +212,43 @@ def test_prefix_slices_streams_and_graphs():
         close(out2, want, tol, "replay beside another")
     dec.status()
     dec2.status()
+
+
+def test_prefix_without_any_key():
+    """No prefix and no own caches: every query sees nothing."""
+    cfg = cfg_of("bf16", 128, 2, 3)
+    o, lse = z.prefix_decode(cfg, None, None, 0, rnd(1, 2, 1, 6, 128).cuda(), want_lse=True)
+    assert bool((o == 0).all()) and bool((lse == -math.inf).all())
+    assert z.prefix_decode(cfg, None, None, 0, rnd(1, 0, 1, 6, 128).cuda()).shape == (0, 1, 6, 128)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_calls_back_to_back(dtype):
+    """Forty calls of two operators in one workspace each, nothing waiting between them (each starts under the end of the one
+    before): the bits of the same calls made one at a time."""
+    d, n, B = 64, 900, 3
+    cfg = cfg_of(dtype, d, 2, 4)
+    K, V = rnd(1, 2, n, d, dtype=dtype).cuda(), rnd(2, 2, n, d, dtype=dtype).cuda()
+    Ko, Vo = rnd(3, B, 2, 300, d, dtype=dtype).cuda(), rnd(4, B, 2, 300, d, dtype=dtype).cuda()
+    ln = [torch.tensor([(i * 97) % 301, (i * 31) % 301, 300], dtype=torch.int32, device="cuda") for i in range(20)]
+    Qs = [rnd(10 + i, B, 1, 8, d, dtype=dtype, scale=2.0).cuda() for i in range(20)]
+    dec, w = z.PrefixDecoder(cfg, B, n, 300), z.DenseWeights(cfg, 40, n)
+    Qw = [rnd(50 + i, 40, 8, d, dtype=dtype, scale=2.0).cuda() for i in range(20)]
+
+    def one(i):
+        o = dec(K, V, n - i, Qs[i], Ko, Vo, ln[i], want_lse=True)
+        return [*o, *w(K, V, n - 2 * i, Qw[i], causal=bool(i & 1))]
+
+    alone = []
+    for i in range(20):
+        alone.append([t.clone() for t in one(i)])
+        torch.cuda.synchronize()
+    together = [one(i) for i in range(20)]
+    torch.cuda.synchronize()
+    dec.status()
+    w.status()
+    for x, y in zip(alone, together):
+        assert all(torch.equal(p, q) for p, q in zip(x, y))
 
 
 # ---------------------------------------------------------------- weights

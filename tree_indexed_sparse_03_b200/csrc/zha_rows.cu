@@ -76,19 +76,30 @@ __global__ void __launch_bounds__(kRowsThreads) rows_scalar_kernel(RowsArgs a) {
     for (int t = t_begin; t < t_end; ++t) {
       const int64_t k0 = int64_t(t) * kRowsKeys;
       __syncthreads();
-      for (int i = tid; i < kRowsKeys * CPR; i += kRowsThreads) {
-        const int r = i / CPR, c = i % CPR;
-        float k[EPC], v[EPC];
+      constexpr int G = RT < 8 ? 8 : 4;  // 16-byte pieces of K and of V in flight per thread (RT = 8: the registers are needed)
+#pragma unroll 1
+      for (int i0 = tid; i0 < kRowsKeys * CPR; i0 += G * kRowsThreads) {
+        uint4 kr[G], vr[G];
 #pragma unroll
-        for (int e = 0; e < EPC; ++e) k[e] = v[e] = 0.f;  // keys past the range: zeros, never what lies there
-        if (k0 + r < len) {
-          unpack16<T>(ldg_stream(Kh + (k0 + r) * D + c * EPC), k);
-          if (Vh) unpack16<T>(ldg_stream(Vh + (k0 + r) * D + c * EPC), v);
+        for (int g = 0; g < G; ++g) {
+          const int i = i0 + g * kRowsThreads, r = i / CPR, c = i % CPR;
+          kr[g] = vr[g] = make_uint4(0, 0, 0, 0);  // keys past the range: zeros, never what lies there
+          if (k0 + r < len) {
+            kr[g] = ldg_stream(Kh + (k0 + r) * D + c * EPC);
+            if (Vh) vr[g] = ldg_stream(Vh + (k0 + r) * D + c * EPC);
+          }
         }
 #pragma unroll
-        for (int e = 0; e < EPC; e += 4) {
-          *reinterpret_cast<float4*>(sk + r * LD + c * EPC + e) = make_float4(k[e], k[e + 1], k[e + 2], k[e + 3]);
-          if (Vh) *reinterpret_cast<float4*>(sv + r * LD + c * EPC + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        for (int g = 0; g < G; ++g) {
+          const int i = i0 + g * kRowsThreads, r = i / CPR, c = i % CPR;
+          float k[EPC], v[EPC];
+          unpack16<T>(kr[g], k);
+          unpack16<T>(vr[g], v);
+#pragma unroll
+          for (int e = 0; e < EPC; e += 4) {
+            *reinterpret_cast<float4*>(sk + r * LD + c * EPC + e) = make_float4(k[e], k[e + 1], k[e + 2], k[e + 3]);
+            if (Vh) *reinterpret_cast<float4*>(sv + r * LD + c * EPC + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+          }
         }
       }
       __syncthreads();

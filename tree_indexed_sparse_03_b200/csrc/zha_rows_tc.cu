@@ -336,8 +336,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
       const int nrows = min(128, w.seg_rows - r0);
       const int row_off = w.s.own ? w.s.b * a.m * a.group : 0;
       {
-        constexpr int CH = D / 8, RP = 128 / CH;  // 16-byte pieces of a row, rows per pass of the stream's threads
-        const int c = row % CH, rq = row / CH;
+        // every warp its own rows: they are where its last results left from, and no other warp waits for that
+        constexpr int CH = D / 8, RP = 32 / CH;  // 16-byte pieces of a row, rows per pass of a warp
+        const int c = lane % CH, rq = wrow + lane / CH;
         const __nv_bfloat16* Qp = static_cast<const __nv_bfloat16*>(a.Q) + c * 8;
         const uint32_t dst = base + st * Sh::kQ + (c / 8) * (128 * 128);
 #pragma unroll 1
@@ -607,11 +608,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
           // straight from its registers took 4 us a segment): over the other stream's rows when joining, else over the
           // stream's own queries, which no product reads any more
           constexpr int HC = D / 2, LN = HC / 4;  // columns of a half, lanes for one
-          const int stride = join ? D * 4 : HC * 4;
-          const uint32_t mine = join ? xrow : base + st * Sh::kQ + row * stride;
+          // 16-byte piece k of the half from column c0 on, of row r
+          auto cell = [&](int c0, int k, int r) {
+            return join ? base + r * (D * 4) + c0 * 4 + ((k ^ (r & 7)) << 4)
+                        : base + st * Sh::kQ + (k >> 3) * (128 * 128) + r * 128 + (((k & 7) ^ (r & 7)) << 4);
+          };
 #pragma unroll 1
           for (int c0 = 0; c0 < D; c0 += HC) {
-            const uint32_t at = mine + (join ? c0 * 4 : 0);
 #pragma unroll 1
             for (int j = 0; j < HC; j += 32) {
               float v[32];
@@ -619,24 +622,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
               tmem_wait32(v);
 #pragma unroll
               for (int q = 0; q < 8; ++q) {
-                const uint32_t cell = at + ((((j >> 2) + q) ^ (row & 7)) << 4);
+                const uint32_t at = cell(c0, (j >> 2) + q, row);
                 float4 o = make_float4(v[4 * q] * inv, v[4 * q + 1] * inv, v[4 * q + 2] * inv, v[4 * q + 3] * inv);
                 if (join && other_s != 0.f) {
                   float4 t;
                   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
                                : "=f"(t.x), "=f"(t.y), "=f"(t.z), "=f"(t.w)
-                               : "r"(cell));
+                               : "r"(at));
                   o.x = fmaf(t.x, other_s, o.x);
                   o.y = fmaf(t.y, other_s, o.y);
                   o.z = fmaf(t.z, other_s, o.z);
                   o.w = fmaf(t.w, other_s, o.w);
                 }
-                asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(cell), "f"(o.x), "f"(o.y), "f"(o.z), "f"(o.w)
+                asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(o.x), "f"(o.y), "f"(o.z), "f"(o.w)
                              : "memory");
               }
             }
             __syncwarp();
-            const uint32_t warp_at = at - lane * stride;
             const int ln = lane % LN;
 #pragma unroll 4
             for (int r = lane / LN; r < min(32, nrows - wrow); r += 32 / LN) {
@@ -644,7 +646,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
               float4 o;
               asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
                            : "=f"(o.x), "=f"(o.y), "=f"(o.z), "=f"(o.w)
-                           : "r"(warp_at + r * stride + ((ln ^ (rr & 7)) << 4)));
+                           : "r"(cell(c0, ln, rr)));
               float* dst = whole ? a.O + row_index(a, w.s.h, row_off + r0 + rr) * D : a.part + (pr - row + rr) * D;
               *reinterpret_cast<float4*>(dst + c0 + ln * 4) = o;
             }

@@ -30,9 +30,9 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-// Bounded wait: about a second of SM cycles.  `gave_up` is shared by the CTA: once any wait runs out, every
+// Bounded wait: about four seconds of SM cycles.  `gave_up` is shared by the CTA: once any wait runs out, every
 // other wait returns false at its next look, so that all roles leave their loops.
-constexpr long long kTcWaitCycles = 1ll << 31;
+constexpr long long kTcWaitCycles = 1ll << 33;
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
   if (bar_try(bar, parity)) return true;
   const long long t0 = clock64();

@@ -521,8 +521,8 @@ class PrefixDecoder(_Attend):
 def prefix_decode(cfg: ZhaConfig, K, V, n: int, Q: torch.Tensor, K_own=None, V_own=None, own_len=None, *,
                   want_lse: bool = False, stream=None):
     """One call of a PrefixDecoder made for it."""
-    dec = PrefixDecoder(cfg, Q.shape[0], n, 0 if K_own is None else K_own.shape[-2], Q.shape[1] if Q.dim() == 4 else 1,
-                        device=Q.device)
+    dec = PrefixDecoder(cfg, max(1, Q.shape[0]), n, 0 if K_own is None else K_own.shape[-2],
+                        max(1, Q.shape[1]) if Q.dim() == 4 else 1, device=Q.device)
     res = dec(K, V, n, Q, K_own, V_own, own_len, want_lse=want_lse, stream=stream)
     if stream is not None:
         dec.scratch.record_stream(stream)
