@@ -214,6 +214,40 @@ def test_prefix_slices_streams_and_graphs():
     dec2.status()
 
 
+@pytest.mark.parametrize("B,m,own,rising", [(1, 1, 0, False), (1, 1, 0, True), (40, 8, 60, False), (40, 8, 60, True)])
+def test_prefix_long(B, m, own, rising):
+    """Shares of many tiles: the accumulator is added up outside tensor memory several times, also while the running maximum
+    moves (rising: keys grow along the cache by a factor of 16, each longer key ahead of all before it)."""
+    n, hkv, d = 700003, 1, 64
+    K, V = rnd(1, hkv, n, d).cuda(), rnd(2, hkv, n, d).cuda()
+    Q = rnd(3, B, m, 4, d, scale=2.0).cuda()
+    if rising:
+        K = (K * (0.25 + 3.75 * torch.arange(n, device="cuda")[:, None] / n)).to(torch.bfloat16)
+    Ko, Vo = (rnd(4, B, hkv, own, d).cuda(), rnd(5, B, hkv, own, d).cuda()) if own else (None, None)
+    ln = torch.tensor([(b * 7) % (own + 1) for b in range(B)], dtype=torch.int32, device="cuda") if own else None
+    dec = z.PrefixDecoder(cfg_of("bf16", d, hkv, 4, capacity=n), B, n, own, m)
+    o, lse = dec(K, V, n, Q, Ko, Vo, ln, want_lse=True)
+    torch.cuda.synchronize()
+    dec.status()
+    k, v = K[0].double(), V[0].double()
+    worst = norm = 0.0
+    for b in range(0, B, 13):
+        for i in range(m):
+            seen = max(0, int(ln[b]) - m + i + 1) if own else 0
+            kk = torch.cat([k, Ko[b, 0, :seen].double()]) if seen else k
+            vv = torch.cat([v, Vo[b, 0, :seen].double()]) if seen else v
+            x = Q[b, i].double() @ kk.T / math.sqrt(d)
+            want = torch.softmax(x, 1) @ vv
+            worst += float((o[b, i].double() - want).square().sum())
+            norm += float(want.square().sum())
+            # logits up to 64: the exponent's argument is rounded to 64 * 2^-23 = 8e-6, weights to 1.9e-5 in all; the same
+            # for the sum
+            assert float((o[b, i].double() - want).abs().max()) <= 4e-5 * float(v.abs().max())
+            assert float((lse[b, i].double() - torch.logsumexp(x, 1)).abs().max()) <= 4e-5
+    # by the 2-norm: 16 tiles of 16 products add at most 256 * 2^-24 = 1.5e-5 of an output (all of the same sign), beside the 1.9e-5
+    assert math.sqrt(worst / norm) <= 3.4e-5
+
+
 def test_prefix_without_any_key():
     """No prefix and no own caches: every query sees nothing."""
     cfg = cfg_of("bf16", 128, 2, 3)

@@ -618,6 +618,8 @@ static void fill_rows(const zha_config* cfg, const RowsPlan& p, int32_t B, int32
   a->status = static_cast<int*>(scratch);
   a->plan = reinterpret_cast<int*>(static_cast<char*>(scratch) + kScratchHead);
   a->part = reinterpret_cast<float*>(static_cast<char*>(scratch) + kScratchHead + rows_plan_bytes(cfg, B, m));
+  a->part_tmp = a->part + p.part_tmp * cfg->d;
+  a->rt = p.rt;
   a->part_ml = reinterpret_cast<float2*>(a->part + p.part_rows * cfg->d);
 }
 

@@ -532,6 +532,8 @@ static void plan_parts(int hkv, int64_t B, int64_t n, int64_t ld_own, int most, 
     p->part_own = 0;
     p->part_rows = 2 * uint64_t(p->nc) * p->rp;
   }
+  p->part_tmp = p->part_rows;
+  p->part_rows += uint64_t(p->nc) * p->rt;
 }
 
 static void scalar_plan(int d, int rt, int hkv, int64_t B, int64_t rows, int64_t mg, int64_t n, int64_t ld_own,
@@ -544,6 +546,7 @@ static void scalar_plan(int d, int rt, int hkv, int64_t B, int64_t rows, int64_t
   p->po = ld_own > 0 ? int((mg + rb - 1) / rb) : 0;
   p->rp = int(rows < rb ? rows : rb);
   p->ro = int(mg < rb ? mg : rb);
+  p->rt = 0;
   const int per_sm = int(220 * 1024 / (rows_smem(d, rt) + 1024));
   plan_parts(hkv, B, n, ld_own, 148 * (per_sm < 1 ? 1 : (per_sm > 4 ? 4 : per_sm)), p);
 }

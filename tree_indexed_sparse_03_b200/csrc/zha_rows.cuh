@@ -32,6 +32,7 @@ struct RowsArgs {
   float* O;                 // [B][m][hq][d] (NULL with V)
   float* lse;               // [B][m][hq] natural log, may be NULL
   float* part;              // partials: numerators, d floats per row
+  float* part_tmp;          // tensor cores: [nc][rt] rows where the streams add up what they have so far
   float2* part_ml;          // and (running max in powers of two, running sum) per row
   float* logits;            // NULL, or [hkv][rows][ld_logits]: the prefix logits in powers of two (-inf where masked), kept
                             // for the weights pass
@@ -49,6 +50,7 @@ struct RowsArgs {
   int extra;                // empty places behind a segment's tiles
   int pp, po;               // row blocks of a prefix / an own segment
   int rp, ro;               // rows of a prefix / an own partial slot
+  int rt;                   // rows of part_tmp per CTA
   int nc;                   // CTAs
   float scale;              // 1 / sqrt(d)
 };
@@ -292,9 +294,9 @@ struct WeightsArgs {
 
 // Host side: the plan of a call (kernel variant, CTAs, partial rows).
 struct RowsPlan {
-  int rb_log, kt_log, extra, nc, pp, po, rp, ro;
+  int rb_log, kt_log, extra, nc, pp, po, rp, ro, rt;
   double places;  // most places the flat list can have
-  uint64_t part_rows, part_own;
+  uint64_t part_rows, part_own, part_tmp;
 };
 void rows_plan(int dtype, int d, int hkv, int group, int64_t B, int64_t m, int64_t n, int64_t ld_own, RowsPlan* p);
 uint64_t rows_part_bound(int dtype, int d, int hkv, int group, int64_t B, int64_t m, int64_t n, int64_t ld_own);

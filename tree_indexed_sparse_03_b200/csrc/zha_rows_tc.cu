@@ -19,6 +19,12 @@
 // The maximum is lazy: O is rescaled in tensor memory only when a row's maximum has grown by more than 2^8, so
 // weights stay below 2^8 and the usual tile rescales nothing.
 //
+// The tensor pipe's fp32 accumulation cuts off instead of rounding, so the error of O grows with the number of products added
+// to it, 2.1e-8 of O each (measured: 3.7e-5 after 1,760, one stream's share of 256K tokens behind 64 sequences).  After
+// kFlushTiles tiles (16 products each) O is therefore added to a place of the stream's own in global memory (L2) with rounded
+// additions and starts again.  A warpgroup of its own does that under the next tile's exponentials, the streams half a
+// period apart.  MEASUREDTEXT
+//
 // Roles: warps 0-3 and 4-7 the two streams' rows, warp 8 the TMA loads into a ring of K / V
 // tiles, warps 9 and 10 issue the two streams' products (a product's operands are five registers that one thread has to
 // provide: one warp for both streams took 100 cycles a product, above the 64 it runs).
@@ -36,8 +42,10 @@
 namespace zha {
 
 constexpr int kTcKeys = 128;               // keys per tile
-constexpr int kTcThreads = 384;
+constexpr int kTcThreads = 512;
+constexpr int kRowRegs = 168, kFewRegs = 88;  // registers a thread: 256 * 168 + 256 * 88 = 512 * 128, the launch's own
 constexpr int kTcRows = 256;               // rows of a row block: two streams of 128
+constexpr int kFlushTiles = 16;              // tiles of a stream that O adds up
 constexpr int kTurnTiles = 4;              // segments of more tiles: the streams take turns
 constexpr float kLazyMax = 8.f;            // growth of the maximum (log2) that rescales O
 
@@ -77,6 +85,29 @@ __device__ __forceinline__ void keep_logits(const RowsArgs& a, float* lg, const 
       __stcg(reinterpret_cast<float4*>(lg + c0 + q), make_float4(v[q] * c2, v[q + 1] * c2, v[q + 2] * c2, v[q + 3] * c2));
 }
 
+__device__ __forceinline__ void st_shared4(uint32_t at, const float* v) {
+  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]) : "memory");
+}
+__device__ __forceinline__ void ld_shared4(uint32_t at, float* v) {
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void red_add4(float* p, const float* v) {
+  asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]) : "memory");
+}
+__device__ __forceinline__ void add_row32(float* v, const float* p) {
+#pragma unroll
+  for (int q = 0; q < 32; q += 4) {
+    const float4 t = __ldcg(reinterpret_cast<const float4*>(p + q));
+    v[q] += t.x;
+    v[q + 1] += t.y;
+    v[q + 2] += t.z;
+    v[q + 3] += t.w;
+  }
+}
+
 // One share of a segment as every role sees it.
 struct TcWork {
   RowsSeg s;
@@ -106,7 +137,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
   using Sh = TcShape<D>;
   constexpr int NS = Sh::kSlots, PANELS = D / 64, PANEL = kTcKeys * 128;  // bytes of a 64-wide panel of a tile
   extern __shared__ uint8_t raw[];
-  __shared__ __align__(8) uint64_t bars[2 * NS + 19];
+  __shared__ __align__(8) uint64_t bars[2 * NS + 25];
   __shared__ float2 x_ml[128];  // stream 1's sums for the join
   __shared__ uint32_t tmem_base;
   __shared__ volatile int gave_up;
@@ -121,6 +152,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
   auto q_full = [&](int s) { return b0 + 8 * (2 * NS + 4 + s); };
   auto p_full = [&](int s, int half) { return b0 + 8 * (2 * NS + 6 + 2 * s + half); };
   const uint32_t fix = b0 + 8 * (2 * NS + 10), done = fix + 8, x_full = fix + 16, x_free = fix + 24, x_may = fix + 32;
+  auto o_chunk = [&](int s) { return b0 + 8 * (2 * NS + 19 + s); };     // O is complete up to a point where it starts again
+  auto o_free = [&](int s) { return b0 + 8 * (2 * NS + 21 + s); };      // and has been read
+  auto flush_done = [&](int s) { return b0 + 8 * (2 * NS + 23 + s); };  // and added to global memory
   auto turn = [&](int s) { return fix + 40 + 8 * s; };  // the other stream has weighed its tile
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
 
@@ -135,6 +169,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
         bar_init(s_full(s, 1), 1);
         bar_init(o_full(s), 1);
         bar_init(q_full(s), 4);
+        bar_init(o_chunk(s), 1);
+        bar_init(o_free(s), 4);
+        bar_init(flush_done(s), 4);
         bar_init(p_full(s, 0), 4);
         bar_init(p_full(s, 1), 4);
       }
@@ -162,6 +199,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
   tc_fence_after();
   const uint32_t tm = tmem_base;
 
+  if (wid >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
   if (wid == 8) {  // ---------------------------------------------------------------- loads
     int slot = 0;
     uint32_t round = 0, fix_phase = 0;
@@ -238,7 +277,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
     const uint32_t q_lo = desc_low(base + st * Sh::kQ, 16);
     const uint32_t k_lo = desc_low(ring, 16), v_lo = desc_low(ring, PANEL);
     int slot = 0;
-    uint32_t round = 0, p_phase = 0, q_phase = 0, b_round = 0;
+    uint32_t round = 0, p_phase = 0, q_phase = 0, b_round = 0, o_phase = 0;
     int buf = 0;
     bool ok = true;
     while (ok && next_work(a, tot, &x, x_end, &w)) {
@@ -246,13 +285,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
       if (!(ok = bar_wait(q_full(st), q_phase, &gave_up))) break;
       q_phase ^= 1;
       if (!w.both && w.cnt == 1 && st == 1 && lane == 0) bar_arrive(o_full(1));  // no tile for stream 1: nothing to wait for
-      bool fresh = true;  // the stream's first tile of the segment
+      int room = kFlushTiles - st * (kFlushTiles / 2);  // tiles until O starts again
+      bool fresh = true, first = true;
 #pragma unroll 1
       for (int i = 0; i < w.cnt + lag && ok; ++i) {
         const bool mine = w.both || (i & 1) == st;
         if (i >= lag && PV) {
           if (!(ok = bar_wait(full(slot), round & 1, &gave_up))) break;
           if (mine) {
+            if (fresh && !first && !(ok = bar_wait(o_free(st), o_phase, &gave_up))) break;
+            if (fresh && !first) o_phase ^= 1;
+            first = false;
             // the weights come in two halves of 64 keys: the products of the first run under the exponentials of the second
             const uint32_t v = v_lo + slot * (Sh::kTile >> 4);
 #pragma unroll
@@ -271,8 +314,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
             }
             if (!ok) break;
             p_phase ^= 1;
-            fresh = false;
+            fresh = --room == 0;
+            if (fresh) room = kFlushTiles;
             if (lane == 0) {
+              if (fresh && i + (w.both ? 1 : 2) < w.cnt + lag) mma_commit(o_chunk(st));
               mma_commit(empty(slot));
               if (i + lag >= w.cnt + lag) mma_commit(o_full(st));
             }
@@ -322,21 +367,68 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
     bar_wait(done, 0, &never);
   } else if (wid == 11) {
     if (blockIdx.x == 0) rows_publish(a, tot);
+  } else if (PV) {  // ---------------------------------------------------------------- O to global memory
+    const int row = tid & 127, wrow = (wid & 3) * 32;
+    uint32_t phase[2] = {0, 0};
+    bool ok = true;
+    while (ok && next_work(a, tot, &x, x_end, &w)) {
+      // the streams' flushes in the order of their tiles: stream 1 after kFlushTiles / 2, stream 0 after kFlushTiles, ...
+      const int n0 = w.both ? w.cnt : (w.cnt + 1) / 2, n1 = w.both ? w.cnt : w.cnt / 2;
+#pragma unroll 1
+      for (int f = 0; f * (kFlushTiles / 2) + kFlushTiles / 2 < max(n0, n1) && ok; ++f) {
+        const int st = (f & 1) ^ 1;
+        if ((f + 1) * (kFlushTiles / 2) >= (st ? n1 : n0)) continue;  // the stream ends before
+        if (!(ok = bar_wait(o_chunk(st), phase[st], &gave_up))) break;
+        phase[st] ^= 1;
+        tc_fence_after();
+        const int nrows = min(128, w.seg_rows - w.s.p * kTcRows - (w.both ? st * 128 : 0));
+        const uint32_t to = tm + (uint32_t(wrow) << 16) + 256 + st * D;
+        float* dst = a.part_tmp + (int64_t(blockIdx.x) * a.rt + st * (a.rt / 2) + row) * D;
+        const bool first = f < 2;
+        if (wrow < nrows) {
+#pragma unroll 1
+          for (int j = 0; j < D; j += 32) {
+            float v[32];
+            tmem_ld32(to + j, v);
+            tmem_wait32(v);
+            if (j + 32 == D) {  // the last of O is in registers
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) bar_arrive(o_free(st));
+            }
+            if (row < nrows) {
+#pragma unroll
+              for (int q = 0; q < 32; q += 4) {
+                if (first) __stcg(reinterpret_cast<float4*>(dst + j + q), make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]));
+                else red_add4(dst + j + q, v + q);
+              }
+            }
+          }
+          __threadfence();
+          __syncwarp();
+        } else if (lane == 0) {
+          bar_arrive(o_free(st));
+        }
+        if (lane == 0) bar_arrive(flush_done(st));
+      }
+    }
+  }
   } else {  // ---------------------------------------------------------------- the streams' rows
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowRegs));
     const int st = wid >> 2, row = tid & 127, wrow = (wid & 3) * 32;
     const uint32_t lane_base = uint32_t(wrow) << 16;
     const uint32_t ts = tm + lane_base + st * 128, to = tm + lane_base + 256 + st * D;
     const float c2 = a.scale * 1.4426950408889634f;  // weights as powers of two
     const uint64_t cc = pair(c2, c2), minus = pair(-1.f, -1.f);
-    uint32_t s_phase = 0, o_phase = 0, x_phase = 0, t_phase = 0;
+    uint32_t s_phase = 0, o_phase = 0, x_phase = 0, t_phase = 0, f_phase = 0;
     int buf = 0;
     bool ok = true;
     while (ok && next_work(a, tot, &x, x_end, &w)) {
       const int r0 = w.s.p * kTcRows + (w.both ? st * 128 : 0);  // the stream's first row
       const int nrows = min(128, w.seg_rows - r0);
       const int row_off = w.s.own ? w.s.b * a.m * a.group : 0;
-      {
-        // every warp its own rows: they are where its last results left from, and no other warp waits for that
+      // queries to shared memory, every warp its own rows: they are where its results leave from, and no other warp waits for that
+      auto load_queries = [&]() {
         constexpr int CH = D / 8, RP = 32 / CH;  // 16-byte pieces of a row, rows per pass of a warp
         const int c = lane % CH, rq = wrow + lane / CH;
         const __nv_bfloat16* Qp = static_cast<const __nv_bfloat16*>(a.Q) + c * 8;
@@ -358,7 +450,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
                          : "memory");
           }
         }
-      }
+      };
+      load_queries();
       fence_async_smem();
       __syncwarp();
       if (lane == 0) bar_arrive(q_full(st));
@@ -366,12 +459,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
       const int lim = row >= nrows ? INT_MAX : int(w.s.own ? own_limit(a, own_tokens(a, w.s.b), r0 + row) : prefix_limit(a, r0 + row));
       const bool active = wrow < nrows;  // a warp of padding rows leaves its weights alone: they reach no valid row
       float m_ref = -INFINITY, l_run = 0.f;
+      bool flushed = false, pending = false;  // O has been added to global memory; maybe not done yet
+      // where the rows' results go: a partial, or the result itself where this CTA's share holds all tiles
+      const bool whole = !a.has_own && w.t0 == 0 && w.cnt == w.s.tiles;
+      const int64_t pr = part_row(a, blockIdx.x, w.s.own, w.s.id, x_begin < w.s.first) + (w.both ? st * 128 : 0) + row;
+      const int64_t ri = row < nrows ? row_index(a, w.s.h, row_off + r0 + row) : 0;
+      // and where O is added up meanwhile
+      float* sofar = a.part_tmp + (int64_t(blockIdx.x) * a.rt + st * (a.rt / 2) + row) * D;
+      constexpr int HC = D / 2, LN = HC / 4;  // columns of half a row, lanes for one
+      // 16-byte piece k of the half row from column c0 on, of row r: over both streams' queries, or over the stream's own
+      auto cell = [&](bool all, int c0, int k, int r) {
+        return all ? base + r * (D * 4) + c0 * 4 + ((k ^ (r & 7)) << 4)
+                   : base + st * Sh::kQ + (k >> 3) * (128 * 128) + r * 128 + (((k & 7) ^ (r & 7)) << 4);
+      };
       const int step = w.both ? 1 : 2, i0 = w.both ? 0 : st;
       if constexpr (PV) {
       // Streams take turns: a tile may begin once the other stream has handed over half of its own.  Left alone they fall into
       // step, and the tensor pipe idles while both weigh (256K tokens behind 64 sequences: 413 us, whole turns 400, half
       // turns 380).
       const bool turns = w.cnt > kTurnTiles;
+      int room = kFlushTiles - st * (kFlushTiles / 2);  // tiles until O starts again
+      bool fresh = true, first_tile = true;
 #pragma unroll 1
       for (int i = i0; i < w.cnt; i += step) {
         if (turns && (st || i != i0)) {
@@ -381,6 +489,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
         if (!(ok = bar_wait(s_full(st), s_phase, &gave_up))) break;
         s_phase ^= 1;
         tc_fence_after();
+        if (fresh && !first_tile) pending = flushed = true;  // O is being added to global memory
+        // before this tile's weights can complete O and have it added again, every warp has seen the time before
+        if (pending && room == 1) {
+          if (!(ok = bar_wait(flush_done(st), f_phase, &gave_up))) break;
+          f_phase ^= 1;
+          pending = false;
+        }
         if (active) {
           const int left = lim - (w.t0 + i) * kTcKeys;  // keys of the tile that the row sees
           const bool mask = __any_sync(0xffffffffu, left < kTcKeys);
@@ -410,7 +525,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
           if (__any_sync(0xffffffffu, grow)) {
             const float up = grow ? m_new : m_ref;
             const float sc = m_ref == -INFINITY ? 0.f : ex2(m_ref - up);
-            if (i != i0) {
+            if (flushed) {  // what has left O already
+              if (pending) {
+                if (!(ok = bar_wait(flush_done(st), f_phase, &gave_up))) break;
+                f_phase ^= 1;
+                pending = false;
+              }
+              if (grow) {
+#pragma unroll 1
+                for (int j = 0; j < D; j += 4) {
+                  float4 t = __ldcg(reinterpret_cast<const float4*>(sofar + j));
+                  t = m_ref == -INFINITY ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(t.x * sc, t.y * sc, t.z * sc, t.w * sc);
+                  __stcg(reinterpret_cast<float4*>(sofar + j), t);
+                }
+                __threadfence();
+              }
+              __syncwarp();
+            }
+            if (!fresh) {
 #pragma unroll 1
               for (int j = 0; j < D; j += 32) {
                 tmem_ld32(to + j, vb);
@@ -480,6 +612,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
             if (turns) bar_arrive(turn(st ^ 1));
           }
         }
+        first_tile = false;
+        fresh = --room == 0;
+        if (fresh) room = kFlushTiles;
       }
       // turns of the other stream that this one has no tile to wait for: the last one of stream 1, for stream 0 and of
       // stream 0 for a stream 1 with one tile less
@@ -548,7 +683,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
       }
       // streams that shared the rows: stream 1 leaves its sums and rows where the queries lay, stream 0 joins them
       const bool join = !w.both && w.cnt > 1;
-      const uint32_t xrow = base + row * (D * 4);  // the row's place, 16-byte pieces swizzled by the row
+      if (pending) {
+        if (!(ok = bar_wait(flush_done(st), f_phase, &gave_up))) break;
+        f_phase ^= 1;
+      }
+      flushed = flushed && row < nrows;
       float other_l = 0.f, mine_s = 1.f, other_s = 0.f;
       if (join) {
         if (st == 1) {
@@ -560,11 +699,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
                 float v[32];
                 tmem_ld32(to + j, v);
                 tmem_wait32(v);
+                if (flushed) add_row32(v, sofar + j);
 #pragma unroll
                 for (int q = 0; q < 8; ++q)
-                  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(xrow + ((((j >> 2) + q) ^ (row & 7)) << 4)),
-                               "f"(v[4 * q]), "f"(v[4 * q + 1]), "f"(v[4 * q + 2]), "f"(v[4 * q + 3])
-                               : "memory");
+                  st_shared4(cell(true, j & ~(HC - 1), ((j & (HC - 1)) >> 2) + q, row), v + 4 * q);
               }
             }
             x_ml[row] = make_float2(m_ref, l_run);
@@ -587,11 +725,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
           }
         }
       }
-      // the segment's share of this CTA: a partial, or the result where the share holds all its tiles
       if (active && (w.both || st == 0)) {
-        const bool whole = !a.has_own && w.t0 == 0 && w.cnt == w.s.tiles;
-        const int64_t pr = part_row(a, blockIdx.x, w.s.own, w.s.id, x_begin < w.s.first) + (w.both ? st * 128 : 0) + row;
-        const int64_t ri = row < nrows ? row_index(a, w.s.h, row_off + r0 + row) : 0;
         float inv = mine_s;
         if (row < nrows) {
           if (whole) {
@@ -607,12 +741,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
           // through shared memory, half a row at a time, so that it leaves in whole runs (one thread's row
           // straight from its registers took 4 us a segment): over the other stream's rows when joining, else over the
           // stream's own queries, which no product reads any more
-          constexpr int HC = D / 2, LN = HC / 4;  // columns of a half, lanes for one
-          // 16-byte piece k of the half from column c0 on, of row r
-          auto cell = [&](int c0, int k, int r) {
-            return join ? base + r * (D * 4) + c0 * 4 + ((k ^ (r & 7)) << 4)
-                        : base + st * Sh::kQ + (k >> 3) * (128 * 128) + r * 128 + (((k & 7) ^ (r & 7)) << 4);
-          };
 #pragma unroll 1
           for (int c0 = 0; c0 < D; c0 += HC) {
 #pragma unroll 1
@@ -620,22 +748,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
               float v[32];
               tmem_ld32(to + c0 + j, v);
               tmem_wait32(v);
+              if (flushed) add_row32(v, sofar + c0 + j);
 #pragma unroll
               for (int q = 0; q < 8; ++q) {
-                const uint32_t at = cell(c0, (j >> 2) + q, row);
-                float4 o = make_float4(v[4 * q] * inv, v[4 * q + 1] * inv, v[4 * q + 2] * inv, v[4 * q + 3] * inv);
+                const uint32_t at = cell(join, c0, (j >> 2) + q, row);
+                float o[4] = {v[4 * q] * inv, v[4 * q + 1] * inv, v[4 * q + 2] * inv, v[4 * q + 3] * inv};
                 if (join && other_s != 0.f) {
-                  float4 t;
-                  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                               : "=f"(t.x), "=f"(t.y), "=f"(t.z), "=f"(t.w)
-                               : "r"(at));
-                  o.x = fmaf(t.x, other_s, o.x);
-                  o.y = fmaf(t.y, other_s, o.y);
-                  o.z = fmaf(t.z, other_s, o.z);
-                  o.w = fmaf(t.w, other_s, o.w);
+                  float t[4];
+                  ld_shared4(at, t);
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) o[e] = fmaf(t[e], other_s, o[e]);
                 }
-                asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(o.x), "f"(o.y), "f"(o.z), "f"(o.w)
-                             : "memory");
+                st_shared4(at, o);
               }
             }
             __syncwarp();
@@ -643,10 +767,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
 #pragma unroll 4
             for (int r = lane / LN; r < min(32, nrows - wrow); r += 32 / LN) {
               const int rr = wrow + r;
-              float4 o;
-              asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                           : "=f"(o.x), "=f"(o.y), "=f"(o.z), "=f"(o.w)
-                           : "r"(cell(c0, ln, rr)));
+              float t[4];
+              ld_shared4(cell(join, c0, ln, rr), t);
+              const float4 o = make_float4(t[0], t[1], t[2], t[3]);
               float* dst = whole ? a.O + row_index(a, w.s.h, row_off + r0 + rr) * D : a.part + (pr - row + rr) * D;
               *reinterpret_cast<float4*>(dst + c0 + ln * 4) = o;
             }
@@ -744,6 +867,7 @@ void tc_plan(int64_t rows, int64_t mg, int64_t ld_own, RowsPlan* p) {
   p->po = ld_own > 0 ? int((mg + kTcRows - 1) / kTcRows) : 0;
   p->rp = int(min64(rows, kTcRows));
   p->ro = int(min64(mg, kTcRows));
+  p->rt = 2 * int((min64(rows, 128) + 31) / 32 * 32);  // both streams, whole warps
 }
 
 }  // namespace zha
