@@ -22,8 +22,8 @@
 // The tensor pipe's fp32 accumulation cuts off instead of rounding, so the error of O grows with the number of products added
 // to it, 2.1e-8 of O each (measured: 3.7e-5 after 1,760, one stream's share of 256K tokens behind 64 sequences).  After
 // kFlushTiles tiles (16 products each) O is therefore added to a place of the stream's own in global memory (L2) with rounded
-// additions and starts again.  A warpgroup of its own does that under the next tile's exponentials, the streams half a
-// period apart.  MEASUREDTEXT
+// additions and starts again (5.4e-6 on the same case).  A warpgroup of its own does that under the next tile's
+// exponentials, through shared memory by bulk reductions, the streams half a period apart.
 //
 // Roles: warps 0-3 and 4-7 the two streams' rows, warp 8 the TMA loads into a ring of K / V
 // tiles, warps 9 and 10 issue the two streams' products (a product's operands are five registers that one thread has to
@@ -52,8 +52,9 @@ constexpr float kLazyMax = 8.f;            // growth of the maximum (log2) that 
 template <int D> struct TcShape {
   static constexpr int kTile = kTcKeys * D * 2;            // bytes of a K or V tile
   static constexpr int kQ = 128 * D * 2;                   // bytes of a stream's Q tile
-  static constexpr int kSlots = D == 128 ? 5 : 10;         // ring slots
-  static constexpr int kSmem = 2 * kQ + kSlots * kTile + 1024;  // + alignment
+  static constexpr int kSlots = D == 128 ? 4 : 10;         // ring slots (d = 128: five were no faster)
+  static constexpr int kStage = 128 * 64 * 4;              // 64 columns of O on their way to global memory
+  static constexpr int kSmem = 2 * kQ + kSlots * kTile + kStage + 1024;  // + alignment
 };
 
 struct TcMaps {
@@ -94,18 +95,19 @@ __device__ __forceinline__ void ld_shared4(uint32_t at, float* v) {
                : "r"(at)
                : "memory");
 }
-__device__ __forceinline__ void red_add4(float* p, const float* v) {
-  asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]) : "memory");
-}
-__device__ __forceinline__ void add_row32(float* v, const float* p) {
+template <typename F> __device__ __forceinline__ void add_row32(float* v, F at) {
 #pragma unroll
   for (int q = 0; q < 32; q += 4) {
-    const float4 t = __ldcg(reinterpret_cast<const float4*>(p + q));
+    const float4 t = __ldcg(reinterpret_cast<const float4*>(at(q)));
     v[q] += t.x;
     v[q + 1] += t.y;
     v[q + 2] += t.z;
     v[q + 3] += t.w;
   }
+}
+// Where the 32 rows from wrow on of stream st add up what they have so far.
+__device__ __forceinline__ float* sofar_base(const RowsArgs& a, int st, int wrow, int d) {
+  return a.part_tmp + (int64_t(blockIdx.x) * a.rt + st * (a.rt / 2) + wrow) * d;
 }
 
 // One share of a segment as every role sees it.
@@ -368,7 +370,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
   } else if (wid == 11) {
     if (blockIdx.x == 0) rows_publish(a, tot);
   } else if (PV) {  // ---------------------------------------------------------------- O to global memory
-    const int row = tid & 127, wrow = (wid & 3) * 32;
+    const int wrow = (wid & 3) * 32;
+    const uint32_t stage = ring + NS * Sh::kTile + wrow * 256;
     uint32_t phase[2] = {0, 0};
     bool ok = true;
     while (ok && next_work(a, tot, &x, x_end, &w)) {
@@ -383,29 +386,35 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
         tc_fence_after();
         const int nrows = min(128, w.seg_rows - w.s.p * kTcRows - (w.both ? st * 128 : 0));
         const uint32_t to = tm + (uint32_t(wrow) << 16) + 256 + st * D;
-        float* dst = a.part_tmp + (int64_t(blockIdx.x) * a.rt + st * (a.rt / 2) + row) * D;
-        const bool first = f < 2;
+        float* dst = sofar_base(a, st, wrow, D);
         if (wrow < nrows) {
 #pragma unroll 1
-          for (int j = 0; j < D; j += 32) {
-            float v[32];
-            tmem_ld32(to + j, v);
-            tmem_wait32(v);
-            if (j + 32 == D) {  // the last of O is in registers
+          for (int c0 = 0; c0 < D; c0 += 64) {
+#pragma unroll 1
+            for (int j = 0; j < 64; j += 32) {
+              float v[32];
+              tmem_ld32(to + c0 + j, v);
+              tmem_wait32(v);
+#pragma unroll
+              for (int q = 0; q < 8; ++q) st_shared4(stage + lane * 256 + ((((j >> 2) + q) ^ (lane & 7)) << 4), v + 4 * q);
+            }
+            if (c0 + 64 == D) {  // all of O has been read
               tc_fence_before();
               __syncwarp();
               if (lane == 0) bar_arrive(o_free(st));
             }
-            if (row < nrows) {
-#pragma unroll
-              for (int q = 0; q < 32; q += 4) {
-                if (first) __stcg(reinterpret_cast<float4*>(dst + j + q), make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]));
-                else red_add4(dst + j + q, v + q);
-              }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (f < 2) bulk_store(dst + c0 * 32, stage, 32 * 256);
+              else bulk_add(dst + c0 * 32, stage, 32 * 256);
+              bulk_commit();
+              if (c0 + 64 == D) bulk_wait_all();  // before the next addition to the same place, and before anyone reads it
+              else bulk_wait_read();
             }
+            __syncwarp();
           }
-          __threadfence();
-          __syncwarp();
+          asm volatile("fence.proxy.async;" ::: "memory");
         } else if (lane == 0) {
           bar_arrive(o_free(st));
         }
@@ -464,8 +473,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
       const bool whole = !a.has_own && w.t0 == 0 && w.cnt == w.s.tiles;
       const int64_t pr = part_row(a, blockIdx.x, w.s.own, w.s.id, x_begin < w.s.first) + (w.both ? st * 128 : 0) + row;
       const int64_t ri = row < nrows ? row_index(a, w.s.h, row_off + r0 + row) : 0;
-      // and where O is added up meanwhile
-      float* sofar = a.part_tmp + (int64_t(blockIdx.x) * a.rt + st * (a.rt / 2) + row) * D;
+      // and where O is added up meanwhile, in the order it leaves shared memory: 64 columns, rows, swizzled 16-byte pieces
+      float* const sofar = sofar_base(a, st, wrow, D);
+      auto sofar_at = [&](int col) {
+        return sofar + (col >> 6) * (32 * 64) + lane * 64 + ((((col & 63) >> 2) ^ (lane & 7)) << 2);
+      };
       constexpr int HC = D / 2, LN = HC / 4;  // columns of half a row, lanes for one
       // 16-byte piece k of the half row from column c0 on, of row r: over both streams' queries, or over the stream's own
       auto cell = [&](bool all, int c0, int k, int r) {
@@ -534,11 +546,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
               if (grow) {
 #pragma unroll 1
                 for (int j = 0; j < D; j += 4) {
-                  float4 t = __ldcg(reinterpret_cast<const float4*>(sofar + j));
+                  float4 t = __ldcg(reinterpret_cast<const float4*>(sofar_at(j)));
                   t = m_ref == -INFINITY ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(t.x * sc, t.y * sc, t.z * sc, t.w * sc);
-                  __stcg(reinterpret_cast<float4*>(sofar + j), t);
+                  __stcg(reinterpret_cast<float4*>(sofar_at(j)), t);
                 }
                 __threadfence();
+                asm volatile("fence.proxy.async;" ::: "memory");
               }
               __syncwarp();
             }
@@ -699,7 +712,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
                 float v[32];
                 tmem_ld32(to + j, v);
                 tmem_wait32(v);
-                if (flushed) add_row32(v, sofar + j);
+                if (flushed) add_row32(v, [&](int c) { return sofar_at(j + c); });
 #pragma unroll
                 for (int q = 0; q < 8; ++q)
                   st_shared4(cell(true, j & ~(HC - 1), ((j & (HC - 1)) >> 2) + q, row), v + 4 * q);
@@ -748,7 +761,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
               float v[32];
               tmem_ld32(to + c0 + j, v);
               tmem_wait32(v);
-              if (flushed) add_row32(v, sofar + c0 + j);
+              if (flushed) add_row32(v, [&](int c) { return sofar_at(c0 + j + c); });
 #pragma unroll
               for (int q = 0; q < 8; ++q) {
                 const uint32_t at = cell(join, c0, (j >> 2) + q, row);
