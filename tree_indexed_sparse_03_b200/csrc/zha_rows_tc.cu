@@ -16,8 +16,8 @@
 // tile is loaded once for 256 rows); a smaller one gives both streams the same rows and every other tile,
 // and stream 0 joins the two results.
 //
-// The maximum is lazy: O is rescaled in tensor memory only when a row's maximum has grown by more than 2^8, so
-// weights stay below 2^8 and the usual tile rescales nothing.
+// The maximum is lazy: O is rescaled only when a row's maximum has grown by more than 2^20, so weights stay below
+// 2^20 (the sums are floating point: nothing is lost) and the usual tile rescales nothing.
 //
 // The tensor pipe's fp32 accumulation cuts off instead of rounding, so the error of O grows with the number of products added
 // to it, 2.1e-8 of O each (measured: 3.7e-5 after 1,760, one stream's share of 256K tokens behind 64 sequences).  After
@@ -47,7 +47,7 @@ constexpr int kRowRegs = 168, kFewRegs = 88;  // registers a thread: 256 * 168 +
 constexpr int kTcRows = 256;               // rows of a row block: two streams of 128
 constexpr int kFlushTiles = 16;              // tiles of a stream that O adds up
 constexpr int kTurnTiles = 4;              // segments of more tiles: the streams take turns
-constexpr float kLazyMax = 8.f;            // growth of the maximum (log2) that rescales O
+constexpr float kLazyMax = 20.f;           // growth of the maximum (log2) that rescales O
 
 template <int D> struct TcShape {
   static constexpr int kTile = kTcKeys * D * 2;            // bytes of a K or V tile
@@ -545,10 +545,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
               }
               if (grow) {
 #pragma unroll 1
-                for (int j = 0; j < D; j += 4) {
-                  float4 t = __ldcg(reinterpret_cast<const float4*>(sofar_at(j)));
-                  t = m_ref == -INFINITY ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(t.x * sc, t.y * sc, t.z * sc, t.w * sc);
-                  __stcg(reinterpret_cast<float4*>(sofar_at(j)), t);
+                for (int j = 0; j < D; j += 32) {  // eight pieces on their way
+#pragma unroll
+                  for (int q = 0; q < 32; q += 4)
+                    *reinterpret_cast<float4*>(vb + q) = __ldcg(reinterpret_cast<const float4*>(sofar_at(j + q)));
+#pragma unroll
+                  for (int q = 0; q < 32; q += 4) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) vb[q + e] = m_ref == -INFINITY ? 0.f : vb[q + e] * sc;
+                    __stcg(reinterpret_cast<float4*>(sofar_at(j + q)), make_float4(vb[q], vb[q + 1], vb[q + 2], vb[q + 3]));
+                  }
                 }
                 __threadfence();
                 asm volatile("fence.proxy.async;" ::: "memory");
@@ -700,6 +706,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
         if (!(ok = bar_wait(flush_done(st), f_phase, &gave_up))) break;
         f_phase ^= 1;
       }
+      const bool added = flushed;
       flushed = flushed && row < nrows;
       float other_l = 0.f, mine_s = 1.f, other_s = 0.f;
       if (join) {
@@ -761,7 +768,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
               float v[32];
               tmem_ld32(to + c0 + j, v);
               tmem_wait32(v);
-              if (flushed) add_row32(v, [&](int c) { return sofar_at(c0 + j + c); });
 #pragma unroll
               for (int q = 0; q < 8; ++q) {
                 const uint32_t at = cell(join, c0, (j >> 2) + q, row);
@@ -777,14 +783,30 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
             }
             __syncwarp();
             const int ln = lane % LN;
-#pragma unroll 4
-            for (int r = lane / LN; r < min(32, nrows - wrow); r += 32 / LN) {
-              const int rr = wrow + r;
-              float t[4];
-              ld_shared4(cell(join, c0, ln, rr), t);
-              const float4 o = make_float4(t[0], t[1], t[2], t[3]);
-              float* dst = whole ? a.O + row_index(a, w.s.h, row_off + r0 + rr) * D : a.part + (pr - row + rr) * D;
-              *reinterpret_cast<float4*>(dst + c0 + ln * 4) = o;
+            constexpr int RS = 32 / LN, BATCH = 8;  // rows at a time, and of these on their way
+#pragma unroll 1
+            for (int rb = lane / LN; rb - lane / LN < min(32, nrows - wrow); rb += BATCH * RS) {
+              float4 t[BATCH];
+#pragma unroll
+              for (int u = 0; u < BATCH; ++u) {
+                const int r = rb + u * RS;
+                t[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (added && wrow + r < nrows)  // what left O before
+                  t[u] = __ldcg(reinterpret_cast<const float4*>(sofar + (c0 >> 6) * (32 * 64) + r * 64 +
+                                                                (((((c0 & 63) >> 2) + ln) ^ (r & 7)) << 2)));
+              }
+#pragma unroll
+              for (int u = 0; u < BATCH; ++u) {
+                const int r = rb + u * RS, rr = wrow + r;
+                const float f = __shfl_sync(0xffffffffu, inv, r);
+                if (rr < nrows) {
+                  float o[4];
+                  ld_shared4(cell(join, c0, ln, rr), o);
+                  float* dst = whole ? a.O + row_index(a, w.s.h, row_off + r0 + rr) * D : a.part + (pr - row + rr) * D;
+                  *reinterpret_cast<float4*>(dst + c0 + ln * 4) =
+                      make_float4(fmaf(t[u].x, f, o[0]), fmaf(t[u].y, f, o[1]), fmaf(t[u].z, f, o[2]), fmaf(t[u].w, f, o[3]));
+                }
+              }
             }
             __syncwarp();
           }
@@ -875,7 +897,10 @@ cudaError_t launch_rows_tc(const RowsArgs& a, int d, cudaStream_t st) {
 void tc_plan(int64_t rows, int64_t mg, int64_t ld_own, RowsPlan* p) {
   p->rb_log = 8;
   p->kt_log = 7;
-  p->extra = 2;  // queries, first loads and the write-out of a segment take about as long as two tiles
+  // queries, first loads and the write-out of a segment take about as long as four tiles of one stream's rows each, three of
+  // both (32K behind 16 sequences: 2 places 44 us, 4 places 39, 8 places 40; a 4,099-token prompt: 2 places 126, 3 places 120,
+  // 4 places 122)
+  p->extra = rows > 128 ? 3 : 4;
   p->pp = int((rows + kTcRows - 1) / kTcRows);
   p->po = ld_own > 0 ? int((mg + kTcRows - 1) / kTcRows) : 0;
   p->rp = int(min64(rows, kTcRows));
