@@ -214,7 +214,8 @@ def test_prefix_slices_streams_and_graphs():
     dec2.status()
 
 
-@pytest.mark.parametrize("B,m,own,rising", [(1, 1, 0, False), (1, 1, 0, True), (40, 8, 60, False), (40, 8, 60, True)])
+@pytest.mark.parametrize("B,m,own,rising", [(1, 1, 0, False), (1, 1, 0, True), (40, 8, 60, False), (40, 8, 60, True),
+                                              (2, 1, 600001, True)])
 def test_prefix_long(B, m, own, rising):
     """Shares of many tiles: the accumulator is added up outside tensor memory several times, also while the running maximum
     moves (rising: keys grow along the cache by a factor of 16, each longer key ahead of all before it)."""
@@ -224,7 +225,7 @@ def test_prefix_long(B, m, own, rising):
     if rising:
         K = (K * (0.25 + 3.75 * torch.arange(n, device="cuda")[:, None] / n)).to(torch.bfloat16)
     Ko, Vo = (rnd(4, B, hkv, own, d).cuda(), rnd(5, B, hkv, own, d).cuda()) if own else (None, None)
-    ln = torch.tensor([(b * 7) % (own + 1) for b in range(B)], dtype=torch.int32, device="cuda") if own else None
+    ln = torch.tensor([own - (b * 7) % (own + 1) for b in range(B)], dtype=torch.int32, device="cuda") if own else None
     dec = z.PrefixDecoder(cfg_of("bf16", d, hkv, 4, capacity=n), B, n, own, m)
     o, lse = dec(K, V, n, Q, Ko, Vo, ln, want_lse=True)
     torch.cuda.synchronize()
@@ -360,6 +361,30 @@ def test_weights_many_short_segments(dtype, d, hkv, group, m, n):
         close(o, want_o, REL * float(V.abs().max()) + 1e-6, "O")
         close(a, want_a, REL * want_a + 1e-6, "acc")
     dec.status()
+
+
+@pytest.mark.parametrize("m", [1, 70])
+def test_weights_long(m):
+    """One step (kept logits) and a window over a long context, against fp64 on the GPU."""
+    n, d, G = 500001, 64, 4
+    K, V = rnd(1, 1, n, d).cuda(), rnd(2, 1, n, d).cuda()
+    Q = rnd(3, m, G, d, scale=2.0).cuda()
+    dec = z.DenseWeights(cfg_of("bf16", d, 1, G, capacity=n), m, n)
+    o, a = dec(K, V, n, Q, causal=True)
+    torch.cuda.synchronize()
+    dec.status()
+    acc = torch.zeros(n, dtype=torch.float64, device="cuda")
+    worst = norm = 0.0
+    for i in range(m):
+        seen = n - m + 1 + i
+        w = torch.softmax(Q[i].double() @ K[0, :seen].double().T / math.sqrt(d), 1)
+        acc[:seen] += w.sum(0)
+        want = w @ V[0, :seen].double()
+        worst += float((o[i].double() - want).square().sum())
+        norm += float(want.square().sum())
+    assert bool(((a[0].double() - acc).abs() <= REL * acc + 1e-6).all())
+    # weights to 1.1e-5 (above), beside them at most 256 cut-off additions of 2^-24 = 1.5e-5
+    assert math.sqrt(worst / norm) <= 2.6e-5
 
 
 def test_weights_graph_and_stream():

@@ -11,7 +11,10 @@
 // two), because the output is fp32: one part alone leaves 2^-9 of every weight, the two 2^-17.  That
 // makes three products per tile instead of two: 3 * 512 cycles at 128 x 128 x 128 against 1024 cycles of exponentials
 // (16 per cycle and SM), so with both streams in flight - one in its exponentials while the other's products
-// run - the tensor pipe is the limit for many rows, HBM for few.
+// run - the tensor pipe is the limit for many rows, HBM for few.  Measured: 64 sequences behind 256K tokens (4 KV heads
+// of 8, d = 128) 411 us in short runs, 1.0e15 tensor operations a second with the third product counted, 480 us in long
+// ones at the power limit; 5,250 cycles per tile of both streams of the 3,072 that its products take.  One sequence
+// (8 rows a head) 105 us for 537 MB of K and V, 5.1 TB/s.
 // A segment of more than 128 rows gives each stream its own rows and both the same tiles (each K and V
 // tile is loaded once for 256 rows); a smaller one gives both streams the same rows and every other tile,
 // and stream 0 joins the two results.
@@ -202,226 +205,226 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
   const uint32_t tm = tmem_base;
 
   if (wid >= 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
-  if (wid == 8) {  // ---------------------------------------------------------------- loads
-    int slot = 0;
-    uint32_t round = 0, fix_phase = 0;
-    bool ok = true;
-    const uint64_t once = l2_evict_first(), many = l2_evict_normal();
-    int pend_slot = -1, pend_row = 0;  // a V tile whose rows from pend_row on are still to be cleared
-    auto clear_pending = [&]() {
-      if (pend_slot < 0) return true;
-      if (!bar_wait(fix, fix_phase, &gave_up)) return false;
-      fix_phase ^= 1;
-      const uint32_t dst = ring + pend_slot * Sh::kTile + pend_row * 128;
-      const int per = (kTcKeys - pend_row) * 8;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+    if (wid == 8) {  // ---------------------------------------------------------------- loads
+      int slot = 0;
+      uint32_t round = 0, fix_phase = 0;
+      bool ok = true;
+      const uint64_t once = l2_evict_first(), many = l2_evict_normal();
+      int pend_slot = -1, pend_row = 0;  // a V tile whose rows from pend_row on are still to be cleared
+      auto clear_pending = [&]() {
+        if (pend_slot < 0) return true;
+        if (!bar_wait(fix, fix_phase, &gave_up)) return false;
+        fix_phase ^= 1;
+        const uint32_t dst = ring + pend_slot * Sh::kTile + pend_row * 128;
+        const int per = (kTcKeys - pend_row) * 8;
 #pragma unroll 1
-      for (int p = 0; p < PANELS; ++p)
+        for (int p = 0; p < PANELS; ++p)
 #pragma unroll 1
-        for (int q = lane; q < per; q += 32)
-          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst + p * PANEL + q * 16), "r"(0) : "memory");
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) bar_arrive(full(pend_slot));
-      pend_slot = -1;
-      return true;
-    };
-    while (ok && next_work(a, tot, &x, x_end, &w)) {
-      const int lag = w.both ? 1 : 2;
-      // tiles that no other row block reads go first when L2 needs room (kept logits stay)
-      const uint64_t policy = w.s.own || a.pp == 1 ? once : many;
-      const CUtensorMap* mk = w.s.own ? &maps.ko : &maps.k;
-      const CUtensorMap* mv = w.s.own ? &maps.vo : &maps.v;
-      const int plane = w.s.own ? w.s.b * a.hkv + w.s.h : w.s.h;
-      const int len = int(w.s.own ? own_tokens(a, w.s.b) : a.n);
+          for (int q = lane; q < per; q += 32)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst + p * PANEL + q * 16), "r"(0) : "memory");
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) bar_arrive(full(pend_slot));
+        pend_slot = -1;
+        return true;
+      };
+      while (ok && next_work(a, tot, &x, x_end, &w)) {
+        const int lag = w.both ? 1 : 2;
+        // tiles that no other row block reads go first when L2 needs room (kept logits stay)
+        const uint64_t policy = w.s.own || a.pp == 1 ? once : many;
+        const CUtensorMap* mk = w.s.own ? &maps.ko : &maps.k;
+        const CUtensorMap* mv = w.s.own ? &maps.vo : &maps.v;
+        const int plane = w.s.own ? w.s.b * a.hkv + w.s.h : w.s.h;
+        const int len = int(w.s.own ? own_tokens(a, w.s.b) : a.n);
 #pragma unroll 1
-      for (int i = 0; i < 2 * (w.cnt + lag) && ok; ++i) {
-        const bool kv = !(i & 1);  // V of tile i/2 - lag, then K of tile i/2: the order of their use
-        const int t = (i >> 1) - (kv ? lag : 0);
-        if (kv ? (!PV || t < 0) : t >= w.cnt) continue;
-        const int k0 = (w.t0 + t) * kTcKeys;
-        // rows of V past a sequence's end hold anything (0 * NaN is NaN): cleared before the product sees them, once the
-        // copy has landed; meanwhile the next copies start, as long as none has to wait.  Past the prefix's end the
-        // tensor map ends, so the copy itself fills zeros.
-        const bool clear = kv && w.s.own && k0 + kTcKeys > len;
-        if ((clear || !bar_done(empty(slot), (round & 1) ^ 1)) && !(ok = clear_pending())) break;
-        if (!(ok = bar_wait(empty(slot), (round & 1) ^ 1, &gave_up))) break;
-        const uint32_t dst = ring + slot * Sh::kTile;
-        const uint32_t bar = clear ? fix : full(slot);
-        if (lane == 0) {
-          bar_expect(bar, Sh::kTile);
+        for (int i = 0; i < 2 * (w.cnt + lag) && ok; ++i) {
+          const bool kv = !(i & 1);  // V of tile i/2 - lag, then K of tile i/2: the order of their use
+          const int t = (i >> 1) - (kv ? lag : 0);
+          if (kv ? (!PV || t < 0) : t >= w.cnt) continue;
+          const int k0 = (w.t0 + t) * kTcKeys;
+          // rows of V past a sequence's end hold anything (0 * NaN is NaN): cleared before the product sees them, once the
+          // copy has landed; meanwhile the next copies start, as long as none has to wait.  Past the prefix's end the
+          // tensor map ends, so the copy itself fills zeros.
+          const bool clear = kv && w.s.own && k0 + kTcKeys > len;
+          if ((clear || !bar_done(empty(slot), (round & 1) ^ 1)) && !(ok = clear_pending())) break;
+          if (!(ok = bar_wait(empty(slot), (round & 1) ^ 1, &gave_up))) break;
+          const uint32_t dst = ring + slot * Sh::kTile;
+          const uint32_t bar = clear ? fix : full(slot);
+          if (lane == 0) {
+            bar_expect(bar, Sh::kTile);
 #pragma unroll
-          for (int p = 0; p < PANELS; ++p) tma_load(dst + p * PANEL, kv ? mv : mk, bar, p * 64, k0, plane, policy);
-        }
-        if (clear) {
-          pend_slot = slot;
-          pend_row = len - k0;
-        }
-        if (++slot == NS) {
-          slot = 0;
-          ++round;
+            for (int p = 0; p < PANELS; ++p) tma_load(dst + p * PANEL, kv ? mv : mk, bar, p * 64, k0, plane, policy);
+          }
+          if (clear) {
+            pend_slot = slot;
+            pend_row = len - k0;
+          }
+          if (++slot == NS) {
+            slot = 0;
+            ++round;
+          }
         }
       }
-    }
-    if (ok) clear_pending();
-    // copies in flight when a wait gave up: let them land before the CTA's shared memory goes away
-    if (gave_up) {
-      int never = 0;
-      for (int q = 0; q < NS; ++q) {
-        const uint32_t r = q < slot ? round : round - 1;  // the slot's last use
-        if (q < slot || round > 0) bar_wait(q == pend_slot ? fix : full(q), q == pend_slot ? fix_phase : r & 1, &never);
+      if (ok) clear_pending();
+      // copies in flight when a wait gave up: let them land before the CTA's shared memory goes away
+      if (gave_up) {
+        int never = 0;
+        for (int q = 0; q < NS; ++q) {
+          const uint32_t r = q < slot ? round : round - 1;  // the slot's last use
+          if (q < slot || round > 0) bar_wait(q == pend_slot ? fix : full(q), q == pend_slot ? fix_phase : r & 1, &never);
+        }
       }
-    }
-  } else if (wid == 9 || wid == 10) {  // ---------------------------------------------------------------- products
-    const int st = wid - 9;
-    constexpr uint32_t id_s = mma_idesc(kTcKeys, false), id_o = mma_idesc(D, true);
-    const uint32_t ts = tm + st * 128, to = tm + 256 + st * D;
-    const uint32_t q_lo = desc_low(base + st * Sh::kQ, 16);
-    const uint32_t k_lo = desc_low(ring, 16), v_lo = desc_low(ring, PANEL);
-    int slot = 0;
-    uint32_t round = 0, p_phase = 0, q_phase = 0, b_round = 0, o_phase = 0;
-    int buf = 0;
-    bool ok = true;
-    while (ok && next_work(a, tot, &x, x_end, &w)) {
-      const int lag = w.both ? 1 : 2;
-      if (!(ok = bar_wait(q_full(st), q_phase, &gave_up))) break;
-      q_phase ^= 1;
-      if (!w.both && w.cnt == 1 && st == 1 && lane == 0) bar_arrive(o_full(1));  // no tile for stream 1: nothing to wait for
-      int room = kFlushTiles - st * (kFlushTiles / 2);  // tiles until O starts again
-      bool fresh = true, first = true;
+    } else if (wid == 9 || wid == 10) {  // ---------------------------------------------------------------- products
+      const int st = wid - 9;
+      constexpr uint32_t id_s = mma_idesc(kTcKeys, false), id_o = mma_idesc(D, true);
+      const uint32_t ts = tm + st * 128, to = tm + 256 + st * D;
+      const uint32_t q_lo = desc_low(base + st * Sh::kQ, 16);
+      const uint32_t k_lo = desc_low(ring, 16), v_lo = desc_low(ring, PANEL);
+      int slot = 0;
+      uint32_t round = 0, p_phase = 0, q_phase = 0, b_round = 0, o_phase = 0;
+      int buf = 0;
+      bool ok = true;
+      while (ok && next_work(a, tot, &x, x_end, &w)) {
+        const int lag = w.both ? 1 : 2;
+        if (!(ok = bar_wait(q_full(st), q_phase, &gave_up))) break;
+        q_phase ^= 1;
+        if (!w.both && w.cnt == 1 && st == 1 && lane == 0) bar_arrive(o_full(1));  // no tile for stream 1: nothing to wait for
+        int room = kFlushTiles - st * (kFlushTiles / 2);  // tiles until O starts again
+        bool fresh = true, first = true;
 #pragma unroll 1
-      for (int i = 0; i < w.cnt + lag && ok; ++i) {
-        const bool mine = w.both || (i & 1) == st;
-        if (i >= lag && PV) {
-          if (!(ok = bar_wait(full(slot), round & 1, &gave_up))) break;
-          if (mine) {
-            if (fresh && !first && !(ok = bar_wait(o_free(st), o_phase, &gave_up))) break;
-            if (fresh && !first) o_phase ^= 1;
-            first = false;
-            // the weights come in two halves of 64 keys: the products of the first run under the exponentials of the second
-            const uint32_t v = v_lo + slot * (Sh::kTile >> 4);
+        for (int i = 0; i < w.cnt + lag && ok; ++i) {
+          const bool mine = w.both || (i & 1) == st;
+          if (i >= lag && PV) {
+            if (!(ok = bar_wait(full(slot), round & 1, &gave_up))) break;
+            if (mine) {
+              if (fresh && !first && !(ok = bar_wait(o_free(st), o_phase, &gave_up))) break;
+              if (fresh && !first) o_phase ^= 1;
+              first = false;
+              // the weights come in two halves of 64 keys: the products of the first run under the exponentials of the second
+              const uint32_t v = v_lo + slot * (Sh::kTile >> 4);
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              if (!(ok = bar_wait(p_full(st, half), p_phase, &gave_up))) break;
+              for (int half = 0; half < 2; ++half) {
+                if (!(ok = bar_wait(p_full(st, half), p_phase, &gave_up))) break;
+                tc_fence_after();
+                if (lane == 0) {
+#pragma unroll
+                  for (int k = half * 4; k < half * 4 + 4; ++k)
+#pragma unroll
+                    for (int part = 0; part < 2; ++part)
+                      mma_ts(to, ts + (k / 2) * 32 + part * 16 + (k & 1) * 8, v + k * (2048 >> 4), id_o,
+                             k || part ? 1u : uint32_t(!fresh));
+                }
+                __syncwarp();
+              }
+              if (!ok) break;
+              p_phase ^= 1;
+              fresh = --room == 0;
+              if (fresh) room = kFlushTiles;
+              if (lane == 0) {
+                if (fresh && i + (w.both ? 1 : 2) < w.cnt + lag) mma_commit(o_chunk(st));
+                mma_commit(empty(slot));
+                if (i + lag >= w.cnt + lag) mma_commit(o_full(st));
+              }
+            } else if (lane == 0) {
+              bar_arrive(empty(slot));
+            }
+            __syncwarp();
+            if (++slot == NS) {
+              slot = 0;
+              ++round;
+            }
+          }
+          if (i < w.cnt) {
+            if (!(ok = bar_wait(full(slot), round & 1, &gave_up))) break;
+            if (mine) {
+              if (!PV && !(ok = bar_wait(p_full(st, buf), (b_round & 1) ^ 1, &gave_up))) break;  // the buffer has been read
               tc_fence_after();
               if (lane == 0) {
+                const uint32_t k = k_lo + slot * (Sh::kTile >> 4);
 #pragma unroll
-                for (int k = half * 4; k < half * 4 + 4; ++k)
-#pragma unroll
-                  for (int part = 0; part < 2; ++part)
-                    mma_ts(to, ts + (k / 2) * 32 + part * 16 + (k & 1) * 8, v + k * (2048 >> 4), id_o,
-                           k || part ? 1u : uint32_t(!fresh));
+                for (int e = 0; e < D / 16; ++e) {
+                  const uint32_t off = ((e / 4) * PANEL + (e % 4) * 32) >> 4;
+                  mma_ss(ts + (PV ? 0 : buf * 256), q_lo + off, k + off, id_s, e ? 1u : 0u);
+                }
+                mma_commit(s_full(st, PV ? 0 : buf));
+                mma_commit(empty(slot));
               }
-              __syncwarp();
-            }
-            if (!ok) break;
-            p_phase ^= 1;
-            fresh = --room == 0;
-            if (fresh) room = kFlushTiles;
-            if (lane == 0) {
-              if (fresh && i + (w.both ? 1 : 2) < w.cnt + lag) mma_commit(o_chunk(st));
-              mma_commit(empty(slot));
-              if (i + lag >= w.cnt + lag) mma_commit(o_full(st));
-            }
-          } else if (lane == 0) {
-            bar_arrive(empty(slot));
-          }
-          __syncwarp();
-          if (++slot == NS) {
-            slot = 0;
-            ++round;
-          }
-        }
-        if (i < w.cnt) {
-          if (!(ok = bar_wait(full(slot), round & 1, &gave_up))) break;
-          if (mine) {
-            if (!PV && !(ok = bar_wait(p_full(st, buf), (b_round & 1) ^ 1, &gave_up))) break;  // the buffer has been read
-            tc_fence_after();
-            if (lane == 0) {
-              const uint32_t k = k_lo + slot * (Sh::kTile >> 4);
-#pragma unroll
-              for (int e = 0; e < D / 16; ++e) {
-                const uint32_t off = ((e / 4) * PANEL + (e % 4) * 32) >> 4;
-                mma_ss(ts + (PV ? 0 : buf * 256), q_lo + off, k + off, id_s, e ? 1u : 0u);
+              if (!PV && ++buf == 2) {
+                buf = 0;
+                ++b_round;
               }
-              mma_commit(s_full(st, PV ? 0 : buf));
-              mma_commit(empty(slot));
+            } else if (lane == 0) {
+              bar_arrive(empty(slot));
             }
-            if (!PV && ++buf == 2) {
-              buf = 0;
-              ++b_round;
+            __syncwarp();
+            if (++slot == NS) {
+              slot = 0;
+              ++round;
             }
-          } else if (lane == 0) {
-            bar_arrive(empty(slot));
-          }
-          __syncwarp();
-          if (++slot == NS) {
-            slot = 0;
-            ++round;
           }
         }
       }
-    }
-    // nothing of the tensor pipe may be in flight when tensor memory is given back
-    if (lane == 0) mma_commit(done);
-    __syncwarp();
-    int never = 0;
-    bar_wait(done, 0, &never);
-  } else if (wid == 11) {
-    if (blockIdx.x == 0) rows_publish(a, tot);
-  } else if (PV) {  // ---------------------------------------------------------------- O to global memory
-    const int wrow = (wid & 3) * 32;
-    const uint32_t stage = ring + NS * Sh::kTile + wrow * 256;
-    uint32_t phase[2] = {0, 0};
-    bool ok = true;
-    while (ok && next_work(a, tot, &x, x_end, &w)) {
-      // the streams' flushes in the order of their tiles: stream 1 after kFlushTiles / 2, stream 0 after kFlushTiles, ...
-      const int n0 = w.both ? w.cnt : (w.cnt + 1) / 2, n1 = w.both ? w.cnt : w.cnt / 2;
+      // nothing of the tensor pipe may be in flight when tensor memory is given back
+      if (lane == 0) mma_commit(done);
+      __syncwarp();
+      int never = 0;
+      bar_wait(done, 0, &never);
+    } else if (wid == 11) {
+      if (blockIdx.x == 0) rows_publish(a, tot);
+    } else if (PV) {  // ---------------------------------------------------------------- O to global memory
+      const int wrow = (wid & 3) * 32;
+      const uint32_t stage = ring + NS * Sh::kTile + wrow * 256;
+      uint32_t phase[2] = {0, 0};
+      bool ok = true;
+      while (ok && next_work(a, tot, &x, x_end, &w)) {
+        // the streams' flushes in the order of their tiles: stream 1 after kFlushTiles / 2, stream 0 after kFlushTiles, ...
+        const int n0 = w.both ? w.cnt : (w.cnt + 1) / 2, n1 = w.both ? w.cnt : w.cnt / 2;
 #pragma unroll 1
-      for (int f = 0; f * (kFlushTiles / 2) + kFlushTiles / 2 < max(n0, n1) && ok; ++f) {
-        const int st = (f & 1) ^ 1;
-        if ((f + 1) * (kFlushTiles / 2) >= (st ? n1 : n0)) continue;  // the stream ends before
-        if (!(ok = bar_wait(o_chunk(st), phase[st], &gave_up))) break;
-        phase[st] ^= 1;
-        tc_fence_after();
-        const int nrows = min(128, w.seg_rows - w.s.p * kTcRows - (w.both ? st * 128 : 0));
-        const uint32_t to = tm + (uint32_t(wrow) << 16) + 256 + st * D;
-        float* dst = sofar_base(a, st, wrow, D);
-        if (wrow < nrows) {
+        for (int f = 0; f * (kFlushTiles / 2) + kFlushTiles / 2 < max(n0, n1) && ok; ++f) {
+          const int st = (f & 1) ^ 1;
+          if ((f + 1) * (kFlushTiles / 2) >= (st ? n1 : n0)) continue;  // the stream ends before
+          if (!(ok = bar_wait(o_chunk(st), phase[st], &gave_up))) break;
+          phase[st] ^= 1;
+          tc_fence_after();
+          const int nrows = min(128, w.seg_rows - w.s.p * kTcRows - (w.both ? st * 128 : 0));
+          const uint32_t to = tm + (uint32_t(wrow) << 16) + 256 + st * D;
+          float* dst = sofar_base(a, st, wrow, D);
+          if (wrow < nrows) {
 #pragma unroll 1
-          for (int c0 = 0; c0 < D; c0 += 64) {
+            for (int c0 = 0; c0 < D; c0 += 64) {
 #pragma unroll 1
-            for (int j = 0; j < 64; j += 32) {
-              float v[32];
-              tmem_ld32(to + c0 + j, v);
-              tmem_wait32(v);
+              for (int j = 0; j < 64; j += 32) {
+                float v[32];
+                tmem_ld32(to + c0 + j, v);
+                tmem_wait32(v);
 #pragma unroll
-              for (int q = 0; q < 8; ++q) st_shared4(stage + lane * 256 + ((((j >> 2) + q) ^ (lane & 7)) << 4), v + 4 * q);
-            }
-            if (c0 + 64 == D) {  // all of O has been read
-              tc_fence_before();
+                for (int q = 0; q < 8; ++q) st_shared4(stage + lane * 256 + ((((j >> 2) + q) ^ (lane & 7)) << 4), v + 4 * q);
+              }
+              if (c0 + 64 == D) {  // all of O has been read
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(o_free(st));
+              }
+              fence_async_smem();
               __syncwarp();
-              if (lane == 0) bar_arrive(o_free(st));
+              if (lane == 0) {
+                if (f < 2) bulk_store(dst + c0 * 32, stage, 32 * 256);
+                else bulk_add(dst + c0 * 32, stage, 32 * 256);
+                bulk_commit();
+                if (c0 + 64 == D) bulk_wait_all();  // before the next addition to the same place, and before anyone reads it
+                else bulk_wait_read();
+              }
+              __syncwarp();
             }
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              if (f < 2) bulk_store(dst + c0 * 32, stage, 32 * 256);
-              else bulk_add(dst + c0 * 32, stage, 32 * 256);
-              bulk_commit();
-              if (c0 + 64 == D) bulk_wait_all();  // before the next addition to the same place, and before anyone reads it
-              else bulk_wait_read();
-            }
-            __syncwarp();
+            asm volatile("fence.proxy.async;" ::: "memory");
+          } else if (lane == 0) {
+            bar_arrive(o_free(st));
           }
-          asm volatile("fence.proxy.async;" ::: "memory");
-        } else if (lane == 0) {
-          bar_arrive(o_free(st));
+          if (lane == 0) bar_arrive(flush_done(st));
         }
-        if (lane == 0) bar_arrive(flush_done(st));
       }
     }
-  }
   } else {  // ---------------------------------------------------------------- the streams' rows
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowRegs));
     const int st = wid >> 2, row = tid & 127, wrow = (wid & 3) * 32;
@@ -486,213 +489,213 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
       };
       const int step = w.both ? 1 : 2, i0 = w.both ? 0 : st;
       if constexpr (PV) {
-      // Streams take turns: a tile may begin once the other stream has handed over half of its own.  Left alone they fall into
-      // step, and the tensor pipe idles while both weigh (256K tokens behind 64 sequences: 413 us, whole turns 400, half
-      // turns 380).
-      const bool turns = w.cnt > kTurnTiles;
-      int room = kFlushTiles - st * (kFlushTiles / 2);  // tiles until O starts again
-      bool fresh = true, first_tile = true;
+        // Streams take turns: a tile may begin once the other stream has handed over half of its own.  Left alone they fall into
+        // step, and the tensor pipe idles while both weigh (256K tokens behind 64 sequences: 413 us, whole turns 400, half
+        // turns 380).
+        const bool turns = w.cnt > kTurnTiles;
+        int room = kFlushTiles - st * (kFlushTiles / 2);  // tiles until O starts again
+        bool fresh = true, first_tile = true;
 #pragma unroll 1
-      for (int i = i0; i < w.cnt; i += step) {
-        if (turns && (st || i != i0)) {
-          if (!(ok = bar_wait(turn(st), t_phase, &gave_up))) break;
-          t_phase ^= 1;
-        }
-        if (!(ok = bar_wait(s_full(st), s_phase, &gave_up))) break;
-        s_phase ^= 1;
-        tc_fence_after();
-        if (fresh && !first_tile) pending = flushed = true;  // O is being added to global memory
-        // before this tile's weights can complete O and have it added again, every warp has seen the time before
-        if (pending && room == 1) {
-          if (!(ok = bar_wait(flush_done(st), f_phase, &gave_up))) break;
-          f_phase ^= 1;
-          pending = false;
-        }
-        if (active) {
-          const int left = lim - (w.t0 + i) * kTcKeys;  // keys of the tile that the row sees
-          const bool mask = __any_sync(0xffffffffu, left < kTcKeys);
-          float va[32], vb[32];
-          float mx;
-          {
-            float vc[32], vd[32];
-            tmem_ld32(ts, va);
-            tmem_ld32(ts + 32, vb);
-            tmem_ld32(ts + 64, vc);
-            tmem_ld32(ts + 96, vd);
-            tmem_wait32(va);
-            tmem_wait32(vb);
-            tmem_wait32(vc);
-            tmem_wait32(vd);
-            if (mask) {
-              hide32(va, 0, left);
-              hide32(vb, 32, left);
-              hide32(vc, 64, left);
-              hide32(vd, 96, left);
-            }
-            mx = fmaxf(fmaxf(largest32(va), largest32(vb)), fmaxf(largest32(vc), largest32(vd)));
+        for (int i = i0; i < w.cnt; i += step) {
+          if (turns && (st || i != i0)) {
+            if (!(ok = bar_wait(turn(st), t_phase, &gave_up))) break;
+            t_phase ^= 1;
           }
-          tmem_ld32(ts, va);  // again, chunk by chunk, for the exponentials
-          const float m_new = mx * c2;
-          const bool grow = m_new > m_ref + kLazyMax || (m_ref == -INFINITY && m_new > -INFINITY);
-          if (__any_sync(0xffffffffu, grow)) {
-            const float up = grow ? m_new : m_ref;
-            const float sc = m_ref == -INFINITY ? 0.f : ex2(m_ref - up);
-            if (flushed) {  // what has left O already
-              if (pending) {
-                if (!(ok = bar_wait(flush_done(st), f_phase, &gave_up))) break;
-                f_phase ^= 1;
-                pending = false;
+          if (!(ok = bar_wait(s_full(st), s_phase, &gave_up))) break;
+          s_phase ^= 1;
+          tc_fence_after();
+          if (fresh && !first_tile) pending = flushed = true;  // O is being added to global memory
+          // before this tile's weights can complete O and have it added again, every warp has seen the time before
+          if (pending && room == 1) {
+            if (!(ok = bar_wait(flush_done(st), f_phase, &gave_up))) break;
+            f_phase ^= 1;
+            pending = false;
+          }
+          if (active) {
+            const int left = lim - (w.t0 + i) * kTcKeys;  // keys of the tile that the row sees
+            const bool mask = __any_sync(0xffffffffu, left < kTcKeys);
+            float va[32], vb[32];
+            float mx;
+            {
+              float vc[32], vd[32];
+              tmem_ld32(ts, va);
+              tmem_ld32(ts + 32, vb);
+              tmem_ld32(ts + 64, vc);
+              tmem_ld32(ts + 96, vd);
+              tmem_wait32(va);
+              tmem_wait32(vb);
+              tmem_wait32(vc);
+              tmem_wait32(vd);
+              if (mask) {
+                hide32(va, 0, left);
+                hide32(vb, 32, left);
+                hide32(vc, 64, left);
+                hide32(vd, 96, left);
+              }
+              mx = fmaxf(fmaxf(largest32(va), largest32(vb)), fmaxf(largest32(vc), largest32(vd)));
+            }
+            tmem_ld32(ts, va);  // again, chunk by chunk, for the exponentials
+            const float m_new = mx * c2;
+            const bool grow = m_new > m_ref + kLazyMax || (m_ref == -INFINITY && m_new > -INFINITY);
+            if (__any_sync(0xffffffffu, grow)) {
+              const float up = grow ? m_new : m_ref;
+              const float sc = m_ref == -INFINITY ? 0.f : ex2(m_ref - up);
+              if (flushed) {  // what has left O already
+                if (pending) {
+                  if (!(ok = bar_wait(flush_done(st), f_phase, &gave_up))) break;
+                  f_phase ^= 1;
+                  pending = false;
+                }
+                if (grow) {
+#pragma unroll 1
+                  for (int j = 0; j < D; j += 32) {  // eight pieces on their way
+#pragma unroll
+                    for (int q = 0; q < 32; q += 4)
+                      *reinterpret_cast<float4*>(vb + q) = __ldcg(reinterpret_cast<const float4*>(sofar_at(j + q)));
+#pragma unroll
+                    for (int q = 0; q < 32; q += 4) {
+#pragma unroll
+                      for (int e = 0; e < 4; ++e) vb[q + e] = m_ref == -INFINITY ? 0.f : vb[q + e] * sc;
+                      __stcg(reinterpret_cast<float4*>(sofar_at(j + q)), make_float4(vb[q], vb[q + 1], vb[q + 2], vb[q + 3]));
+                    }
+                  }
+                  __threadfence();
+                  asm volatile("fence.proxy.async;" ::: "memory");
+                }
+                __syncwarp();
+              }
+              if (!fresh) {
+#pragma unroll 1
+                for (int j = 0; j < D; j += 32) {
+                  tmem_ld32(to + j, vb);
+                  tmem_wait32(vb);
+                  if (grow) {
+#pragma unroll
+                    for (int q = 0; q < 32; ++q) vb[q] = m_ref == -INFINITY ? 0.f : vb[q] * sc;
+                  }
+                  tmem_st32(to + j, reinterpret_cast<const uint32_t*>(vb));
+                }
               }
               if (grow) {
-#pragma unroll 1
-                for (int j = 0; j < D; j += 32) {  // eight pieces on their way
-#pragma unroll
-                  for (int q = 0; q < 32; q += 4)
-                    *reinterpret_cast<float4*>(vb + q) = __ldcg(reinterpret_cast<const float4*>(sofar_at(j + q)));
-#pragma unroll
-                  for (int q = 0; q < 32; q += 4) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) vb[q + e] = m_ref == -INFINITY ? 0.f : vb[q + e] * sc;
-                    __stcg(reinterpret_cast<float4*>(sofar_at(j + q)), make_float4(vb[q], vb[q + 1], vb[q + 2], vb[q + 3]));
-                  }
-                }
-                __threadfence();
-                asm volatile("fence.proxy.async;" ::: "memory");
+                l_run *= sc;
+                m_ref = up;
               }
+            }
+            const float mb = m_ref == -INFINITY ? 0.f : m_ref;
+            const uint64_t mm = pair(-mb, -mb);
+            uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+            // kept logits: the row's own run of the tile (columns past the last key lie in the padding of the row)
+            float* lg = LG && row < nrows
+                            ? a.logits + (int64_t(w.s.h) * a.rows + r0 + row) * a.ld_logits + int64_t(w.t0 + i) * kTcKeys
+                            : nullptr;
+            auto weigh = [&](const float* v, int c0) {  // 32 keys: their weights' hi parts, then their lo parts, over the logits
+              uint32_t o[32];
+#pragma unroll
+              for (int q = 0; q < 16; ++q) {
+                const uint64_t e = fma2(pair(v[2 * q], v[2 * q + 1]), cc, mm);
+                const uint64_t p = ex2_pair(e);
+                sum[q & 1] = add2(sum[q & 1], p);
+                float p0, p1;
+                unpair(p, &p0, &p1);
+                o[q] = pack_bf16(p0, p1);
+                unpair(fma2(pair(__uint_as_float(o[q] << 16), __uint_as_float(o[q] & 0xffff0000u)), minus, p), &p0, &p1);
+                o[16 + q] = pack_bf16(p0, p1);
+              }
+              tmem_st32(ts + c0, o);
+              if (LG && lg) keep_logits(a, lg, v, (w.t0 + i) * kTcKeys, c0, c2);
+            };
+#pragma unroll 1
+            for (int j = 0; j < kTcKeys; j += 64) {
+              tmem_wait32(va);
+              tmem_ld32(ts + j + 32, vb);
+              if (mask) hide32(va, j, left);
+              weigh(va, j);
+              tmem_wait32(vb);
+              if (j == 0) tmem_ld32(ts + 64, va);
+              if (mask) hide32(vb, j + 32, left);
+              weigh(vb, j + 32);
+              tmem_wait_st();
+              tc_fence_before();
               __syncwarp();
-            }
-            if (!fresh) {
-#pragma unroll 1
-              for (int j = 0; j < D; j += 32) {
-                tmem_ld32(to + j, vb);
-                tmem_wait32(vb);
-                if (grow) {
-#pragma unroll
-                  for (int q = 0; q < 32; ++q) vb[q] = m_ref == -INFINITY ? 0.f : vb[q] * sc;
-                }
-                tmem_st32(to + j, reinterpret_cast<const uint32_t*>(vb));
+              if (lane == 0) {
+                bar_arrive(p_full(st, j >> 6));
+                if (turns && j == 0) bar_arrive(turn(st ^ 1));
               }
             }
-            if (grow) {
-              l_run *= sc;
-              m_ref = up;
-            }
-          }
-          const float mb = m_ref == -INFINITY ? 0.f : m_ref;
-          const uint64_t mm = pair(-mb, -mb);
-          uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
-          // kept logits: the row's own run of the tile (columns past the last key lie in the padding of the row)
-          float* lg = LG && row < nrows
-                          ? a.logits + (int64_t(w.s.h) * a.rows + r0 + row) * a.ld_logits + int64_t(w.t0 + i) * kTcKeys
-                          : nullptr;
-          auto weigh = [&](const float* v, int c0) {  // 32 keys: their weights' hi parts, then their lo parts, over the logits
-            uint32_t o[32];
-#pragma unroll
-            for (int q = 0; q < 16; ++q) {
-              const uint64_t e = fma2(pair(v[2 * q], v[2 * q + 1]), cc, mm);
-              const uint64_t p = ex2_pair(e);
-              sum[q & 1] = add2(sum[q & 1], p);
-              float p0, p1;
-              unpair(p, &p0, &p1);
-              o[q] = pack_bf16(p0, p1);
-              unpair(fma2(pair(__uint_as_float(o[q] << 16), __uint_as_float(o[q] & 0xffff0000u)), minus, p), &p0, &p1);
-              o[16 + q] = pack_bf16(p0, p1);
-            }
-            tmem_st32(ts + c0, o);
-            if (LG && lg) keep_logits(a, lg, v, (w.t0 + i) * kTcKeys, c0, c2);
-          };
-#pragma unroll 1
-          for (int j = 0; j < kTcKeys; j += 64) {
-            tmem_wait32(va);
-            tmem_ld32(ts + j + 32, vb);
-            if (mask) hide32(va, j, left);
-            weigh(va, j);
-            tmem_wait32(vb);
-            if (j == 0) tmem_ld32(ts + 64, va);
-            if (mask) hide32(vb, j + 32, left);
-            weigh(vb, j + 32);
-            tmem_wait_st();
+            float s0, s1;
+            unpair(add2(sum[0], sum[1]), &s0, &s1);
+            l_run += s0 + s1;
+          } else {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-              bar_arrive(p_full(st, j >> 6));
-              if (turns && j == 0) bar_arrive(turn(st ^ 1));
+              bar_arrive(p_full(st, 0));
+              bar_arrive(p_full(st, 1));
+              if (turns) bar_arrive(turn(st ^ 1));
             }
           }
-          float s0, s1;
-          unpair(add2(sum[0], sum[1]), &s0, &s1);
-          l_run += s0 + s1;
-        } else {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            bar_arrive(p_full(st, 0));
-            bar_arrive(p_full(st, 1));
-            if (turns) bar_arrive(turn(st ^ 1));
-          }
+          first_tile = false;
+          fresh = --room == 0;
+          if (fresh) room = kFlushTiles;
         }
-        first_tile = false;
-        fresh = --room == 0;
-        if (fresh) room = kFlushTiles;
-      }
-      // turns of the other stream that this one has no tile to wait for: the last one of stream 1, for stream 0 and of
-      // stream 0 for a stream 1 with one tile less
-      if (ok && turns && (st == 0 ? w.both || !(w.cnt & 1) : !w.both && (w.cnt & 1))) {
-        if (!(ok = bar_wait(turn(st), t_phase, &gave_up))) break;
-        t_phase ^= 1;
-      }
+        // turns of the other stream that this one has no tile to wait for: the last one of stream 1, for stream 0 and of
+        // stream 0 for a stream 1 with one tile less
+        if (ok && turns && (st == 0 ? w.both || !(w.cnt & 1) : !w.both && (w.cnt & 1))) {
+          if (!(ok = bar_wait(turn(st), t_phase, &gave_up))) break;
+          t_phase ^= 1;
+        }
       } else {
 #pragma unroll 1
-      for (int i = i0; i < w.cnt; i += step) {  // only the sums
-        if (!(ok = bar_wait(s_full(st, buf), s_phase, &gave_up))) break;
-        tc_fence_after();
-        if (active) {
-          const int left = lim - (w.t0 + i) * kTcKeys;  // keys of the tile that the row sees
-          const bool mask = __any_sync(0xffffffffu, left < kTcKeys);
-          const uint32_t tb = ts + buf * 256;
-          float* lg = LG && row < nrows
-                          ? a.logits + (int64_t(w.s.h) * a.rows + r0 + row) * a.ld_logits + int64_t(w.t0 + i) * kTcKeys
-                          : nullptr;
-          float v[kTcKeys];
+        for (int i = i0; i < w.cnt; i += step) {  // only the sums
+          if (!(ok = bar_wait(s_full(st, buf), s_phase, &gave_up))) break;
+          tc_fence_after();
+          if (active) {
+            const int left = lim - (w.t0 + i) * kTcKeys;  // keys of the tile that the row sees
+            const bool mask = __any_sync(0xffffffffu, left < kTcKeys);
+            const uint32_t tb = ts + buf * 256;
+            float* lg = LG && row < nrows
+                            ? a.logits + (int64_t(w.s.h) * a.rows + r0 + row) * a.ld_logits + int64_t(w.t0 + i) * kTcKeys
+                            : nullptr;
+            float v[kTcKeys];
 #pragma unroll
-          for (int j = 0; j < kTcKeys; j += 32) tmem_ld32(tb + j, v + j);
+            for (int j = 0; j < kTcKeys; j += 32) tmem_ld32(tb + j, v + j);
 #pragma unroll
-          for (int j = 0; j < kTcKeys; j += 32) tmem_wait32(v + j);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) bar_arrive(p_full(st, buf));  // the buffer has been read
-          if (mask) {
+            for (int j = 0; j < kTcKeys; j += 32) tmem_wait32(v + j);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(p_full(st, buf));  // the buffer has been read
+            if (mask) {
 #pragma unroll
-            for (int j = 0; j < kTcKeys; j += 32) hide32(v + j, j, left);
+              for (int j = 0; j < kTcKeys; j += 32) hide32(v + j, j, left);
+            }
+            const float m_new = fmaxf(fmaxf(largest32(v), largest32(v + 32)), fmaxf(largest32(v + 64), largest32(v + 96))) * c2;
+            if (m_new > m_ref + kLazyMax || (m_ref == -INFINITY && m_new > -INFINITY)) {
+              l_run *= m_ref == -INFINITY ? 0.f : ex2(m_ref - m_new);
+              m_ref = m_new;
+            }
+            const float mb = m_ref == -INFINITY ? 0.f : m_ref;
+            const uint64_t mm = pair(-mb, -mb);
+            uint64_t sum[4] = {pair(0.f, 0.f), pair(0.f, 0.f), pair(0.f, 0.f), pair(0.f, 0.f)};
+#pragma unroll
+            for (int q = 0; q < kTcKeys / 2; ++q)
+              sum[q & 3] = add2(sum[q & 3], ex2_pair(fma2(pair(v[2 * q], v[2 * q + 1]), cc, mm)));
+            float s0, s1;
+            unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), &s0, &s1);
+            l_run += s0 + s1;
+            if (LG && lg) {
+#pragma unroll
+              for (int j = 0; j < kTcKeys; j += 32) keep_logits(a, lg, v + j, (w.t0 + i) * kTcKeys, j, c2);
+            }
+          } else {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(p_full(st, buf));
           }
-          const float m_new = fmaxf(fmaxf(largest32(v), largest32(v + 32)), fmaxf(largest32(v + 64), largest32(v + 96))) * c2;
-          if (m_new > m_ref + kLazyMax || (m_ref == -INFINITY && m_new > -INFINITY)) {
-            l_run *= m_ref == -INFINITY ? 0.f : ex2(m_ref - m_new);
-            m_ref = m_new;
+          if (++buf == 2) {
+            buf = 0;
+            s_phase ^= 1;
           }
-          const float mb = m_ref == -INFINITY ? 0.f : m_ref;
-          const uint64_t mm = pair(-mb, -mb);
-          uint64_t sum[4] = {pair(0.f, 0.f), pair(0.f, 0.f), pair(0.f, 0.f), pair(0.f, 0.f)};
-#pragma unroll
-          for (int q = 0; q < kTcKeys / 2; ++q)
-            sum[q & 3] = add2(sum[q & 3], ex2_pair(fma2(pair(v[2 * q], v[2 * q + 1]), cc, mm)));
-          float s0, s1;
-          unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), &s0, &s1);
-          l_run += s0 + s1;
-          if (LG && lg) {
-#pragma unroll
-            for (int j = 0; j < kTcKeys; j += 32) keep_logits(a, lg, v + j, (w.t0 + i) * kTcKeys, j, c2);
-          }
-        } else {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) bar_arrive(p_full(st, buf));
         }
-        if (++buf == 2) {
-          buf = 0;
-          s_phase ^= 1;
-        }
-      }
       }
       if (!ok) break;
       if (PV || i0 >= w.cnt) {  // also without work: the stream stays within one segment of its products' warp

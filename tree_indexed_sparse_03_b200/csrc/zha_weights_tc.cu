@@ -7,9 +7,11 @@
 // tile of query rows; each has two accumulators in tensor memory, so that one tile's product runs under the other's
 // exponentials, and two warpgroups, each for half of a tile's columns: with one warpgroup the exponential unit stood
 // still between tiles for a quarter of the time, with two on alternate tiles both accumulators came free at the same
-// time and the products had nothing to run under.  The two warpgroups of a stream add up at a segment's end.  Per tile and stream 512 cycles of products (d = 128) against 1024 of
-// exponentials (16 per cycle and SM): the exponentials bound it for many rows, the second read
-// of K for few.
+// time and the products had nothing to run under (64 queries x 8 heads over 64K tokens, the whole call: 129, 116 and
+// 114 us).  The two warpgroups of a stream add up at a segment's end.
+// Per tile and stream 512 cycles of products (d = 128) against 1024 of exponentials (16 per cycle and SM): the
+// exponentials bound it (the unit is busy 65 % of the time), for few row tiles the second read of K.  Taking part of
+// the exponentials to the FMA pipe by a polynomial was slower (132 -> 142 us): the issue slots are needed.
 //
 // Work split: a segment is 256 keys of one KV head against the row tiles that see
 // them; all row tiles of all segments form one flat list that is cut evenly over
