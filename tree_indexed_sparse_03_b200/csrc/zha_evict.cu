@@ -6,13 +6,12 @@
 namespace zha {
 
 // ------------------------------------------------------------------ selection
-// The keep - first - last largest sums among tokens [first, n - last), ties to
-// the lower token.  The threshold is found most significant bits first, 11 + 11 + 10 bits, from histograms of the
-// ordered keys; then each warp counts the tokens above and at the threshold in its run of tokens, a scan gives its
-// output position, and it lists its kept tokens in order.  What bounds it is latency: up to 16K tokens one CTA per head
-// keeps all keys in registers (4K tokens 5 us; read again from L2 in each pass 25 us), above that the passes are
-// kernels over the whole GPU (a cluster of eight CTAs per head took 34 us for 256K tokens and 142 us for 1M, with four
-// heads; these 18 and 50).
+// The keep - first - last largest sums among tokens [first, n - last), ties to the lower token.  The threshold is
+// found most significant bits first, 11 + 11 + 10 bits, from histograms of the ordered keys; then each warp counts
+// the tokens above and at the threshold in its run of tokens, a scan gives its output position, and it lists its
+// kept tokens in order.  What bounds it is latency: up to 16K tokens one CTA per head keeps all keys in registers
+// (4K tokens 5 us; read again from L2 in each pass 25 us), above that the passes are kernels over the whole GPU (a
+// cluster of eight CTAs per head took 34 us for 256K tokens and 142 us for 1M, with four heads; these 18 and 50).
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelBins = 2048;
@@ -23,8 +22,8 @@ __device__ __forceinline__ uint32_t evict_key(float x) {
   return float_to_ordered(x == 0.f ? 0.f : x);
 }
 
-// The bin that holds the want-th largest key and the keys above that bin, from a histogram of kSelBins bins (thread t holds
-// bins 2t and 2t + 1 from the top); the result is in found[] after the next barrier.
+// The bin that holds the want-th largest key and the keys above that bin, from a histogram of kSelBins bins (thread
+// t holds bins 2t and 2t + 1 from the top); the result is in found[] after the next barrier.
 __device__ __forceinline__ void sel_find(const uint32_t* hist, uint32_t want, uint32_t* wsum, uint32_t* found) {
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const uint2 two = *reinterpret_cast<const uint2*>(hist + kSelBins - 2 - 2 * tid);
@@ -149,10 +148,10 @@ template <int RK> __global__ void __launch_bounds__(kSelThreads) evict_select_ke
                __reduce_add_sync(0xffffffffu, lane < wid ? weq[lane] : 0u), int(a.first), out);
 }
 
-// Long caches: chunks of 8192 tokens over the whole GPU, one kernel per pass; the histograms are added in global memory (an
-// integer sum, the same in any order).  Kernel `pass` = 0, 1, 2 adds the pass's histogram, 3 counts each chunk's keys above and at
-// the threshold, 4 lists.  Every kernel finds the bin of the pass before it from that histogram (all CTAs the
-// same one; the first leaves it for the kernels after the next).
+// Long caches: chunks of 8192 tokens over the whole GPU, one kernel per pass; the histograms are added in global
+// memory (an integer sum, the same in any order).  Kernel `pass` = 0, 1, 2 adds the pass's histogram, 3 counts each
+// chunk's keys above and at the threshold, 4 lists.  Every kernel finds the bin of the pass before it from that
+// histogram (all CTAs the same one; the first leaves it for the kernels after the next).
 constexpr int kWideKeys = 8;
 constexpr int kWideChunk = kSelThreads * kWideKeys;
 
@@ -277,8 +276,8 @@ static cudaError_t launch_select(const EvictArgs& a, cudaStream_t st) {
 }
 
 // ------------------------------------------------------------------ moving the rows
-// Separate outputs: a plain gather.  Each thread has four 16-byte pieces in flight; bound by HBM
-// (each kept row read and written once).  1M -> 512K tokens, 4 heads of 128 bf16: 128 threads and streaming stores 435 us with the
+// Separate outputs: a plain gather.  Each thread has four 16-byte pieces in flight; bound by HBM (each kept row read
+// and written once).  1M -> 512K tokens, 4 heads of 128 bf16: 128 threads and streaming stores 435 us with the
 // selection, 256 and plain stores 465, eight pieces 507, two 489.
 constexpr int kMoveThreads = 128;
 constexpr int kMoveUnroll = 4;
@@ -314,10 +313,10 @@ __global__ void __launch_bounds__(kMoveThreads) evict_gather_kernel(EvictArgs a)
 }
 
 // Outputs that are their own inputs: kept row j comes from idx[j] >= j, so rows must be read before an
-// earlier-listed row's place is written.  One CTA moves a 32-byte column slice of one head's K or V (or its
-// sums): rounds of kSlideRows rows, all of a round's loads before a barrier, its stores after it.  Writing rows [i, i +
-// kSlideRows) can only overwrite sources of rows before i + kSlideRows, which have all been read; slices share no bytes,
-// so CTAs need no order among themselves.
+// earlier-listed row's place is written.  One CTA moves a 32-byte column slice of one head's K or V (or its sums):
+// rounds of kSlideRows rows, all of a round's loads before a barrier, its stores after it.  Writing rows [i, i +
+// kSlideRows) can only overwrite sources of rows before i + kSlideRows, which have all been read; slices share no
+// bytes, so CTAs need no order among themselves.
 constexpr int kSlideThreads = 1024;
 constexpr int kSlideUnroll = 4;
 

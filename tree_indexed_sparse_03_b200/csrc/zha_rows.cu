@@ -10,15 +10,13 @@ constexpr int kRowsKeys = 64;  // keys per tile
 constexpr int kWeightsCtas = 148 * 4;  // CTAs that the weights pass splits its rows up to
 
 // ------------------------------------------------------------------ attention, CUDA cores
-// One CTA: RB = 8 * RT rows against tiles of 64 keys.  A half-warp owns RT
-// rows: for S = Q K^T each lane holds RT rows x 4 keys (key = lane + 16 j), so a
-// row's maximum and sum are shuffles within the half-warp; for O += P V each lane
-// holds the same RT rows x d/16 columns, P passed through shared memory within
-// the warp.  Rows of shared memory are padded by 16 bytes, so 16-byte reads of 8
-// consecutive rows meet no bank conflict.  Per 4 dimensions a lane does 16 RT
-// FMAs on RT + 4 16-byte reads: the FMA pipe bounds it for RT >= 4 (16 sequences x 4 heads behind 16K tokens, d = 128:
-// 91 us, 24 TFLOP/s), shared-memory reads and HBM for RT = 1 (8 rows over 64K tokens: 110 us, 2.4 TB/s; with two
-// pieces of K and V in flight per thread instead of sixteen 162 us).
+// One CTA: RB = 8 * RT rows against tiles of 64 keys.  A half-warp owns RT rows: for S = Q K^T each lane holds RT
+// rows x 4 keys (key = lane + 16 j), so a row's maximum and sum are shuffles within the half-warp; for O += P V each
+// lane holds the same RT rows x d/16 columns, P passed through shared memory within the warp.  Rows of shared memory
+// are padded by 16 bytes, so 16-byte reads of 8 consecutive rows meet no bank conflict.  Per 4 dimensions a lane
+// does 16 RT FMAs on RT + 4 16-byte reads: the FMA pipe bounds it for RT >= 4 (16 sequences x 4 heads behind 16K
+// tokens, d = 128: 91 us, 24 TFLOP/s), shared-memory reads and HBM for RT = 1 (8 rows over 64K tokens: 110 us, 2.4
+// TB/s; with two pieces of K and V in flight per thread instead of sixteen 162 us).
 template <typename T, int D, int RT>
 __global__ void __launch_bounds__(kRowsThreads) rows_scalar_kernel(RowsArgs a) {
   constexpr int RB = 8 * RT, LD = D + 4, PLD = kRowsKeys + 4, CT = D / 16;
@@ -327,11 +325,40 @@ __global__ void __launch_bounds__(256) rows_combine_kernel(RowsArgs a) {
 }
 
 // ------------------------------------------------------------------ column sums of the weights, CUDA cores
-// acc_out[h][k] = acc_in[h][k] + sum over rows of 2^(s c - lse): one CTA per (64 keys, KV head, row split); a
-// lane holds RT rows x 4 keys of S as above and sums over its rows; the eight half-warps are joined in order.
+// acc_out[h][k] = acc_in[h][k] + sum over rows of 2^(s c - lse): one CTA per (64 keys, KV head, row split); a lane
+// holds RT rows x 4 keys of S as above and sums over its rows; the eight half-warps are joined in order.  230 rows x
+// 4 heads over 9,000 tokens, causal, d = 128: 182 us with the attention before it, 193 with the keys loaded one
+// piece at a time.
+
+// ROWS padded rows of shared memory from row(r) (NULL: zeros), all 128 threads, G 16-byte pieces in flight per
+// thread.
+template <typename T, int D, int ROWS, typename F> __device__ __forceinline__ void fill_rows(float* dst, F row) {
+  constexpr int EPC = 16 / sizeof(T), CPR = D / EPC, LD = D + 4, N = ROWS * CPR / kRowsThreads, G = N < 8 ? N : 8;
+  static_assert(N * kRowsThreads == ROWS * CPR && N % G == 0, "whole rounds");
+#pragma unroll 1
+  for (int i0 = threadIdx.x; i0 < ROWS * CPR; i0 += G * kRowsThreads) {
+    uint4 v[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const int i = i0 + g * kRowsThreads;
+      const T* p = row(i / CPR);
+      v[g] = p ? ldg_stream(p + i % CPR * EPC) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const int i = i0 + g * kRowsThreads;
+      float f[EPC];
+      unpack16<T>(v[g], f);
+#pragma unroll
+      for (int e = 0; e < EPC; e += 4)
+        *reinterpret_cast<float4*>(dst + i / CPR * LD + i % CPR * EPC + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+    }
+  }
+}
+
 template <typename T, int D, int RT>
 __global__ void __launch_bounds__(kRowsThreads) weights_scalar_kernel(WeightsArgs a) {
-  constexpr int RB = 8 * RT, LD = D + 4, EPC = 16 / sizeof(T), CPR = D / EPC;
+  constexpr int RB = 8 * RT, LD = D + 4;
   extern __shared__ __align__(16) float sm[];
   float* sq = sm;
   float* sk = sq + RB * LD;
@@ -344,16 +371,7 @@ __global__ void __launch_bounds__(kRowsThreads) weights_scalar_kernel(WeightsArg
   pdl_trigger();
   pdl_wait();
   const T* Kh = static_cast<const T*>(a.K) + int64_t(h) * a.ld * D;
-  for (int i = tid; i < kRowsKeys * CPR; i += kRowsThreads) {
-    const int r = i / CPR, c = i % CPR;
-    float k[EPC];
-#pragma unroll
-    for (int e = 0; e < EPC; ++e) k[e] = 0.f;
-    if (k0 + r < a.n) unpack16<T>(ldg_stream(Kh + (k0 + r) * D + c * EPC), k);
-#pragma unroll
-    for (int e = 0; e < EPC; e += 4)
-      *reinterpret_cast<float4*>(sk + r * LD + c * EPC + e) = make_float4(k[e], k[e + 1], k[e + 2], k[e + 3]);
-  }
+  fill_rows<T, D, kRowsKeys>(sk, [&](int r) { return k0 + r < a.n ? Kh + (k0 + r) * D : nullptr; });
   float sum[4] = {0.f, 0.f, 0.f, 0.f};
   const int rend = int(min64(a.rows, int64_t(blockIdx.z + 1) * a.rows_per_split));
   int rbeg = int(int64_t(blockIdx.z) * a.rows_per_split);
@@ -363,24 +381,15 @@ __global__ void __launch_bounds__(kRowsThreads) weights_scalar_kernel(WeightsArg
   }
   for (int r0 = rbeg; r0 < rend; r0 += RB) {
     __syncthreads();
-    for (int i = tid; i < RB * CPR; i += kRowsThreads) {
-      const int r = i / CPR, c = i % CPR;
-      float v[EPC];
-#pragma unroll
-      for (int e = 0; e < EPC; ++e) v[e] = 0.f;
-      const int rr = r0 + r;
-      if (rr < rend) {
-        const int t = rr / a.group;
-        const int64_t ri = int64_t(t) * a.hq + h * a.group + (rr - t * a.group);
-        unpack16<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(a.Q) + ri * D + c * EPC), v);
-        if (c == 0) sl[r] = a.lse[ri] * 1.4426950408889634f;
-      } else if (c == 0) {
-        sl[r] = INFINITY;  // no row: every weight 2^-inf = 0
-      }
-#pragma unroll
-      for (int e = 0; e < EPC; e += 4)
-        *reinterpret_cast<float4*>(sq + r * LD + c * EPC + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-    }
+    auto q_row = [&](int rr) {
+      const int t = rr / a.group;
+      return int64_t(t) * a.hq + h * a.group + (rr - t * a.group);
+    };
+    fill_rows<T, D, RB>(sq, [&](int r) {
+      return r0 + r < rend ? static_cast<const T*>(a.Q) + q_row(r0 + r) * D : nullptr;
+    });
+    if (tid < RB)  // no row: every weight 2^-inf = 0
+      sl[tid] = r0 + tid < rend ? a.lse[q_row(r0 + tid)] * 1.4426950408889634f : INFINITY;
     __syncthreads();
     float acc[RT][4];
 #pragma unroll
@@ -471,6 +480,7 @@ __global__ void __launch_bounds__(256) weights_logits_kernel(WeightsArgs a) {
 // ------------------------------------------------------------------ host side
 namespace {
 
+// Rows per half-warp: few rows leave most of a larger block empty, more rows share each key read from shared memory.
 int scalar_rt(int d, int64_t rows) { return rows <= 8 ? 1 : (d == 128 || rows <= 32 ? 4 : 8); }
 
 size_t rows_smem(int d, int rt) {
@@ -489,8 +499,8 @@ template <typename T, int D, int RT> cudaError_t run_rows(const RowsArgs& a, cud
 template <typename T, int D> cudaError_t run_rows_rt(const RowsArgs& a, cudaStream_t st) {
   switch (1 << a.rb_log >> 3) {
     case 1: return run_rows<T, D, 1>(a, st);
-    case 4: return run_rows<T, D, 4>(a, st);
-    default: return run_rows<T, D, 8>(a, st);
+    case 8: if constexpr (D == 64) return run_rows<T, D, 8>(a, st);  // d = 128: registers and shared memory for half
+    default: return run_rows<T, D, 4>(a, st);
   }
 }
 
@@ -511,15 +521,15 @@ template <typename T, int D, int RT> cudaError_t run_weights(const WeightsArgs& 
 template <typename T, int D> cudaError_t run_weights_rt(const WeightsArgs& a, cudaStream_t st) {
   switch (scalar_rt(D, a.rows)) {
     case 1: return run_weights<T, D, 1>(a, st);
-    case 4: return run_weights<T, D, 4>(a, st);
-    default: return run_weights<T, D, 8>(a, st);
+    case 8: if constexpr (D == 64) return run_weights<T, D, 8>(a, st);
+    default: return run_weights<T, D, 4>(a, st);
   }
 }
 
 }  // namespace
 
-// CTAs (at most `most`, and no more than tiles) and partial rows of a plan whose row blocks and tiles are set.  Own caches
-// are taken as long as they can be.
+// CTAs (at most `most`, and no more than tiles) and partial rows of a plan whose row blocks and tiles are set.  Own
+// caches are taken as long as they can be.
 static void plan_parts(int hkv, int64_t B, int64_t n, int64_t ld_own, int most, RowsPlan* p) {
   const double pt = double((n + (1 << p->kt_log) - 1) >> p->kt_log), ot = double((ld_own + (1 << p->kt_log) - 1) >> p->kt_log);
   const double ps = double(hkv) * p->pp, os = double(B) * hkv * p->po;

@@ -195,8 +195,8 @@ __device__ __forceinline__ RowsSeg rows_find(const RowsArgs& a, const RowsTotals
 }
 
 // Partial slot of CTA c for a segment.  With own caches every row has several partials: slot c + segment number
-// (unique, since along the list either the CTA or the segment advances).  Without, a segment whose tiles lie
-// inside one CTA's share is written out directly, and a share cuts at most two: slot 2c for one that holds the share's
+// (unique, since along the list either the CTA or the segment advances).  Without, a segment whose tiles lie inside
+// one CTA's share is written out directly, and a share cuts at most two: slot 2c for one that holds the share's
 // begin, 2c + 1 for a later one.  Returns the slot's first row in `part`.
 __device__ __forceinline__ int64_t part_row(const RowsArgs& a, int c, int own, int id, bool later) {
   if (!a.has_own) return (2 * int64_t(c) + (later ? 1 : 0)) * a.rp;
@@ -316,8 +316,8 @@ uint64_t weights_tc_floats();
 cudaError_t launch_weights_tc(const WeightsArgs& a, int d, cudaStream_t st);
 cudaError_t launch_weights(const WeightsArgs& a, int dtype, int d, cudaStream_t st);
 
-// Calls of up to this many rows per KV head keep their logits (4 bytes per row and key, mostly in L2) rather than read
-// K again (2 d bytes per key) and run its products again.
+// Calls of up to this many rows per KV head keep their logits (4 bytes per row and key, mostly in L2) rather than
+// read K again (2 d bytes per key) and run its products again.
 constexpr int kLogitRows = 16;
 
 struct EvictArgs {

@@ -7,32 +7,31 @@
 //   P = 2^(S c - m)     (one thread per row: tensor memory -> registers, the row's maximum and sum, and
 //                        back over S as bf16),
 //   O += P V            (P from tensor memory, V from shared memory).
-// P enters the second product as two bf16 parts, hi + lo (S's 128 fp32 columns hold exactly the
-// two), because the output is fp32: one part alone leaves 2^-9 of every weight, the two 2^-17.  That
-// makes three products per tile instead of two: 3 * 512 cycles at 128 x 128 x 128 against 1024 cycles of exponentials
-// (16 per cycle and SM), so with both streams in flight - one in its exponentials while the other's products
-// run - the tensor pipe is the limit for many rows, HBM for few.  Measured: 64 sequences behind 256K tokens (4 KV heads
-// of 8, d = 128) 411 us in short runs, 1.0e15 tensor operations a second with the third product counted, 480 us in long
-// ones at the power limit; 5,250 cycles per tile of both streams of the 3,072 that its products take.  One sequence
-// (8 rows a head) 105 us for 537 MB of K and V, 5.1 TB/s.
-// A segment of more than 128 rows gives each stream its own rows and both the same tiles (each K and V
-// tile is loaded once for 256 rows); a smaller one gives both streams the same rows and every other tile,
-// and stream 0 joins the two results.
+// P enters the second product as two bf16 parts, hi + lo (S's 128 fp32 columns hold exactly the two), because the
+// output is fp32: one part alone leaves 2^-9 of every weight, the two 2^-17.  That makes three products per tile
+// instead of two: 3 * 512 cycles at 128 x 128 x 128 against 1024 cycles of exponentials (16 per cycle and SM), so
+// with both streams in flight - one in its exponentials while the other's products run - the tensor pipe is the
+// limit for many rows, HBM for few.  Measured: 64 sequences behind 256K tokens (4 KV heads of 8, d = 128) 411 us in
+// short runs, 1.0e15 tensor operations a second with the third product counted, 480 us in long ones at the power
+// limit; 5,250 cycles per tile of both streams of the 3,072 that its products take.  One sequence (8 rows a head)
+// 105 us for 537 MB of K and V, 5.1 TB/s. A segment of more than 128 rows gives each stream its own rows and both
+// the same tiles (each K and V tile is loaded once for 256 rows); a smaller one gives both streams the same rows and
+// every other tile, and stream 0 joins the two results.
 //
 // The maximum is lazy: O is rescaled only when a row's maximum has grown by more than 2^20, so weights stay below
 // 2^20 (the sums are floating point: nothing is lost) and the usual tile rescales nothing.
 //
-// The tensor pipe's fp32 accumulation cuts off instead of rounding, so the error of O grows with the number of products added
-// to it, 2.1e-8 of O each (measured: 3.7e-5 after 1,760, one stream's share of 256K tokens behind 64 sequences).  After
-// kFlushTiles tiles (16 products each) O is therefore added to a place of the stream's own in global memory (L2) with rounded
-// additions and starts again (5.4e-6 on the same case).  A warpgroup of its own does that under the next tile's
-// exponentials, through shared memory by bulk reductions, the streams half a period apart.
+// The tensor pipe's fp32 accumulation cuts off instead of rounding, so the error of O grows with the number of
+// products added to it, 2.1e-8 of O each (measured: 3.7e-5 after 1,760, one stream's share of 256K tokens behind 64
+// sequences).  After kFlushTiles tiles (16 products each) O is therefore added to a place of the stream's own in
+// global memory (L2) with rounded additions and starts again (5.4e-6 on the same case).  A warpgroup of its own does
+// that under the next tile's exponentials, through shared memory by bulk reductions, the streams half a period
+// apart.
 //
-// Roles: warps 0-3 and 4-7 the two streams' rows, warp 8 the TMA loads into a ring of K / V
-// tiles, warps 9 and 10 issue the two streams' products (a product's operands are five registers that one thread has to
-// provide: one warp for both streams took 100 cycles a product, above the 64 it runs).
-// Order of the products per stream: P V of the previous tile, then S of the next; a commit after S
-// therefore also says that the earlier P V is complete.
+// Roles: warps 0-3 and 4-7 the two streams' rows, warp 8 the TMA loads into a ring of K / V tiles, warps 9 and 10
+// issue the two streams' products (a product's operands are five registers that one thread has to provide: one warp
+// for both streams took 100 cycles a product, above the 64 it runs). Order of the products per stream: P V of the
+// previous tile, then S of the next; a commit after S therefore also says that the earlier P V is complete.
 //
 // The code of a role runs a few times per launch when lengths are short, and its first run waits for its
 // instructions: loops over a row's 128 logits go in two rounds of 2 x 32 columns rather than unrolled.
@@ -80,8 +79,8 @@ __device__ __forceinline__ float largest32(const float* v) {
   for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], v[28 + e]);
   return fmaxf(max3(m[0], m[1], m[2]), m[3]);
 }
-// Kept logits: lg is the row's run of the tile that begins at key k0.  Columns past the last key of a 16-byte piece lie in the
-// row's padding.
+// Kept logits: lg is the row's run of the tile that begins at key k0.  Columns past the last key of a 16-byte piece
+// lie in the row's padding.
 __device__ __forceinline__ void keep_logits(const RowsArgs& a, float* lg, const float* v, int k0, int c0, float c2) {
 #pragma unroll
   for (int q = 0; q < 32; q += 4)
@@ -243,9 +242,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
           const int t = (i >> 1) - (kv ? lag : 0);
           if (kv ? (!PV || t < 0) : t >= w.cnt) continue;
           const int k0 = (w.t0 + t) * kTcKeys;
-          // rows of V past a sequence's end hold anything (0 * NaN is NaN): cleared before the product sees them, once the
-          // copy has landed; meanwhile the next copies start, as long as none has to wait.  Past the prefix's end the
-          // tensor map ends, so the copy itself fills zeros.
+          // rows of V past a sequence's end hold anything (0 * NaN is NaN): cleared before the product sees them,
+          // once the copy has landed; meanwhile the next copies start, as long as none has to wait.  Past the
+          // prefix's end the tensor map ends, so the copy itself fills zeros.
           const bool clear = kv && w.s.own && k0 + kTcKeys > len;
           if ((clear || !bar_done(empty(slot), (round & 1) ^ 1)) && !(ok = clear_pending())) break;
           if (!(ok = bar_wait(empty(slot), (round & 1) ^ 1, &gave_up))) break;
@@ -301,7 +300,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
               if (fresh && !first && !(ok = bar_wait(o_free(st), o_phase, &gave_up))) break;
               if (fresh && !first) o_phase ^= 1;
               first = false;
-              // the weights come in two halves of 64 keys: the products of the first run under the exponentials of the second
+              // the weights come in two halves of 64 keys: the products of the first run under the exponentials of
+              // the second
               const uint32_t v = v_lo + slot * (Sh::kTile >> 4);
 #pragma unroll
               for (int half = 0; half < 2; ++half) {
@@ -378,7 +378,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
       uint32_t phase[2] = {0, 0};
       bool ok = true;
       while (ok && next_work(a, tot, &x, x_end, &w)) {
-        // the streams' flushes in the order of their tiles: stream 1 after kFlushTiles / 2, stream 0 after kFlushTiles, ...
+        // the streams' flushes in the order of their tiles: stream 1 after kFlushTiles / 2, stream 0 after
+        // kFlushTiles, ...
         const int n0 = w.both ? w.cnt : (w.cnt + 1) / 2, n1 = w.both ? w.cnt : w.cnt / 2;
 #pragma unroll 1
         for (int f = 0; f * (kFlushTiles / 2) + kFlushTiles / 2 < max(n0, n1) && ok; ++f) {
@@ -439,7 +440,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
       const int r0 = w.s.p * kTcRows + (w.both ? st * 128 : 0);  // the stream's first row
       const int nrows = min(128, w.seg_rows - r0);
       const int row_off = w.s.own ? w.s.b * a.m * a.group : 0;
-      // queries to shared memory, every warp its own rows: they are where its results leave from, and no other warp waits for that
+      // queries to shared memory, every warp its own rows: they are where its results leave from, and no other warp
+      // waits for that
       auto load_queries = [&]() {
         constexpr int CH = D / 8, RP = 32 / CH;  // 16-byte pieces of a row, rows per pass of a warp
         const int c = lane % CH, rq = wrow + lane / CH;
@@ -476,22 +478,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
       const bool whole = !a.has_own && w.t0 == 0 && w.cnt == w.s.tiles;
       const int64_t pr = part_row(a, blockIdx.x, w.s.own, w.s.id, x_begin < w.s.first) + (w.both ? st * 128 : 0) + row;
       const int64_t ri = row < nrows ? row_index(a, w.s.h, row_off + r0 + row) : 0;
-      // and where O is added up meanwhile, in the order it leaves shared memory: 64 columns, rows, swizzled 16-byte pieces
+      // and where O is added up meanwhile, in the order it leaves shared memory: 64 columns, rows, swizzled 16-byte
+      // pieces
       float* const sofar = sofar_base(a, st, wrow, D);
       auto sofar_at = [&](int col) {
         return sofar + (col >> 6) * (32 * 64) + lane * 64 + ((((col & 63) >> 2) ^ (lane & 7)) << 2);
       };
       constexpr int HC = D / 2, LN = HC / 4;  // columns of half a row, lanes for one
-      // 16-byte piece k of the half row from column c0 on, of row r: over both streams' queries, or over the stream's own
+      // 16-byte piece k of the half row from column c0 on, of row r: over both streams' queries, or over the
+      // stream's own
       auto cell = [&](bool all, int c0, int k, int r) {
         return all ? base + r * (D * 4) + c0 * 4 + ((k ^ (r & 7)) << 4)
                    : base + st * Sh::kQ + (k >> 3) * (128 * 128) + r * 128 + (((k & 7) ^ (r & 7)) << 4);
       };
       const int step = w.both ? 1 : 2, i0 = w.both ? 0 : st;
       if constexpr (PV) {
-        // Streams take turns: a tile may begin once the other stream has handed over half of its own.  Left alone they fall into
-        // step, and the tensor pipe idles while both weigh (256K tokens behind 64 sequences: 413 us, whole turns 400, half
-        // turns 380).
+        // Streams take turns: a tile may begin once the other stream has handed over half of its own.  Left alone
+        // they fall into step, and the tensor pipe idles while both weigh (256K tokens behind 64 sequences: 413 us,
+        // whole turns 400, half turns 380).
         const bool turns = w.cnt > kTurnTiles;
         int room = kFlushTiles - st * (kFlushTiles / 2);  // tiles until O starts again
         bool fresh = true, first_tile = true;
@@ -638,8 +642,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
           fresh = --room == 0;
           if (fresh) room = kFlushTiles;
         }
-        // turns of the other stream that this one has no tile to wait for: the last one of stream 1, for stream 0 and of
-        // stream 0 for a stream 1 with one tile less
+        // turns of the other stream that this one has no tile to wait for: the last one of stream 1, for stream 0
+        // and of stream 0 for a stream 1 with one tile less
         if (ok && turns && (st == 0 ? w.both || !(w.cnt & 1) : !w.both && (w.cnt & 1))) {
           if (!(ok = bar_wait(turn(st), t_phase, &gave_up))) break;
           t_phase ^= 1;
@@ -761,8 +765,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
           }
         }
         if (PV) {
-          // through shared memory, half a row at a time, so that it leaves in whole runs (one thread's row
-          // straight from its registers took 4 us a segment): over the other stream's rows when joining, else over the
+          // through shared memory, half a row at a time, so that it leaves in whole runs (one thread's row straight
+          // from its registers took 4 us a segment): over the other stream's rows when joining, else over the
           // stream's own queries, which no product reads any more
 #pragma unroll 1
           for (int c0 = 0; c0 < D; c0 += HC) {
@@ -900,9 +904,9 @@ cudaError_t launch_rows_tc(const RowsArgs& a, int d, cudaStream_t st) {
 void tc_plan(int64_t rows, int64_t mg, int64_t ld_own, RowsPlan* p) {
   p->rb_log = 8;
   p->kt_log = 7;
-  // queries, first loads and the write-out of a segment take about as long as four tiles of one stream's rows each, three of
-  // both (32K behind 16 sequences: 2 places 44 us, 4 places 39, 8 places 40; a 4,099-token prompt: 2 places 126, 3 places 120,
-  // 4 places 122)
+  // queries, first loads and the write-out of a segment take about as long as four tiles of one stream's rows each,
+  // three of both (32K behind 16 sequences: 2 places 44 us, 4 places 39, 8 places 40; a 4,099-token prompt: 2 places
+  // 126, 3 places 120, 4 places 122)
   p->extra = rows > 128 ? 3 : 4;
   p->pp = int((rows + kTcRows - 1) / kTcRows);
   p->po = ld_own > 0 ? int((mg + kTcRows - 1) / kTcRows) : 0;

@@ -18,8 +18,8 @@
 // the CTAs.  A segment inside one CTA is written out directly, one cut by
 // a CTA border leaves partial sums that weights_tc_join_kernel adds in CTA order.
 //
-// Roles: warps 0-15 the keys (warpgroup g: stream g & 1, columns 64 (g >> 1) on), warp 16 the loads (K pairs, row tiles),
-// warp 17 the products, warp 18 the row tiles' log-sum-exps.
+// Roles: warps 0-15 the keys (warpgroup g: stream g & 1, columns 64 (g >> 1) on), warp 16 the loads (K pairs, row
+// tiles), warp 17 the products, warp 18 the row tiles' log-sum-exps.
 #include <cstring>
 
 #include "zha_rows.cuh"
