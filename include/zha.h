@@ -317,7 +317,9 @@ ZHA_API int zha_prefix_decode(const zha_config* cfg, const void* K, const void* 
  *              of KV head h, j in [0, n); entries past n are left as they are.
  *              acc_out may be acc_in (with ld_acc_out == ld_acc_in); otherwise
  *              they must not overlap.
- * Every sum is taken in a fixed order: equal calls give equal bits.
+ * K and V must be finite for all n tokens.  Every sum is taken in a fixed order: equal
+ * calls give equal bits.  The workspace of calls with few rows (m * Hq / Hkv <= 16) holds
+ * their logits, 4 bytes per query row and token.
  * Scratch, stream and graphs as for zha_prefix_decode (n >= 1; m * Hq < 2^24).
  */
 ZHA_API size_t zha_weights_scratch_bytes(const zha_config* cfg, int32_t m, int64_t n);
