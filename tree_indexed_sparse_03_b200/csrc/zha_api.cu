@@ -31,6 +31,7 @@ cudaError_t dense_static_scratch(float** out);
 }  // namespace zha
 
 #include "zha_rows.cuh"
+#include "zha_tc.cuh"
 
 using namespace zha;
 
@@ -598,6 +599,15 @@ static uint64_t rows_bound_bytes(const zha_config* cfg, int64_t B, int64_t m, in
                                   ld_own) * uint64_t(cfg->d + 2) * 4);
 }
 
+// Bound of the waits of the tensor-core kernels in SM cycles.
+static long long wait_limit() {
+  if (const char* v = std::getenv("ZHA_WAIT_CYCLES")) {  // test hook: 0 makes a wait that is not over at once give up
+    const long long x = std::atoll(v);
+    if (x >= 0 && (x > 0 || v[0] == '0')) return x;
+  }
+  return kTcWaitCycles;
+}
+
 static void fill_rows(const zha_config* cfg, const RowsPlan& p, int32_t B, int32_t m, void* scratch, RowsArgs* a) {
   std::memset(a, 0, sizeof(*a));
   a->B = B;
@@ -615,6 +625,7 @@ static void fill_rows(const zha_config* cfg, const RowsPlan& p, int32_t B, int32
   a->nc = p.nc;
   a->part_own = int64_t(p.part_own);
   a->scale = 1.0f / std::sqrt(float(cfg->d));
+  a->wait_limit = wait_limit();
   a->status = static_cast<int*>(scratch);
   a->plan = reinterpret_cast<int*>(static_cast<char*>(scratch) + kScratchHead);
   a->part = reinterpret_cast<float*>(static_cast<char*>(scratch) + kScratchHead + rows_plan_bytes(cfg, B, m));
@@ -760,6 +771,7 @@ int zha_dense_weights(const zha_config* cfg, const void* K, const void* V, int64
   w.rsplit = wp.rsplit;
   w.rows_per_split = wp.rows_per_split;
   w.scale = a.scale;
+  w.wait_limit = a.wait_limit;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = launch_rows(a, cfg->dtype, cfg->d, st);
   if (e != cudaSuccess) return fail_cuda(e, "zha_dense_weights: attention");

@@ -53,6 +53,7 @@ struct RowsArgs {
   int rt;                   // rows of part_tmp per CTA
   int nc;                   // CTAs
   float scale;              // 1 / sqrt(d)
+  long long wait_limit;     // bound of the waits on copies and products, SM cycles
 };
 
 // Tokens of sequence b's own cache (a length outside [0, ld_own] is clamped, so that no read leaves the cache).
@@ -290,6 +291,7 @@ struct WeightsArgs {
   int m, hq, hkv, group, causal, rsplit;
   int64_t rows_per_split;  // rows of one split (a multiple of the kernel's row block)
   float scale;
+  long long wait_limit;  // bound of the waits on copies and products, SM cycles
 };
 
 // Host side: the plan of a call (kernel variant, CTAs, partial rows).

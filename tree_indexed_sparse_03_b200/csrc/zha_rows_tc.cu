@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
   __shared__ __align__(8) uint64_t bars[2 * NS + 25];
   __shared__ float2 x_ml[128];  // stream 1's sums for the join
   __shared__ uint32_t tmem_base;
-  __shared__ volatile int gave_up;
+  __shared__ Waits waits;
   const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
   const uint32_t ring = base + 2 * Sh::kQ;
   const uint32_t b0 = smem_u32(bars);
@@ -186,7 +186,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
       bar_init(x_may, 4);
       bar_init(turn(0), 4);
       bar_init(turn(1), 4);
-      gave_up = 0;
+      waits.gave_up = 0;
+      waits.limit = a.wait_limit;
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncwarp();
@@ -213,7 +214,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
       int pend_slot = -1, pend_row = 0;  // a V tile whose rows from pend_row on are still to be cleared
       auto clear_pending = [&]() {
         if (pend_slot < 0) return true;
-        if (!bar_wait(fix, fix_phase, &gave_up)) return false;
+        if (!bar_wait(fix, fix_phase, &waits)) return false;
         fix_phase ^= 1;
         const uint32_t dst = ring + pend_slot * Sh::kTile + pend_row * 128;
         const int per = (kTcKeys - pend_row) * 8;
@@ -246,8 +247,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
           // once the copy has landed; meanwhile the next copies start, as long as none has to wait.  Past the
           // prefix's end the tensor map ends, so the copy itself fills zeros.
           const bool clear = kv && w.s.own && k0 + kTcKeys > len;
-          if ((clear || !bar_done(empty(slot), (round & 1) ^ 1)) && !(ok = clear_pending())) break;
-          if (!(ok = bar_wait(empty(slot), (round & 1) ^ 1, &gave_up))) break;
+          if ((clear || !bar_look(empty(slot), (round & 1) ^ 1)) && !(ok = clear_pending())) break;
+          if (!(ok = bar_wait(empty(slot), (round & 1) ^ 1, &waits))) break;
           const uint32_t dst = ring + slot * Sh::kTile;
           const uint32_t bar = clear ? fix : full(slot);
           if (lane == 0) {
@@ -266,13 +267,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
         }
       }
       if (ok) clear_pending();
-      // copies in flight when a wait gave up: let them land before the CTA's shared memory goes away
-      if (gave_up) {
-        int never = 0;
-        for (int q = 0; q < NS; ++q) {
-          const uint32_t r = q < slot ? round : round - 1;  // the slot's last use
-          if (q < slot || round > 0) bar_wait(q == pend_slot ? fix : full(q), q == pend_slot ? fix_phase : r & 1, &never);
-        }
+      // no copy may be in flight when the CTA's shared memory goes away (other roles may give up after this one's end)
+      for (int q = 0; q < NS; ++q) {
+        const uint32_t r = q < slot ? round : round - 1;  // the slot's last use
+        if (q < slot || round > 0) bar_drain(q == pend_slot ? fix : full(q), q == pend_slot ? fix_phase : r & 1);
       }
     } else if (wid == 9 || wid == 10) {  // ---------------------------------------------------------------- products
       const int st = wid - 9;
@@ -286,7 +284,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
       bool ok = true;
       while (ok && next_work(a, tot, &x, x_end, &w)) {
         const int lag = w.both ? 1 : 2;
-        if (!(ok = bar_wait(q_full(st), q_phase, &gave_up))) break;
+        if (!(ok = bar_wait(q_full(st), q_phase, &waits))) break;
         q_phase ^= 1;
         if (!w.both && w.cnt == 1 && st == 1 && lane == 0) bar_arrive(o_full(1));  // no tile for stream 1: nothing to wait for
         int room = kFlushTiles - st * (kFlushTiles / 2);  // tiles until O starts again
@@ -295,9 +293,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
         for (int i = 0; i < w.cnt + lag && ok; ++i) {
           const bool mine = w.both || (i & 1) == st;
           if (i >= lag && PV) {
-            if (!(ok = bar_wait(full(slot), round & 1, &gave_up))) break;
+            if (!(ok = bar_wait(full(slot), round & 1, &waits))) break;
             if (mine) {
-              if (fresh && !first && !(ok = bar_wait(o_free(st), o_phase, &gave_up))) break;
+              if (fresh && !first && !(ok = bar_wait(o_free(st), o_phase, &waits))) break;
               if (fresh && !first) o_phase ^= 1;
               first = false;
               // the weights come in two halves of 64 keys: the products of the first run under the exponentials of
@@ -305,7 +303,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
               const uint32_t v = v_lo + slot * (Sh::kTile >> 4);
 #pragma unroll
               for (int half = 0; half < 2; ++half) {
-                if (!(ok = bar_wait(p_full(st, half), p_phase, &gave_up))) break;
+                if (!(ok = bar_wait(p_full(st, half), p_phase, &waits))) break;
                 tc_fence_after();
                 if (lane == 0) {
 #pragma unroll
@@ -336,9 +334,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
             }
           }
           if (i < w.cnt) {
-            if (!(ok = bar_wait(full(slot), round & 1, &gave_up))) break;
+            if (!(ok = bar_wait(full(slot), round & 1, &waits))) break;
             if (mine) {
-              if (!PV && !(ok = bar_wait(p_full(st, buf), (b_round & 1) ^ 1, &gave_up))) break;  // the buffer has been read
+              if (!PV && !(ok = bar_wait(p_full(st, buf), (b_round & 1) ^ 1, &waits))) break;  // the buffer has been read
               tc_fence_after();
               if (lane == 0) {
                 const uint32_t k = k_lo + slot * (Sh::kTile >> 4);
@@ -368,8 +366,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
       // nothing of the tensor pipe may be in flight when tensor memory is given back
       if (lane == 0) mma_commit(done);
       __syncwarp();
-      int never = 0;
-      bar_wait(done, 0, &never);
+      bar_drain(done, 0);
     } else if (wid == 11) {
       if (blockIdx.x == 0) rows_publish(a, tot);
     } else if (PV) {  // ---------------------------------------------------------------- O to global memory
@@ -385,7 +382,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
         for (int f = 0; f * (kFlushTiles / 2) + kFlushTiles / 2 < max(n0, n1) && ok; ++f) {
           const int st = (f & 1) ^ 1;
           if ((f + 1) * (kFlushTiles / 2) >= (st ? n1 : n0)) continue;  // the stream ends before
-          if (!(ok = bar_wait(o_chunk(st), phase[st], &gave_up))) break;
+          if (!(ok = bar_wait(o_chunk(st), phase[st], &waits))) break;
           phase[st] ^= 1;
           tc_fence_after();
           const int nrows = min(128, w.seg_rows - w.s.p * kTcRows - (w.both ? st * 128 : 0));
@@ -502,16 +499,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
 #pragma unroll 1
         for (int i = i0; i < w.cnt; i += step) {
           if (turns && (st || i != i0)) {
-            if (!(ok = bar_wait(turn(st), t_phase, &gave_up))) break;
+            if (!(ok = bar_wait(turn(st), t_phase, &waits))) break;
             t_phase ^= 1;
           }
-          if (!(ok = bar_wait(s_full(st), s_phase, &gave_up))) break;
+          if (!(ok = bar_wait(s_full(st), s_phase, &waits))) break;
           s_phase ^= 1;
           tc_fence_after();
           if (fresh && !first_tile) pending = flushed = true;  // O is being added to global memory
           // before this tile's weights can complete O and have it added again, every warp has seen the time before
           if (pending && room == 1) {
-            if (!(ok = bar_wait(flush_done(st), f_phase, &gave_up))) break;
+            if (!(ok = bar_wait(flush_done(st), f_phase, &waits))) break;
             f_phase ^= 1;
             pending = false;
           }
@@ -546,7 +543,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
               const float sc = m_ref == -INFINITY ? 0.f : ex2(m_ref - up);
               if (flushed) {  // what has left O already
                 if (pending) {
-                  if (!(ok = bar_wait(flush_done(st), f_phase, &gave_up))) break;
+                  if (!(ok = bar_wait(flush_done(st), f_phase, &waits))) {
+                    tmem_wait32(va);  // the load above must not outlive the loop
+                    break;
+                  }
                   f_phase ^= 1;
                   pending = false;
                 }
@@ -645,13 +645,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
         // turns of the other stream that this one has no tile to wait for: the last one of stream 1, for stream 0
         // and of stream 0 for a stream 1 with one tile less
         if (ok && turns && (st == 0 ? w.both || !(w.cnt & 1) : !w.both && (w.cnt & 1))) {
-          if (!(ok = bar_wait(turn(st), t_phase, &gave_up))) break;
+          if (!(ok = bar_wait(turn(st), t_phase, &waits))) break;
           t_phase ^= 1;
         }
       } else {
 #pragma unroll 1
         for (int i = i0; i < w.cnt; i += step) {  // only the sums
-          if (!(ok = bar_wait(s_full(st, buf), s_phase, &gave_up))) break;
+          if (!(ok = bar_wait(s_full(st, buf), s_phase, &waits))) break;
           tc_fence_after();
           if (active) {
             const int left = lim - (w.t0 + i) * kTcKeys;  // keys of the tile that the row sees
@@ -703,14 +703,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
       }
       if (!ok) break;
       if (PV || i0 >= w.cnt) {  // also without work: the stream stays within one segment of its products' warp
-        if (!(ok = bar_wait(o_full(st), o_phase, &gave_up))) break;
+        if (!(ok = bar_wait(o_full(st), o_phase, &waits))) break;
         o_phase ^= 1;
         tc_fence_after();
       }
       // streams that shared the rows: stream 1 leaves its sums and rows where the queries lay, stream 0 joins them
       const bool join = !w.both && w.cnt > 1;
       if (pending) {
-        if (!(ok = bar_wait(flush_done(st), f_phase, &gave_up))) break;
+        if (!(ok = bar_wait(flush_done(st), f_phase, &waits))) break;
         f_phase ^= 1;
       }
       const bool added = flushed;
@@ -718,7 +718,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
       float other_l = 0.f, mine_s = 1.f, other_s = 0.f;
       if (join) {
         if (st == 1) {
-          if (!(ok = bar_wait(x_may, x_phase, &gave_up))) break;  // stream 0's products still read its queries
+          if (!(ok = bar_wait(x_may, x_phase, &waits))) break;  // stream 0's products still read its queries
           if (active) {
             if (PV) {
 #pragma unroll 1
@@ -739,7 +739,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
         } else {
           __syncwarp();
           if (lane == 0) bar_arrive(x_may);
-          if (!(ok = bar_wait(x_full, x_phase, &gave_up))) break;
+          if (!(ok = bar_wait(x_full, x_phase, &waits))) break;
           if (active) {
             const float2 ml = x_ml[row];
             const bool none = ml.x == -INFINITY && ml.y == 0.f;
@@ -824,7 +824,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
           __syncwarp();
           if (lane == 0) bar_arrive(x_free);
         }
-        if (!(ok = bar_wait(x_free, x_phase, &gave_up))) break;
+        if (!(ok = bar_wait(x_free, x_phase, &waits))) break;
         x_phase ^= 1;
       }
       tc_fence_before();
@@ -832,7 +832,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(RowsArgs a, cons
   }
   tc_fence_before();
   __syncthreads();
-  if (gave_up && tid == 0) raise_status(a.status, ZHA_ERR_TIMEOUT);
+  if (waits.gave_up && tid == 0) raise_status(a.status, ZHA_ERR_TIMEOUT);
   if (wid == 11) tmem_free(tm, 512);
 }
 

@@ -30,22 +30,6 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-// Bounded wait: about four seconds of SM cycles.  `gave_up` is shared by the CTA: once any wait runs out, every
-// other wait returns false at its next look, so that all roles leave their loops.
-constexpr long long kTcWaitCycles = 1ll << 33;
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
-  if (bar_try(bar, parity)) return true;
-  const long long t0 = clock64();
-  while (!bar_try(bar, parity)) {
-    if (*gave_up) return false;
-    if (clock64() - t0 > kTcWaitCycles) {
-      *gave_up = 1;
-      return false;
-    }
-  }
-  return true;
-}
-
 // Without waiting longer than one look.
 __device__ __forceinline__ bool bar_done(uint32_t bar, uint32_t parity) {
   uint32_t ok;
@@ -55,6 +39,46 @@ __device__ __forceinline__ bool bar_done(uint32_t bar, uint32_t parity) {
       : "r"(bar), "r"(parity)
       : "memory");
   return ok != 0;
+}
+
+// What the waits of a CTA share, in its shared memory: once any wait runs out, every other one returns false at its
+// next look, so that all roles leave their loops.
+struct Waits {
+  volatile int gave_up;
+  long long limit;  // SM cycles
+};
+constexpr long long kTcWaitCycles = 1ll << 33;  // about four seconds
+
+// Bounded wait by a full warp.  Every lane looks (what the phase published is then visible to each), the answer is the
+// warp's: lanes could otherwise see a phase, or the limit, at different looks and leave for different code, where
+// the warp-wide instructions would wait for each other without end.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, Waits* w) {
+  bool seen = bar_done(bar, parity);
+  if (__all_sync(0xffffffffu, seen)) return true;
+  const long long t0 = clock64(), limit = w->limit;
+  while (true) {
+    if (__any_sync(0xffffffffu, w->gave_up || clock64() - t0 >= limit)) {
+      w->gave_up = 1;
+      return false;
+    }
+    seen = seen || bar_try(bar, parity);
+    if (__all_sync(0xffffffffu, seen)) return true;
+  }
+}
+
+// One look by a full warp, one answer.
+__device__ __forceinline__ bool bar_look(uint32_t bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, bar_done(bar, parity));
+}
+
+// A full warp's wait for its own asynchronous work before it leaves, with a limit of its own: copies and products in
+// flight must not outlive the CTA's shared and tensor memory, whatever made the CTA leave.
+__device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity) {
+  const long long t0 = clock64();
+  bool seen = false;
+  do {
+    seen = seen || bar_try(bar, parity);
+  } while (!__all_sync(0xffffffffu, seen) && !__any_sync(0xffffffffu, clock64() - t0 > kTcWaitCycles));
 }
 
 // ---------------------------------------------------------------- TMA

@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
   __shared__ float other[2][2][128];  // [segment parity][stream]: sums of the stream's second warpgroup
   __shared__ __align__(16) float minus_lse[NL][kWtCols];  // in powers of two; -inf where a tile has no row
   __shared__ uint32_t tmem_base;
-  __shared__ volatile int gave_up;
+  __shared__ Waits waits;
   const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
   const uint32_t k_sm = base, ring = base + 4 * Sh::kHalf;  // K: [pair slot][stream]
   const uint32_t b0 = smem_u32(bars);
@@ -166,7 +166,8 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
       }
     }
     bar_init(done, 1);
-    gave_up = 0;
+    waits.gave_up = 0;
+    waits.limit = a.wait_limit;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   // rows of a tile that no copy writes (heads that do not divide 128) stay zero
@@ -193,7 +194,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
     while (x < x_end && ok) {
       const WtSeg s = wt_find(a, plan, x);
       const int t1 = min(s.first + s.tiles, x_end) - s.first;
-      if (!(ok = bar_wait(k_empty(ks), (k_round & 1) ^ 1, &gave_up))) break;
+      if (!(ok = bar_wait(k_empty(ks), (k_round & 1) ^ 1, &waits))) break;
       if (lane == 0) {
         bar_expect(k_full(ks), 2 * Sh::kHalf);
 #pragma unroll
@@ -209,7 +210,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
       }
       for (int t = x - s.first; t < t1; ++t) {
         const WtTile w = wt_tile(a, plan, s.t_first + t);
-        if (!(ok = bar_wait(empty(slot), (round & 1) ^ 1, &gave_up))) break;
+        if (!(ok = bar_wait(empty(slot), (round & 1) ^ 1, &waits))) break;
         if (lane == 0) {
           bar_expect(full(slot), tile_bytes);
 #pragma unroll
@@ -224,13 +225,11 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
       }
       x = s.first + t1;
     }
-    if (gave_up) {  // copies in flight land before the CTA's shared memory goes away
-      int never = 0;
-      for (int q = 0; q < NS; ++q)
-        if (q < slot || round > 0) bar_wait(full(q), (q < slot ? round : round - 1) & 1, &never);
-      for (int q = 0; q < 2; ++q)
-        if (q < ks || k_round > 0) bar_wait(k_full(q), (q < ks ? k_round : k_round - 1) & 1, &never);
-    }
+    // no copy may be in flight when the CTA's shared memory goes away (other roles may give up after this one's end)
+    for (int q = 0; q < NS; ++q)
+      if (q < slot || round > 0) bar_drain(full(q), (q < slot ? round : round - 1) & 1);
+    for (int q = 0; q < 2; ++q)
+      if (q < ks || k_round > 0) bar_drain(k_full(q), (q < ks ? k_round : k_round - 1) & 1);
   } else if (wid == 18) {  // ---------------------------------------------------------------- log-sum-exps
     int slot = 0;
     uint32_t round = 0;
@@ -246,7 +245,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
           const int c = lane + 32 * q, i = c / w.gw;
           v[q] = c < w.cols ? a.lse[int64_t(w.tok0 + i) * a.hq + s.h * a.group + w.g0 + (c - i * w.gw)] : INFINITY;
         }
-        if (!(ok = bar_wait(l_empty(slot), (round & 1) ^ 1, &gave_up))) break;
+        if (!(ok = bar_wait(l_empty(slot), (round & 1) ^ 1, &waits))) break;
 #pragma unroll
         for (int q = 0; q < kWtCols / 32; ++q) minus_lse[slot][lane + 32 * q] = v[q] * -1.4426950408889634f;
         __syncwarp();
@@ -265,13 +264,13 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
     while (x < x_end && ok) {
       const WtSeg s = wt_find(a, plan, x);
       const int t1 = min(s.first + s.tiles, x_end) - s.first;
-      ok = bar_wait(k_full(ks), k_round & 1, &gave_up);
+      ok = bar_wait(k_full(ks), k_round & 1, &waits);
       for (int t = x - s.first; t < t1 && ok; ++t) {
         const WtTile w = wt_tile(a, plan, s.t_first + t);
         const uint32_t idesc = mma_idesc((w.cols + 15) / 16 * 16, false);
-        ok = bar_wait(full(slot), round & 1, &gave_up);
+        ok = bar_wait(full(slot), round & 1, &waits);
         for (int st = 0; st < 2 && ok; ++st) {
-          if (!(ok = bar_wait(s_free(st, buf), (b_round & 1) ^ 1, &gave_up))) break;
+          if (!(ok = bar_wait(s_free(st, buf), (b_round & 1) ^ 1, &waits))) break;
           tc_fence_after();
           if (lane == 0) {
             const uint32_t k = desc_low(k_sm + (2 * ks + st) * Sh::kHalf, 16), q = desc_low(ring + slot * Sh::kHalf, 16);
@@ -303,10 +302,10 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
       }
       x = s.first + t1;
     }
-    int never = 0;  // nothing of the tensor pipe may be in flight when tensor memory is given back
+    // nothing of the tensor pipe may be in flight when tensor memory is given back
     if (lane == 0) mma_commit(done);
     __syncwarp();
-    bar_wait(done, 0, &never);
+    bar_drain(done, 0);
   } else {  // ---------------------------------------------------------------- the streams' keys
     const int st = (wid >> 2) & 1, mine = wid >> 3, key = tid & 127;
     const uint32_t lane_base = uint32_t((wid & 3) * 32) << 16;
@@ -324,8 +323,8 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
       uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
       for (int t = x - s.first; t < t1; ++t) {
         const WtTile w = wt_tile(a, plan, s.t_first + t);
-        if (!(ok = bar_wait(l_full(slot), round & 1, &gave_up))) break;
-        if (!(ok = bar_wait(s_full(st, buf), b_round & 1, &gave_up))) break;
+        if (!(ok = bar_wait(l_full(slot), round & 1, &waits))) break;
+        if (!(ok = bar_wait(s_full(st, buf), b_round & 1, &waits))) break;
         tc_fence_after();
         const int64_t hid = (tok_min - w.tok0) * w.gw;  // columns before this one do not see the key
         const int c_min = hid < 0 ? 0 : (hid > kWtCols ? kWtCols : int(hid));
@@ -372,12 +371,12 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
       const uint32_t use = uint32_t(seg_no >> 1) & 1;  // the parity's pair of barriers serves every other segment
       ++seg_no;
       if (mine == 1) {
-        if (!(ok = bar_wait(x_free(par, st), use ^ 1, &gave_up))) break;
+        if (!(ok = bar_wait(x_free(par, st), use ^ 1, &waits))) break;
         other[par][st][key] = total;
         __syncwarp();
         if (lane == 0) bar_arrive(x_full(par, st));
       } else {
-        if (!(ok = bar_wait(x_full(par, st), use, &gave_up))) break;
+        if (!(ok = bar_wait(x_full(par, st), use, &waits))) break;
         total += other[par][st][key];
         __syncwarp();
         if (lane == 0) bar_arrive(x_free(par, st));
@@ -392,7 +391,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_tc_kernel(WeightsArgs a
   }
   tc_fence_before();
   __syncthreads();
-  if (gave_up && tid == 0) raise_status(a.status, ZHA_ERR_TIMEOUT);
+  if (waits.gave_up && tid == 0) raise_status(a.status, ZHA_ERR_TIMEOUT);
   if (wid == 17) tmem_free(tm, 512);
 }
 
