@@ -318,7 +318,9 @@ ZHA_API int zha_prefix_decode(const zha_config* cfg, const void* K, const void* 
  *              acc_out may be acc_in (with ld_acc_out == ld_acc_in); otherwise
  *              they must not overlap.
  * K and V must be finite for all n tokens.  Every sum is taken in a fixed order: equal
- * calls give equal bits.  The workspace of calls with few rows (m * Hq / Hkv <= 16) holds
+ * calls give equal bits.  When a wait of the call runs out (see zha_scratch_status) its outputs
+ * are undefined, but sums in place are as they were, also after later calls until the
+ * status has been looked at.  The workspace of calls with few rows (m * Hq / Hkv <= 16) holds
  * their logits, 4 bytes per query row and token.
  * Scratch, stream and graphs as for zha_prefix_decode (n >= 1; m * Hq < 2^24).
  */

@@ -80,3 +80,37 @@ def test_weights_waits_that_run_out(monkeypatch, d, outputs, hkv, group, m, n):
         torch.cuda.synchronize()
         dec.status()
         assert torch.equal(got[1], want[1]) and (not outputs or torch.equal(got[0], want[0]))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("outputs", [True, False])
+@pytest.mark.parametrize("hkv,group,m,n", [(2, 4, 1, 900), (2, 4, 33, 901), (1, 8, 300, 3000), (2, 150, 5, 700)])
+def test_sums_in_place_survive_a_wait_that_runs_out(monkeypatch, d, outputs, hkv, group, m, n):
+    """Running sums that a call adds to in place are all as they were when one of its waits ran out, and stay so until
+    the status has been looked at; all complete otherwise."""
+    K, V, Q = rnd(1, hkv, n, d), rnd(2, hkv, n, d), rnd(3, m, hkv * group, d, scale=2.0)
+    before = torch.rand(hkv, n + 3, generator=torch.Generator(device="cuda").manual_seed(4), device="cuda")
+    dec = z.DenseWeights(cfg_of(d, hkv, group), m, n)
+    after = before.clone()
+    after[:, :n] = dec(K, V if outputs else None, n, Q, before, causal=True)[1]
+    for bound in BOUNDS:
+        acc = before.clone()
+
+        def call():
+            dec(K, V if outputs else None, n, Q, acc, causal=True, acc_out=acc)
+
+        monkeypatch.setenv("ZHA_WAIT_CYCLES", str(bound))
+        call()
+        monkeypatch.delenv("ZHA_WAIT_CYCLES")
+        if bound == 0:
+            call()  # nobody has looked
+        torch.cuda.synchronize()
+        try:
+            dec.status()
+            assert bound > 0 and torch.equal(acc, after)
+        except z.ZhaError as e:
+            assert e.code == zb.ZHA_ERR_TIMEOUT and torch.equal(acc, before)
+            call()
+            torch.cuda.synchronize()
+            dec.status()
+            assert torch.equal(acc, after)

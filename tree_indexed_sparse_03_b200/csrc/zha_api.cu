@@ -757,7 +757,7 @@ int zha_dense_weights(const zha_config* cfg, const void* K, const void* V, int64
   w.acc_in = acc_in;
   w.acc_out = acc_out;
   w.sums = reinterpret_cast<float*>(static_cast<char*>(scratch) + sums_off);
-  w.status = a.status;
+  w.status = cfg->dtype == ZHA_BF16 ? a.status : nullptr;
   w.ld = ld;
   w.n = n;
   w.ld_acc_in = ld_acc_in;

@@ -456,12 +456,13 @@ __global__ void __launch_bounds__(256) weights_logits_kernel(WeightsArgs a) {
   const int h = blockIdx.y;
   const int64_t k = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4;
   pdl_wait();
+  const bool failed = a.status && __ldcg(a.status) != 0;  // a wait ran out: the logits may not be these queries'
   if (threadIdx.x < a.rows) {
     const int t = threadIdx.x / a.group;
     lse2[threadIdx.x] = a.lse[int64_t(t) * a.hq + h * a.group + (threadIdx.x - t * a.group)] * 1.4426950408889634f;
   }
   __syncthreads();
-  if (k >= a.n) return;
+  if (k >= a.n || failed) return;
   const float* lg = a.logits + int64_t(h) * a.rows * a.ld_logits + k;
   float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
@@ -475,6 +476,20 @@ __global__ void __launch_bounds__(256) weights_logits_kernel(WeightsArgs a) {
 #pragma unroll
   for (int e = 0; e < 4; ++e)
     if (k + e < a.n) a.acc_out[h * a.ld_acc_out + k + e] = (a.acc_in ? a.acc_in[h * a.ld_acc_in + k + e] : 0.f) + s[e];
+}
+
+// Sums in place, last: acc_out = the staged sums, unless a wait of the tensor-core kernels before has run out (some CTAs
+// may then have left without theirs).
+__global__ void __launch_bounds__(256) weights_commit_kernel(WeightsArgs a, float* acc_out, int64_t ld_acc_out) {
+  const int h = blockIdx.y;
+  const int64_t k0 = int64_t(blockIdx.x) * 1024 + threadIdx.x;
+  pdl_wait();
+  if (__ldcg(a.status) != 0) return;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int64_t k = k0 + 256 * e;
+    if (k < a.n) acc_out[h * ld_acc_out + k] = __ldcg(a.acc_out + h * a.ld_acc_out + k);
+  }
 }
 
 // ------------------------------------------------------------------ host side
@@ -607,7 +622,7 @@ void weights_plan(int dtype, int d, int hkv, int64_t rows, int64_t n, WeightsPla
   if (dtype == ZHA_BF16) {
     p->rsplit = 1;
     p->rows_per_split = rows;
-    p->sum_floats = weights_tc_floats();
+    p->sum_floats = weights_tc_floats() + uint64_t(hkv) * uint64_t(n);  // and the sums in place until they are complete
     p->places = double(hkv) * double((n + 255) / 256) * double(rows / 64 + 1);  // 64 rows per tile at least
     return;
   }
@@ -625,7 +640,7 @@ void weights_plan(int dtype, int d, int hkv, int64_t rows, int64_t n, WeightsPla
 // Floats of column sums that cover every call with at most n tokens: the splits of n' <= n tokens take
 // ceil(kWeightsCtas / ctas) * hkv * n' <= 64 * kWeightsCtas + hkv * n floats.
 uint64_t weights_sums_bound(int dtype, int hkv, int64_t n) {
-  return dtype == ZHA_BF16 ? weights_tc_floats() : uint64_t(kWeightsCtas) * kRowsKeys + uint64_t(hkv) * n;
+  return (dtype == ZHA_BF16 ? weights_tc_floats() : uint64_t(kWeightsCtas) * kRowsKeys) + uint64_t(hkv) * uint64_t(n);
 }
 
 cudaError_t launch_weights(const WeightsArgs& a, int dtype, int d, cudaStream_t st) {
@@ -633,7 +648,18 @@ cudaError_t launch_weights(const WeightsArgs& a, int dtype, int d, cudaStream_t 
     count_launches(1);
     return launch_after(weights_logits_kernel, dim3(unsigned((a.n + 1023) / 1024), unsigned(a.hkv)), 256, 0, st, a);
   }
-  if (dtype == ZHA_BF16) return launch_weights_tc(a, d, st);
+  if (dtype == ZHA_BF16) {
+    if (a.acc_in != a.acc_out) return launch_weights_tc(a, d, st);
+    // in place: the kernels add up behind the partial sums, and nothing of the caller's changes before all have ended
+    WeightsArgs b = a;
+    b.acc_out = a.sums + weights_tc_floats();
+    b.ld_acc_out = a.n;
+    const cudaError_t e = launch_weights_tc(b, d, st);
+    if (e != cudaSuccess) return e;
+    count_launches(1);
+    return launch_after(weights_commit_kernel, dim3(unsigned((a.n + 1023) / 1024), unsigned(a.hkv)), 256, 0, st, b, a.acc_out,
+                        a.ld_acc_out);
+  }
   count_launches(a.rsplit > 1 ? 2 : 1);
   const cudaError_t e = d == 128 ? run_weights_rt<float, 128>(a, st) : run_weights_rt<float, 64>(a, st);
   if (e != cudaSuccess || a.rsplit <= 1) return e;

@@ -282,10 +282,11 @@ struct WeightsArgs {
   const float* lse;      // [m][hq]
   const float* acc_in;   // NULL: zeros
   float* acc_out;        // [hkv][ld_acc_out]
-  float* sums;           // partial column sums: [rsplit][hkv][n] (rsplit > 1), tensor cores: [CTA][2][256]
+  float* sums;           // partial column sums: [rsplit][hkv][n] (rsplit > 1), tensor cores: [CTA][2][256], then [hkv][n]
+                         // for sums in place
   const float* logits;   // [hkv][rows][ld_logits] as the attention left them (NULL: computed again)
   int64_t ld_logits;
-  int* status;
+  int* status;           // NULL: no kernel of the call waits (fp32)
   int64_t ld, n, ld_acc_in, ld_acc_out;
   int rows;              // m * group
   int m, hq, hkv, group, causal, rsplit;
