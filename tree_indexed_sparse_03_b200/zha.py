@@ -272,6 +272,7 @@ class ZhaTree:
             _refuse_device("the cache and acc")
         idx = _empty(acc, (c.n_kv_heads, keep), torch.int32, stream)
         work, nbytes = _evict_scratch(c, acc, n, stream)
+        _record(stream, dev, acc, self.K, self.V, self.refs, self.nodes, self.scratch)
         _check(lib().zha_tree_evict(self._h, acc.data_ptr(), ld_acc, keep, first, last, idx.data_ptr(), _ptr(work), nbytes,
                                     _stream(stream)))
         return idx
@@ -353,8 +354,9 @@ def dense_decode(cfg: ZhaConfig, K: torch.Tensor, V: torch.Tensor, n: int, Q: to
 
 # ---------------------------------------------------------------- shared prefix, weights, eviction
 # These entry points take tensors as they lie (row strides included) and never copy them; every tensor must be on
-# the current CUDA device.  Outputs they allocate belong to the stream the call runs on.  A short call takes the GPU
-# about ten microseconds, so the checks read each tensor's attributes once.
+# the current CUDA device.  Outputs they allocate belong to the stream the call runs on; what else a call on another
+# stream than the current one uses is recorded there, so that it may be dropped before that stream is done.  A short
+# call takes the GPU about ten microseconds, so the checks read each tensor's attributes once.
 
 _F32 = torch.float32
 
@@ -368,6 +370,15 @@ def _empty(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
         return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
         return like.new_empty(shape, dtype=dtype)
+
+
+def _record(stream, dev: int, *tensors) -> None:
+    """The memory of tensors that a call on `stream` uses is not handed out again before the call is done."""
+    if stream is None or stream.cuda_stream == torch._C._cuda_getCurrentRawStream(dev):
+        return
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
 
 
 def _refuse_device(name: str):
@@ -432,6 +443,14 @@ class _Attend:
         self.scratch = _new_scratch(nbytes, device)
         self._device = self.scratch.get_device()
         self._scratch = (self.scratch.data_ptr(), self.scratch.numel())
+        self._home = torch.cuda.current_stream(self.scratch.device).cuda_stream  # the stream its memory belongs to
+
+    def _on(self, stream) -> int:
+        """The raw stream of a call; the workspace lives until the call is done, whatever stream that is."""
+        raw = _raw_stream(stream, self._device)
+        if raw != self._home:
+            self.scratch.record_stream(stream if stream is not None else torch.cuda.current_stream())
+        return raw
 
     def _check_q(self, Q: torch.Tensor, dims, lead: str):
         c = self.cfg
@@ -511,8 +530,10 @@ class PrefixDecoder(_Attend):
                 _refuse_device("out")
         lse = _empty(Q, shape[:-1], _F32, stream) if want_lse else None
         if B and m:
+            raw = self._on(stream)
+            _record(stream, dev, Q, K, V, K_own, V_own, own_len, out)
             rc = lib().zha_prefix_decode(self._cfg, k, v, ld, n, ko, vo, ld_own, ln, Q.data_ptr(), out.data_ptr(),
-                                         _ptr(lse), B, m, *self._scratch, _raw_stream(stream, dev))
+                                         _ptr(lse), B, m, *self._scratch, raw)
             if rc:
                 _check(rc)
         return (out, lse) if want_lse else out
@@ -523,10 +544,7 @@ def prefix_decode(cfg: ZhaConfig, K, V, n: int, Q: torch.Tensor, K_own=None, V_o
     """One call of a PrefixDecoder made for it."""
     dec = PrefixDecoder(cfg, max(1, Q.shape[0]), n, 0 if K_own is None else K_own.shape[-2],
                         max(1, Q.shape[1]) if Q.dim() == 4 else 1, device=Q.device)
-    res = dec(K, V, n, Q, K_own, V_own, own_len, want_lse=want_lse, stream=stream)
-    if stream is not None:
-        dec.scratch.record_stream(stream)
-    return res
+    return dec(K, V, n, Q, K_own, V_own, own_len, want_lse=want_lse, stream=stream)
 
 
 class DenseWeights(_Attend):
@@ -579,8 +597,10 @@ class DenseWeights(_Attend):
             ld_out = _sums_ld("acc_out", acc_out, hkv, n)
             if acc_out.get_device() != dev:
                 _refuse_device("acc_out")
+        raw = self._on(stream)
+        _record(stream, dev, Q, K, V, acc, acc_out, out)
         rc = lib().zha_dense_weights(self._cfg, K.data_ptr(), v, ld, n, Q.data_ptr(), o, m, 1 if causal else 0, a, ld_in,
-                                     acc_out.data_ptr(), ld_out, *self._scratch, _raw_stream(stream, dev))
+                                     acc_out.data_ptr(), ld_out, *self._scratch, raw)
         if rc:
             _check(rc)
         return out, acc_out
@@ -629,6 +649,7 @@ def cache_evict(cfg: ZhaConfig, K: torch.Tensor, V: torch.Tensor, n: int, acc: t
             _refuse_device("acc_out")
     idx = _empty(acc, (hkv, keep), torch.int32, stream)
     work, nbytes = _evict_scratch(cfg, acc, n, stream)
+    _record(stream, dev, K, V, acc, K_out, V_out, acc_out)
     rc = lib().zha_cache_evict(ctypes.byref(cfg), K.data_ptr(), V.data_ptr(), ld, n, acc.data_ptr(), ld_acc, keep, first,
                                last, K_out.data_ptr(), V_out.data_ptr(), ld_out, acc_out.data_ptr(), ld_acc_out,
                                idx.data_ptr(), _ptr(work), nbytes, _raw_stream(stream, dev))
