@@ -401,6 +401,9 @@ ZHA_API uint64_t zha_launch_count(void);
 /* Message for the last failing call on this thread ("" if none). */
 ZHA_API const char* zha_last_error(void);
 
+/* Its code (ZHA_OK if none): why a size function that answers 0 refused the request. */
+ZHA_API int zha_last_error_code(void);
+
 #ifdef __cplusplus
 }
 #endif

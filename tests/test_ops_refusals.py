@@ -173,3 +173,22 @@ def test_workspaces_cover_smaller_calls(L, d, hq, hkv, dtype):
         assert s > 256
         for k in ((ms[max(0, ms.index(m) - 1)], n), (m, ns[max(0, ns.index(n) - 1)])):
             assert size[k] <= s, (k, (m, n))
+
+
+def test_workspace_requests_that_are_refused_keep_their_code(L):
+    """The size functions answer 0 for a request that no call would take; the classes raise what the call would return."""
+    with pytest.raises(z.ZhaError) as e:
+        z.PrefixDecoder(cfg(), 1 << 20, 100)
+    assert e.value.code == zb.ZHA_ERR_UNSUPPORTED and "2^24" in str(e.value)
+    with pytest.raises(z.ZhaError) as e:
+        z.DenseWeights(cfg(d=96), 1, 100)
+    assert e.value.code == zb.ZHA_ERR_UNSUPPORTED and "head dim" in str(e.value)
+    with pytest.raises(z.ZhaError) as e:
+        z.PrefixDecoder(cfg(), 0, 100)
+    assert e.value.code == zb.ZHA_ERR_INVALID
+    with pytest.raises(z.ZhaError) as e:
+        z.DenseWeights(cfg(), 1, 0)
+    assert e.value.code == zb.ZHA_ERR_INVALID
+    assert L.zha_last_error_code() == zb.ZHA_ERR_INVALID
+    assert evict(L, nbytes=0, n=50000, ld=50000, ld_acc=50000, acc=P + (1 << 30), K_out=P + (2 << 30), V=P + (3 << 30),
+                 V_out=P + (4 << 30)) == L.zha_last_error_code() == zb.ZHA_ERR_CAPACITY

@@ -42,15 +42,16 @@ void zha::count_launches(int n) { g_launches.fetch_add(uint64_t(n), std::memory_
 namespace {
 
 thread_local std::string g_err;
+thread_local int g_code = ZHA_OK;
 
 int fail(int code, const char* msg) {
   g_err = msg;
-  return code;
+  return g_code = code;
 }
 
 int fail_cuda(cudaError_t e, const char* where) {
   g_err = std::string(where) + ": " + cudaGetErrorString(e);
-  return ZHA_ERR_CUDA;
+  return g_code = ZHA_ERR_CUDA;
 }
 
 struct Layout {
@@ -189,6 +190,8 @@ struct zha_tree {
 extern "C" {
 
 const char* zha_last_error(void) { return g_err.c_str(); }
+
+int zha_last_error_code(void) { return g_code; }
 
 uint64_t zha_launch_count(void) { return g_launches.load(std::memory_order_relaxed); }
 

@@ -68,6 +68,7 @@ _SIGS = {
     "zha_tree_set_step_p": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_int32]),
     "zha_tree_destroy": (None, [_c.c_void_p]),
     "zha_last_error": (_c.c_char_p, []),
+    "zha_last_error_code": (_c.c_int, []),
     "zha_launch_count": (_c.c_uint64, []),
 }
 
@@ -427,7 +428,7 @@ def _check_out(name: str, t: torch.Tensor, shape) -> None:
 
 def _new_scratch(nbytes: int, device) -> torch.Tensor:
     if nbytes == 0:
-        raise ZhaError(ZHA_ERR_INVALID, lib().zha_last_error().decode())
+        _check(lib().zha_last_error_code())
     scratch = torch.zeros(nbytes, dtype=torch.uint8, device=device)
     torch.cuda.current_stream(scratch.device).synchronize()  # cleared before any stream uses it
     return scratch
