@@ -143,3 +143,21 @@ def test_tree_dropped_while_its_eviction_runs():
     assert not s.query()
     s.synchronize()
     assert torch.equal(idx, want) and keep
+
+
+def test_workspaces_are_not_made_inside_a_capture():
+    """Refused before anything reaches the stream: the capture goes on and its graph replays."""
+    K, V, Q = rnd(1, HKV, N, D), rnd(2, HKV, N, D), rnd(3, B, 1, HKV * G, D, scale=2.0)
+    dec = z.PrefixDecoder(cfg_of(), B, N)
+    want = dec(K, V, N, Q)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        with pytest.raises(ValueError):
+            z.prefix_decode(cfg_of(), K, V, N, Q)
+        with pytest.raises(ValueError):
+            z.DenseWeights(cfg_of(), 30, N)
+        o = dec(K, V, N, Q)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, want)

@@ -429,6 +429,8 @@ def _check_out(name: str, t: torch.Tensor, shape) -> None:
 def _new_scratch(nbytes: int, device) -> torch.Tensor:
     if nbytes == 0:
         _check(lib().zha_last_error_code())
+    if torch.cuda.is_current_stream_capturing():
+        raise ValueError("a workspace cannot be made while the stream is captured into a graph: make it before, call it inside")
     scratch = torch.zeros(nbytes, dtype=torch.uint8, device=device)
     torch.cuda.current_stream(scratch.device).synchronize()  # cleared before any stream uses it
     return scratch
@@ -542,7 +544,8 @@ class PrefixDecoder(_Attend):
 
 def prefix_decode(cfg: ZhaConfig, K, V, n: int, Q: torch.Tensor, K_own=None, V_own=None, own_len=None, *,
                   want_lse: bool = False, stream=None):
-    """One call of a PrefixDecoder made for it."""
+    """One call of a PrefixDecoder made for it.  Making its workspace waits for the current stream: loops and graph
+    captures (where it is refused) make a PrefixDecoder once."""
     dec = PrefixDecoder(cfg, max(1, Q.shape[0]), n, 0 if K_own is None else K_own.shape[-2],
                         max(1, Q.shape[1]) if Q.dim() == 4 else 1, device=Q.device)
     return dec(K, V, n, Q, K_own, V_own, own_len, want_lse=want_lse, stream=stream)
