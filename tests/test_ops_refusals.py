@@ -2,6 +2,8 @@
 error code before any device work, and the sizes of the workspaces cover every smaller call."""
 import ctypes
 import itertools
+import math
+import random
 
 import pytest
 import torch
@@ -192,3 +194,40 @@ def test_workspace_requests_that_are_refused_keep_their_code(L):
     assert L.zha_last_error_code() == zb.ZHA_ERR_INVALID
     assert evict(L, nbytes=0, n=50000, ld=50000, ld_acc=50000, acc=P + (1 << 30), K_out=P + (2 << 30), V=P + (3 << 30),
                  V_out=P + (4 << 30)) == L.zha_last_error_code() == zb.ZHA_ERR_CAPACITY
+
+
+@pytest.mark.parametrize("d,hq,hkv,dtype", [(128, 32, 4, "bf16"), (64, 6, 2, "bf16"), (64, 300, 2, "bf16"),
+                                            (128, 5, 5, "f32"), (64, 8, 1, "f32"), (64, 96, 3, "f32")])
+def test_workspaces_hold_what_calls_need(L, d, hq, hkv, dtype):
+    """A workspace of the size that one shape asks for passes the check of every call with no more of anything: the
+    call's own need, not the size function, decides.  A misaligned result, looked at after the workspace, keeps every
+    call from reaching the device."""
+    c = cfg(d=d, n_q_heads=hq, n_kv_heads=hkv, dtype=dtype)
+    ref = ctypes.byref(c)
+    rng = random.Random(5)
+
+    def log(lo, hi):
+        return min(hi, int(lo + math.exp(rng.uniform(0, math.log(hi - lo + 1))) - 1))
+
+    for _ in range(4000):
+        big = (log(1, 130), log(1, 40), log(0, 400000), rng.choice([0, log(1, 3000)]))
+        if rng.random() < 0.3:
+            small = big
+        else:
+            small = tuple(log(min(lo, b), b) if rng.random() < 0.7 else b for lo, b in zip((1, 1, 0, 0), big))
+        size = L.zha_prefix_scratch_bytes(ref, *big)
+        assert size > 0
+        B, m, n, own = small
+        args = dict(B=B, m=m, n=n, ld=n, ld_own=own, lse=P + 2)
+        assert prefix(L, c, nbytes=size, **args) == zb.ZHA_ERR_INVALID, (small, big, L.zha_last_error())
+        assert b"aligned" in L.zha_last_error()
+        assert prefix(L, c, nbytes=300, **args) == zb.ZHA_ERR_CAPACITY
+    for _ in range(4000):
+        big = (log(1, 5000), log(1, 400000))
+        small = big if rng.random() < 0.3 else (log(1, big[0]), log(1, big[1]))
+        size = L.zha_weights_scratch_bytes(ref, *big)
+        assert size > 0
+        m, n = small
+        args = dict(m=m, n=n, ld=n, ld_in=n, ld_out=n, causal=0, acc_out=P + 2)
+        assert weights(L, c, nbytes=size, **args) == zb.ZHA_ERR_INVALID, (small, big, L.zha_last_error())
+        assert b"aligned" in L.zha_last_error()

@@ -654,12 +654,12 @@ int zha_prefix_decode(const zha_config* cfg, const void* K, const void* V, int64
   if (n > 0 && (!K || !V)) return fail(ZHA_ERR_INVALID, "K and V go with n > 0");
   if (ld_own > 0 && (!K_own || !V_own || !own_len))
     return fail(ZHA_ERR_INVALID, "K_own, V_own and own_len go with ld_own > 0");
-  if (!aligned(K, 16) || !aligned(V, 16) || !aligned(K_own, 16) || !aligned(V_own, 16) || !aligned(Q, 16) ||
-      !aligned(O, 16) || !aligned(lse, 4) || !aligned(own_len, 4))
-    return fail(ZHA_ERR_INVALID, "K, V, K_own, V_own, Q and O must be 16-byte aligned, lse and own_len 4-byte");
   if (!aligned(scratch, 256)) return fail(ZHA_ERR_INVALID, "scratch must be 256-byte aligned");
   if (scratch_bytes < kScratchHead + rows_part_bytes(cfg, B, m, p))
     return fail(ZHA_ERR_CAPACITY, "scratch is smaller than zha_prefix_scratch_bytes");
+  if (!aligned(K, 16) || !aligned(V, 16) || !aligned(K_own, 16) || !aligned(V_own, 16) || !aligned(Q, 16) ||
+      !aligned(O, 16) || !aligned(lse, 4) || !aligned(own_len, 4))
+    return fail(ZHA_ERR_INVALID, "K, V, K_own, V_own, Q and O must be 16-byte aligned, lse and own_len 4-byte");
   RowsArgs a;
   fill_rows(cfg, p, B, m, scratch, &a);
   a.K = K;
@@ -726,6 +726,8 @@ int zha_dense_weights(const zha_config* cfg, const void* K, const void* V, int64
   if (causal != 0 && causal != 1) return fail(ZHA_ERR_INVALID, "causal must be 0 or 1");
   if (causal && m > n) return fail(ZHA_ERR_INVALID, "causal needs m <= n");
   if (ld_acc_out < n || (acc_in && ld_acc_in < n)) return fail(ZHA_ERR_INVALID, "the sums' row strides must be >= n");
+  if (!aligned(scratch, 256)) return fail(ZHA_ERR_INVALID, "scratch must be 256-byte aligned");
+  if (scratch_bytes < bytes) return fail(ZHA_ERR_CAPACITY, "scratch is smaller than zha_weights_scratch_bytes");
   if (!aligned(K, 16) || !aligned(V, 16) || !aligned(Q, 16) || !aligned(O, 16) || !aligned(acc_in, 4) ||
       !aligned(acc_out, 4))
     return fail(ZHA_ERR_INVALID, "K, V, Q and O must be 16-byte aligned, the sums 4-byte");
@@ -733,8 +735,6 @@ int zha_dense_weights(const zha_config* cfg, const void* K, const void* V, int64
   const uint64_t out_bytes = (uint64_t(cfg->n_kv_heads - 1) * ld_acc_out + n) * 4;
   if (acc_in && !(acc_in == acc_out && ld_acc_in == ld_acc_out) && overlap(acc_in, in_bytes, acc_out, out_bytes))
     return fail(ZHA_ERR_INVALID, "acc_in and acc_out overlap");
-  if (!aligned(scratch, 256)) return fail(ZHA_ERR_INVALID, "scratch must be 256-byte aligned");
-  if (scratch_bytes < bytes) return fail(ZHA_ERR_CAPACITY, "scratch is smaller than zha_weights_scratch_bytes");
   RowsArgs a;
   fill_rows(cfg, rp, 1, m, scratch, &a);
   a.K = K;
