@@ -122,3 +122,50 @@ def test_weights_by_their_own_size(dtype, d, m, n, outputs):
     assert float((got - want).norm() / want.norm()) <= tol and abs(float(got.sum()) - m * G) <= tol * m * G
     if outputs:
         assert math.sqrt(worst / norm) <= OUT[dtype, d]
+
+
+@pytest.mark.parametrize("dtype,d,hkv,n", [("bf16", 128, 3, 6000011), ("f32", 64, 2, 9000005)])
+def test_offsets_past_32_bits(dtype, d, hkv, n):
+    """Caches of more than 2^32 bytes (bf16: of more than 2^31 elements) per tensor: every head of each operator against
+    fp64, eviction's rows against the positions it returns, into other buffers and in place."""
+    G, keep, first, last = 2, 40000, 3, 500
+    K, V = (torch.empty(hkv, n, d, dtype=DT[dtype], device="cuda") for _ in range(2))
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for t in (K, V):
+        for h in range(hkv):
+            for i in range(0, n, 1 << 20):
+                part = t[h, i:i + (1 << 20)]
+                part.copy_(torch.randn(part.shape, generator=g, device="cuda"))
+    assert K.numel() * K.element_size() > 2 ** 32
+    cfg = cfg_of(dtype, d, hkv, G, n)
+    Q = rnd(3, 1, hkv * G, d, dtype=dtype, scale=2.0)
+    o, lse = z.prefix_decode(cfg, K, V, n, Q, want_lse=True)
+    ow, acc = z.DenseWeights(cfg, 1, n)(K, V, n, Q)
+    x = torch.empty(hkv, G, n, dtype=torch.float64, device="cuda")
+    for h in range(hkv):
+        for i in range(0, n, 1 << 20):
+            x[h, :, i:i + (1 << 20)] = Q[0, h * G:(h + 1) * G].double() @ K[h, i:i + (1 << 20)].double().T / math.sqrt(d)
+    w = torch.softmax(x, 2)
+    want = torch.zeros(hkv, G, d, dtype=torch.float64, device="cuda")
+    for h in range(hkv):
+        for i in range(0, n, 1 << 20):
+            want[h] += w[h, :, i:i + (1 << 20)] @ V[h, i:i + (1 << 20)].double()
+    tol = OUT[dtype, d]
+    for got in (o, ow):
+        err = (got[0].double().view(hkv, G, d) - want).norm(dim=2) / want.norm(dim=2)
+        assert float(err.max()) <= tol
+    assert float((lse[0].double().view(hkv, G) - torch.logsumexp(x, 2)).abs().max()) <= WEIGHT[dtype, d]
+    sums = w.sum(1)
+    assert float(((acc.double() - sums).abs() / sums).max()) <= WEIGHT[dtype, d]
+    del x, w, sums
+    ko, vo = (torch.empty(hkv, keep, d, dtype=DT[dtype], device="cuda") for _ in range(2))
+    idx, ao = z.cache_evict(cfg, K, V, n, acc, keep, first=first, last=last, K_out=ko, V_out=vo)
+    mid = torch.sort(acc[:, first:n - last], dim=1, descending=True, stable=True).indices[:, :keep - first - last] + first
+    ends = torch.cat([torch.arange(first, device="cuda"), torch.arange(n - last, n, device="cuda")]).expand(hkv, -1)
+    assert torch.equal(idx.long(), torch.sort(torch.cat([mid, ends], 1), 1).values)
+    for h in range(hkv):
+        at = idx[h].long()
+        assert torch.equal(ko[h], K[h][at]) and torch.equal(vo[h], V[h][at]) and torch.equal(ao[h], acc[h][at])
+    idx2, _ = z.cache_evict(cfg, K, V, n, acc, keep, first=first, last=last)
+    assert torch.equal(idx2, idx) and torch.equal(K[:, :keep], ko) and torch.equal(V[:, :keep], vo)
+    assert torch.equal(acc[:, :keep], ao) and not bool(acc[:, keep:].any())
