@@ -277,8 +277,8 @@ static cudaError_t launch_select(const EvictArgs& a, cudaStream_t st) {
 
 // ------------------------------------------------------------------ moving the rows
 // Separate outputs: a plain gather.  Each thread has four 16-byte pieces in flight; bound by HBM (each kept row read
-// and written once).  1M -> 512K tokens, 4 heads of 128 bf16: 128 threads and streaming stores 435 us with the
-// selection, 256 and plain stores 465, eight pieces 507, two 489.
+// and written once).  1M -> 512K tokens, 4 heads of 128 bf16: 443 us with the selection.  In the run that compared them
+// 128 threads and streaming stores took 435, 256 and plain stores 465, eight pieces 507, two 489.
 constexpr int kMoveThreads = 128;
 constexpr int kMoveUnroll = 4;
 
@@ -316,7 +316,10 @@ __global__ void __launch_bounds__(kMoveThreads) evict_gather_kernel(EvictArgs a)
 // earlier-listed row's place is written.  One CTA moves a 32-byte column slice of one head's K or V (or its sums):
 // rounds of kSlideRows rows, all of a round's loads before a barrier, its stores after it.  Writing rows [i, i +
 // kSlideRows) can only overwrite sources of rows before i + kSlideRows, which have all been read; slices share no
-// bytes, so CTAs need no order among themselves.
+// bytes, so CTAs need no order among themselves.  Bound by latency: a CTA has one round of loads in flight and few
+// CTAs share the work (4 heads of 128 bf16: 68, one head of 64 bf16: 9).  With the selection 256K -> 64K tokens take 156
+// us and 1M -> 512K 1,092 us for 4 heads of 128 bf16 (other buffers: 74 and 451), 256K -> 64K 140 us for one head of 64
+// (32).
 constexpr int kSlideThreads = 1024;
 constexpr int kSlideUnroll = 4;
 

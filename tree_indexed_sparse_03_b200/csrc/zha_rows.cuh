@@ -319,8 +319,13 @@ uint64_t weights_tc_floats();
 cudaError_t launch_weights_tc(const WeightsArgs& a, int d, cudaStream_t st);
 cudaError_t launch_weights(const WeightsArgs& a, int dtype, int d, cudaStream_t st);
 
-// Calls of up to this many rows per KV head keep their logits (4 bytes per row and key, mostly in L2) rather than
-// read K again (2 d bytes per key) and run its products again.
+// Calls of up to this many rows per KV head keep their logits (4 bytes per row and key) rather than read K again (2 d
+// bytes per key) and run its products again.  Both sides, with outputs, 4 KV heads, us (kept / again):
+//   bf16, 512K tokens   8 rows    16 rows   32 rows   64 rows      fp32     8 rows       16 rows      64 rows
+//     d = 64            237/327   264/325   291/311   439/332              382/547      884/1123     1056/1485
+//     d = 128           255/392   285/396   351/390   488/380              769/1607     1165/1836    2400/3538
+// (64K tokens, bf16, d = 64: 50/65, 53/66, 58/67, 91/68).  Above 16 rows the gain of bf16 shrinks while the workspace
+// grows with the rows, 128 bytes per key at 32; fp32 would gain on, for the same memory.
 constexpr int kLogitRows = 16;
 
 struct EvictArgs {

@@ -11,8 +11,8 @@
 // output is fp32: one part alone leaves 2^-9 of every weight, the two 2^-17.  That makes three products per tile
 // instead of two: 3 * 512 cycles at 128 x 128 x 128 against 1024 cycles of exponentials (16 per cycle and SM), so
 // with both streams in flight - one in its exponentials while the other's products run - the tensor pipe is the
-// limit for many rows, HBM for few.  Measured: 64 sequences behind 256K tokens (4 KV heads of 8, d = 128) 411 us in
-// short runs, 1.0e15 tensor operations a second with the third product counted, 480 us in long ones at the power
+// limit for many rows, HBM for few.  Measured: 64 sequences behind 256K tokens (4 KV heads of 8, d = 128) 415 us in
+// short runs, 1.0e15 tensor operations a second with the third product counted, 475 to 490 us in long ones at the power
 // limit; 5,250 cycles per tile of both streams of the 3,072 that its products take.  One sequence (8 rows a head)
 // 105 us for 537 MB of K and V, 5.1 TB/s. A segment of more than 128 rows gives each stream its own rows and both
 // the same tiles (each K and V tile is loaded once for 256 rows); a smaller one gives both streams the same rows and

@@ -473,7 +473,7 @@ class PrefixDecoder(_Attend):
     to own_max tokens (zha_prefix_decode), with a workspace of its own.
 
     Calls of one PrefixDecoder must be issued in order on one stream, and graphs captured with one must not replay at
-    the same time: they share its workspace.
+    the same time nor outlive it: they share its workspace.
     """
 
     def __init__(self, cfg: ZhaConfig, B: int, n_max: int, own_max: int = 0, m: int = 1, device="cuda"):
@@ -553,7 +553,8 @@ def prefix_decode(cfg: ZhaConfig, K, V, n: int, Q: torch.Tensor, K_own=None, V_o
 
 class DenseWeights(_Attend):
     """Dense attention of up to m query tokens over up to n_max tokens that adds up every token's attention weight
-    (zha_dense_weights), with a workspace of its own (as for PrefixDecoder)."""
+    (zha_dense_weights), with a workspace of its own (as for PrefixDecoder).  Sums in place are left as they were by a
+    call whose status() is ZHA_ERR_TIMEOUT, and by later ones until it has been asked for."""
 
     def __init__(self, cfg: ZhaConfig, m: int, n_max: int, device="cuda"):
         super().__init__(cfg, int(lib().zha_weights_scratch_bytes(ctypes.byref(cfg), m, n_max)), device)
