@@ -321,7 +321,7 @@ ZHA_API int zha_prefix_decode(const zha_config* cfg, const void* K, const void* 
  * calls give equal bits.  When a wait of the call runs out (see zha_scratch_status) its outputs
  * are undefined, but sums in place are as they were, also after later calls until the
  * status has been looked at.  The workspace of calls with few rows (m * Hq / Hkv <= 16) holds
- * their logits, 4 bytes per query row and token.
+ * their logits, 4 bytes per query row and token, that of others (bf16) a second set of sums.
  * Scratch, stream and graphs as for zha_prefix_decode (n >= 1; m * Hq < 2^24).
  */
 ZHA_API size_t zha_weights_scratch_bytes(const zha_config* cfg, int32_t m, int64_t n);

@@ -24,11 +24,11 @@ def rnd(seed, *shape, scale=1.0):
 
 
 def busy():
-    """A stream that is busy for about a tenth of a second."""
+    """A stream that is busy for about half a second."""
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(s):
-        torch.cuda._sleep(200_000_000)
+        torch.cuda._sleep(1_000_000_000)
     return s
 
 

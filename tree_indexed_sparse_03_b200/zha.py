@@ -465,6 +465,7 @@ class _Attend:
         return shape
 
     def status(self, stream=None) -> None:
+        """Waits for `stream` (the one the calls ran on) and raises if a wait of theirs ran out; looking clears it."""
         _check(lib().zha_scratch_status(self.scratch.data_ptr(), _stream(stream)))
 
 
